@@ -80,10 +80,12 @@ def _elf_section(path: str, name: str) -> bytes:
 
 
 def device_code_hash() -> str:
-    """sha256 of the machine code libzero.so carries for the GPU: for every
-    amdgcn code object in its .hip_fatbin section (clang offload bundles), the
-    .text section (the instructions) and the .rodata section (the kernel
-    descriptors: resources, LDS, entry offsets).  Symbol and string tables
+    """sha256 of the machine code that libzero.so carries for the kernels the
+    counter summaries cover: for every amdgcn code object in its .hip_fatbin
+    section (clang offload bundles) that holds the owner update, the .text
+    section (the instructions) and the .rodata section (the kernel
+    descriptors: resources, LDS, entry offsets).  Code objects of other
+    source files (the Muon step's) are left out: no workload here runs them.  Symbol and string tables
     are left out: they carry compilation-unit IDs derived from the source
     path, so the same sources built in another directory keep the hash, and
     so do edits that leave the machine code alone (comments, host code)."""
@@ -101,6 +103,8 @@ def device_code_hash() -> str:
             q += 24 + tlen
             if b"amdgcn" in triple:
                 co = fat[pos + off:pos + off + size]
+                if b"adam_vec_kernel" not in co:
+                    continue
                 h.update(triple)
                 for sec in (".text", ".rodata"):
                     h.update(_elf_section_bytes(co, sec, triple.decode(errors="replace")))

@@ -52,6 +52,13 @@ extern "C" {
 /* doubles in the library's own partial-sum array of zero_grad_norm_sq_no_alloc (128 KiB per GPU) */
 #define ZERO_NORM_SCRATCH_DOUBLES (ZERO_MAX_RANKS * ZERO_NORM_BLOCKS)
 
+/* limits of zero_newton_schulz */
+#define ZERO_NS_MAX_STEPS 16
+#define ZERO_NS_MAX_MATS 65535
+#define ZERO_NS_MAX_SIDE 262144
+#define ZERO_NS_MAX_SIGMA 2   /* largest singular value a step may give */
+#define ZERO_NS_MAX_GAIN 16   /* largest |p(s)/s| of a step */
+
 typedef enum zero_status {
   ZERO_OK = 0,
   ZERO_ERR_ARG = -1,    /* null pointer, count out of range, overlapping buffers, bad hyper-parameter */
@@ -305,6 +312,112 @@ int zero_adam_scalars_fetch(const zero_adam_scalars* ring_host, int ring_len, ui
  * n_shards outside [1, 16], shard_bytes < 0, overlap), ZERO_ERR_HIP. */
 int zero_all_gather_layer(const void* const* shards, int n_shards, int64_t shard_bytes,
                           void* full_view, void* stream);
+
+/* ---------------------------------------------------------------- Muon step
+ *
+ * The optimizer whose only state is the first moment ([blog] 每个参数 16 字节
+ * counts its 12 bytes per parameter: BF16 weight and gradient, FP32 master and
+ * momentum): the momentum of every weight matrix is orthogonalised by
+ * Newton-Schulz products before it is applied.  Its step over sharded units:
+ *   1. zero_reduce_scatter_muon (or zero_reduce_scatter, a gradient norm and
+ *      zero_muon_momentum): every owner's momentum shard and the BF16
+ *      directions of its slice;
+ *   2. zero_all_gather_layer of the directions: the orthogonalisation needs
+ *      whole matrices;
+ *   3. zero_newton_schulz on each stack of equal matrices in the view;
+ *   4. zero_muon_shard_step on each owner's slice of the result;
+ *   5. zero_all_gather_layer of the working weights, as after any update. */
+typedef struct zero_muon_hparams {
+  float lr;            /* learning rate */
+  float momentum;      /* b, in [0, 1) */
+  float weight_decay;  /* decoupled, scaled by lr */
+  int32_t nesterov;    /* 1: look-ahead direction; 0: the momentum itself */
+} zero_muon_hparams;
+
+/* zero_newton_schulz's input types */
+enum { ZERO_BF16 = 0, ZERO_FP32 = 1 };
+
+/* Momentum step over n elements of an owner's shard.
+ *   momentum       FP32[n] device, updated in place.
+ *   direction_out  BF16[n] device, written.
+ *   grad           FP32[n] device, read (the reduced gradient shard).
+ *   grad_scale     NULL, or a device float (4-byte aligned, outside the written
+ *                  buffers): g is first multiplied by it, as in
+ *                  zero_adam_shard_step_scaled.
+ * Per element, with b = hp->momentum and 1-b a binary32 subtraction:
+ *   m' = b*m + (1-b)*g;  u = nesterov ? (1-b)*g + b*m' : m';
+ *   direction_out = round_to_nearest_even_bf16(u).
+ * The averaged form; a form that sums (m' = b*m + g) differs by the factor 1-b
+ * in all of m and u, which the orthogonalisation removes.
+ * Errors: ZERO_ERR_ARG (NULL, n < 0, overlap, momentum outside [0, 1),
+ * nesterov not 0 or 1), ZERO_ERR_ALIGN, ZERO_ERR_SIZE, ZERO_ERR_HIP. */
+int zero_muon_momentum(float* momentum, uint16_t* direction_out, const float* grad,
+                       const float* grad_scale, int64_t n, const zero_muon_hparams* hp, void* stream);
+
+/* Reduce-scatter and momentum step in one pass: for every owner k exactly
+ * zero_reduce_scatter's shard k (grad_acc[k] + red when grad_acc is given),
+ * not stored, and zero_muon_momentum's step with it: bit-identical to the two
+ * calls, with 8 fewer bytes of HBM traffic per parameter.
+ *   rank_grads, rank_weights, n_ranks, numel, n_shards: as zero_reduce_scatter.
+ *   momentum       host array of n_shards device pointers, FP32, numel/n_shards each.
+ *   direction_out  host array of n_shards device pointers, BF16.
+ *   grad_acc       NULL, or a host array of n_shards device pointers, FP32, read.
+ * Errors: as zero_reduce_scatter and zero_muon_momentum; outputs must be
+ * disjoint from every other buffer. */
+int zero_reduce_scatter_muon(const uint16_t* const* rank_grads, const float* rank_weights, int n_ranks,
+                             int64_t numel, int n_shards, float* const* momentum,
+                             uint16_t* const* direction_out, const float* const* grad_acc,
+                             const zero_muon_hparams* hp, void* stream);
+
+/* Bytes of device workspace zero_newton_schulz needs for n_mats matrices of
+ * rows x cols.  Errors: ZERO_ERR_ARG (NULL, a negative size), ZERO_ERR_SIZE. */
+int zero_newton_schulz_workspace(int64_t n_mats, int64_t rows, int64_t cols, int64_t* bytes_out);
+
+/* Orthogonalise a stack of matrices by Newton-Schulz products.  For each
+ * matrix G (rows x cols):
+ *   X = G / ||G||_F  (Frobenius norm; a zero matrix stays zero)
+ *   for each step's (a, b, c):  A = X X^T;  X = a X + (b A + c A A) X
+ *   out = round_to_nearest_even_bf16(scale * X)
+ * that is, every singular value s of X becomes a s + b s^3 + c s^5 per step
+ * and the singular vectors stay.  The result does not depend on the input's
+ * scale.  A matrix holding a NaN or an infinity gives NaN throughout.
+ *   in            device, BF16 or FP32 (in_dtype), element (i, j) of matrix q
+ *                 at in[q*in_mat_stride + i*in_row_stride + j].
+ *   out           device, BF16, laid out likewise with its own strides.
+ *   coefs         host array of 3*steps floats, steps in [1, 16].  They must
+ *                 keep the singular values (from [0, 1] on) within
+ *                 ZERO_NS_MAX_SIGMA and a step's gain |p(s)/s| within
+ *                 ZERO_NS_MAX_GAIN.
+ *   scale         finite factor of the result.
+ *   workspace     device, 256-byte aligned, workspace_bytes >=
+ *                 zero_newton_schulz_workspace's answer; nothing in it carries
+ *                 over between calls.
+ * Arithmetic: the norm in FP64 (fixed order); the products on the matrix
+ * cores with FP16 operands scaled by powers of two and FP32 accumulation, two
+ * to three decimal digits more exact than the BF16 result needs.  Results
+ * are the same bits on every call with the same inputs.
+ * Errors: ZERO_ERR_ARG (NULL, negative sizes, in_dtype, steps, coefficients
+ * that are not finite or break the bounds, a scale that is not finite,
+ * overlapping buffers), ZERO_ERR_ALIGN, ZERO_ERR_SIZE (strides below the
+ * matrix's extent, sides above ZERO_NS_MAX_SIDE, more than ZERO_NS_MAX_MATS
+ * matrices, a small workspace), ZERO_ERR_HIP. */
+int zero_newton_schulz(const void* in, int in_dtype, int64_t in_row_stride, int64_t in_mat_stride,
+                       uint16_t* out, int64_t out_row_stride, int64_t out_mat_stride, int64_t n_mats,
+                       int64_t rows, int64_t cols, const float* coefs, int steps, float scale,
+                       void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Owner update with the orthogonalised directions, n elements of its shard:
+ *   u = o;  if wd != 0: u = o + wd*p;  p' = p - lr*u;
+ *   bf16_out = round_to_nearest_even_bf16(p').
+ *   master     FP32[n] device, updated in place.
+ *   bf16_out   BF16[n] device, written: the new working weights.
+ *   update     BF16[n] device, read: the owner's slice of zero_newton_schulz's results.
+ *   lr_dev     NULL, or a device float (4-byte aligned, outside the written
+ *              buffers) read when the kernel runs, in place of hp->lr: a
+ *              captured graph then replays with each step's learning rate.
+ * Errors: as zero_muon_momentum. */
+int zero_muon_shard_step(float* master, uint16_t* bf16_out, const uint16_t* update, int64_t n,
+                         const zero_muon_hparams* hp, const float* lr_dev, void* stream);
 
 /* ---------------------------------------------------------------- host-offloaded gradient shard */
 

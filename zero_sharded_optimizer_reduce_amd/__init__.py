@@ -8,6 +8,7 @@ that sequence its calls.
 from ._lib import ZERO_OFFLOAD_ADAM, ZERO_OFFLOAD_REDUCE, ZERO_OFFLOAD_REDUCE_ADAM, ZeroError, load  # noqa: F401
 from .api import (  # noqa: F401
     ADAM_SCALARS_FLOATS,
+    NS_COEFS,
     ZeroOffload,
     adam_scalars_tensor,
     zero_adam_scalars_compute,
@@ -19,6 +20,10 @@ from .api import (  # noqa: F401
     zero_grad_norm_sq,
     zero_grad_norm_sq_no_alloc,
     zero_last_path_vectorized,
+    zero_muon_momentum,
+    zero_muon_shard_step,
+    zero_newton_schulz,
+    zero_newton_schulz_workspace,
     zero_offload_create,
     zero_offload_destroy,
     zero_offload_stream,
@@ -28,5 +33,6 @@ from .api import (  # noqa: F401
     zero_reduce_scatter_adam,
     zero_reduce_scatter_adam_dev,
     zero_reduce_scatter_f32,
+    zero_reduce_scatter_muon,
     zero_shard_layout,
 )

@@ -15,6 +15,9 @@ ZERO_MAX_RANKS = 16
 ZERO_NORM_BLOCKS = 1024
 ZERO_OFFLOAD_MAX_CHUNKS = 65536
 ZERO_OFFLOAD_REDUCE, ZERO_OFFLOAD_ADAM, ZERO_OFFLOAD_REDUCE_ADAM = 0, 1, 2
+ZERO_NS_MAX_STEPS, ZERO_NS_MAX_MATS, ZERO_NS_MAX_SIDE = 16, 65535, 262144
+ZERO_NS_MAX_SIGMA, ZERO_NS_MAX_GAIN = 2, 16
+ZERO_BF16, ZERO_FP32 = 0, 1
 
 
 class AdamHparams(C.Structure):
@@ -26,6 +29,10 @@ class AdamScalars(C.Structure):
     _fields_ = [(n, C.c_float) for n in (
         "lr", "beta1", "beta2", "one_minus_beta1", "one_minus_beta2",
         "bias_correction1", "bias_correction2", "eps", "weight_decay")]
+
+
+class MuonHparams(C.Structure):
+    _fields_ = [("lr", C.c_float), ("momentum", C.c_float), ("weight_decay", C.c_float), ("nesterov", C.c_int32)]
 
 
 P = C.c_void_p
@@ -51,6 +58,12 @@ SIGNATURES = {
     "zero_reduce_scatter_adam_dev": (C.c_int, [PP, FP, C.c_int, I64, C.c_int, PP, PP, PP, PP, PP, PP, P, P]),
     "zero_adam_scalars_fetch": (C.c_int, [P, C.c_int, P, P, P]),
     "zero_all_gather_layer": (C.c_int, [PP, C.c_int, I64, P, P]),
+    "zero_muon_momentum": (C.c_int, [P, P, P, P, I64, C.POINTER(MuonHparams), P]),
+    "zero_reduce_scatter_muon": (C.c_int, [PP, FP, C.c_int, I64, C.c_int, PP, PP, PP, C.POINTER(MuonHparams), P]),
+    "zero_newton_schulz_workspace": (C.c_int, [I64, I64, I64, I64P]),
+    "zero_newton_schulz": (C.c_int, [P, C.c_int, I64, I64, P, I64, I64, I64, I64, I64, FP, C.c_int, C.c_float, P, I64,
+                                     P]),
+    "zero_muon_shard_step": (C.c_int, [P, P, P, I64, C.POINTER(MuonHparams), P, P]),
     "zero_offload_create": (C.c_int, [C.c_int, I64, I64, P, PP, PP, C.POINTER(C.c_void_p)]),
     "zero_offload_stream": (C.c_int, [P, C.c_int, I64, C.c_int, FP, P, P, P, P,
                                       C.POINTER(AdamHparams), P]),

@@ -14,7 +14,7 @@ import numpy as np
 import torch
 
 from . import _lib
-from ._lib import AdamHparams, check, load
+from ._lib import AdamHparams, MuonHparams, check, load
 
 _BF16_LIKE = (torch.bfloat16, torch.int16, torch.uint16)
 
@@ -322,6 +322,135 @@ def zero_all_gather_layer(shards: Sequence[torch.Tensor], full_view: torch.Tenso
     if full_view.numel() * full_view.element_size() != n * nbytes:
         raise ValueError("zero_all_gather_layer: full_view must hold exactly n_shards*shard_bytes bytes")
     check(load().zero_all_gather_layer(_ptrs(sp), n, nbytes, vp, _stream(stream)), "zero_all_gather_layer")
+
+
+# ------------------------------------------------------------ Muon step
+# The quintic step's coefficients that raise small singular values fastest
+# while keeping the others near 1, five times.
+NS_COEFS = ((3.4445, -4.7750, 2.0315),) * 5
+
+
+def muon_hparams(hp) -> MuonHparams:
+    """lr, momentum, weight_decay (0) and nesterov (True) as the C struct."""
+    if isinstance(hp, MuonHparams):
+        return hp
+    return MuonHparams(float(hp["lr"]), float(hp["momentum"]), float(hp.get("weight_decay", 0.0)),
+                       int(bool(hp.get("nesterov", True))))
+
+
+def _one_float(t: Optional[torch.Tensor], what: str):
+    if t is None:
+        return None
+    ptr = _dev(t, what, (torch.float32,))
+    if t.numel() < 1:
+        raise ValueError(f"{what}: needs one element")
+    return ptr
+
+
+def zero_muon_momentum(momentum: torch.Tensor, direction_out: torch.Tensor, grad: torch.Tensor, hp,
+                       grad_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Momentum step of an owner's shard: momentum (FP32) in place, direction_out
+    (BF16) written; grad_scale: a one-element FP32 device tensor that multiplies
+    the gradient (the clip coefficient)."""
+    n = momentum.numel()
+    ptrs = [_dev(momentum, "momentum", (torch.float32,)), _dev(direction_out, "direction_out", _BF16_LIKE),
+            _dev(grad, "grad", (torch.float32,))]
+    if any(t.numel() != n for t in (direction_out, grad)):
+        raise ValueError("zero_muon_momentum: all buffers must have the same numel")
+    h = muon_hparams(hp)
+    check(load().zero_muon_momentum(*ptrs, _one_float(grad_scale, "grad_scale"), n, C.byref(h), _stream(stream)),
+          "zero_muon_momentum")
+
+
+def zero_reduce_scatter_muon(rank_grads: Sequence[torch.Tensor], rank_weights, momentum: Sequence[torch.Tensor],
+                             direction_out: Sequence[torch.Tensor], hp, grad_acc=None, stream=None) -> None:
+    """Fused reduce-scatter + momentum step: for each owner k, the reduced shard
+    k (plus grad_acc[k] when given) moves momentum[k] and writes
+    direction_out[k].  Bit-identical to zero_reduce_scatter (accumulate mode
+    with grad_acc) followed by zero_muon_momentum on every owner."""
+    name = "zero_reduce_scatter_muon"
+    n_ranks, n_shards = len(rank_grads), len(momentum)
+    if n_ranks < 1 or n_shards < 1:
+        raise ValueError(f"{name}: need at least one rank and one owner")
+    numel = rank_grads[0].numel()
+    gp = [_dev(g, f"rank_grads[{r}]", _BF16_LIKE) for r, g in enumerate(rank_grads)]
+    if any(g.numel() != numel for g in rank_grads):
+        raise ValueError(f"{name}: rank contributions differ in size")
+    if numel % n_shards:
+        raise ValueError(f"{name}: numel not divisible by the number of owners")
+    tables = []
+    for tname, ts, dt in (("momentum", momentum, (torch.float32,)), ("direction_out", direction_out, _BF16_LIKE),
+                          ("grad_acc", grad_acc, (torch.float32,))):
+        if ts is None:
+            tables.append(None)
+            continue
+        if len(ts) != n_shards or any(t.numel() != numel // n_shards for t in ts):
+            raise ValueError(f"{name}: {tname} needs {n_shards} tensors of {numel // n_shards} elements")
+        tables.append(_ptrs([_dev(t, f"{tname}[{k}]", dt) for k, t in enumerate(ts)]))
+    w = np.ascontiguousarray(np.asarray(rank_weights, dtype=np.float32))
+    if w.size != n_ranks:
+        raise ValueError(f"{name}: one weight per rank")
+    h = muon_hparams(hp)
+    check(load().zero_reduce_scatter_muon(_ptrs(gp), w.ctypes.data_as(_lib.FP), n_ranks, numel, n_shards, *tables,
+                                          C.byref(h), _stream(stream)), name)
+
+
+def _stack(t: torch.Tensor, what: str, dtypes):
+    """(pointer, matrices, rows, cols, row stride, matrix stride) of a 2-D or 3-D
+    tensor whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dim() not in (2, 3):
+        raise TypeError(f"{what}: expected a 2-D or 3-D torch.Tensor")
+    v = t if t.dim() == 3 else t.unsqueeze(0)
+    if v.size(2) > 1 and v.stride(2) != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    row = v.stride(1) if v.size(1) > 1 else v.size(2)
+    mat = v.stride(0) if v.size(0) > 1 else 0
+    # the checks that _dev makes of a contiguous tensor, on the first element's view
+    ptr = _dev(v[:1, :1, :1] if v.numel() else v.contiguous(), what, dtypes)
+    return ptr, v.size(0), v.size(1), v.size(2), row, mat
+
+
+def zero_newton_schulz_workspace(g: torch.Tensor) -> torch.Tensor:
+    """A device workspace for zero_newton_schulz on tensors of g's shape (2-D, or
+    3-D: a stack of matrices)."""
+    shape = tuple(g.shape) if g.dim() == 3 else (1, *g.shape)
+    if len(shape) != 3:
+        raise ValueError("zero_newton_schulz_workspace: expected a 2-D or 3-D tensor")
+    n = C.c_int64()
+    check(load().zero_newton_schulz_workspace(*shape, C.byref(n)), "zero_newton_schulz_workspace")
+    return torch.empty(n.value, dtype=torch.uint8, device=g.device)
+
+
+def zero_newton_schulz(g: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor, coefs=NS_COEFS,
+                       scale: float = 1.0, stream=None) -> None:
+    """out (BF16) = scale * the Newton-Schulz orthogonalisation of each matrix of
+    g (BF16 or FP32; [rows, cols] or [matrices, rows, cols], rows contiguous,
+    other strides free).  coefs: one (a, b, c) per step."""
+    ip, mats, rows, cols, irow, imat = _stack(g, "g", (torch.bfloat16, torch.float32))
+    op, omats, orows, ocols, orow, omat = _stack(out, "out", (torch.bfloat16,))
+    if (mats, rows, cols) != (omats, orows, ocols):
+        raise ValueError("zero_newton_schulz: out must have g's shape")
+    c = np.ascontiguousarray(np.asarray(coefs, dtype=np.float32))
+    if c.ndim != 2 or c.shape[1] != 3:
+        raise ValueError("zero_newton_schulz: coefs needs one (a, b, c) per step")
+    wp = _dev(workspace, "workspace", (torch.uint8,))
+    check(load().zero_newton_schulz(ip, _lib.ZERO_FP32 if g.dtype == torch.float32 else _lib.ZERO_BF16, irow, imat,
+                                    op, orow, omat, mats, rows, cols, c.ctypes.data_as(_lib.FP), c.shape[0],
+                                    float(scale), wp, workspace.numel(), _stream(stream)), "zero_newton_schulz")
+
+
+def zero_muon_shard_step(master: torch.Tensor, bf16_out: torch.Tensor, update: torch.Tensor, hp,
+                         lr_dev: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Owner update: master (FP32) -= lr * (update + wd * master), bf16_out
+    written; lr_dev: a one-element FP32 device tensor read in place of hp's lr."""
+    n = master.numel()
+    ptrs = [_dev(master, "master", (torch.float32,)), _dev(bf16_out, "bf16_out", _BF16_LIKE),
+            _dev(update, "update", _BF16_LIKE)]
+    if any(t.numel() != n for t in (bf16_out, update)):
+        raise ValueError("zero_muon_shard_step: all buffers must have the same numel")
+    h = muon_hparams(hp)
+    check(load().zero_muon_shard_step(*ptrs, n, C.byref(h), _one_float(lr_dev, "lr_dev"), _stream(stream)),
+          "zero_muon_shard_step")
 
 
 def zero_last_path_vectorized() -> int:

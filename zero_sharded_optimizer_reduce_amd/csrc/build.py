@@ -21,7 +21,7 @@ PKG = os.path.dirname(HERE)
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libzero.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
-SOURCES = ["kernels.hip", "zero_api.cpp", "offload.cpp", "validate.cpp"]
+SOURCES = ["muon.hip", "newton_schulz.hip", "kernels.hip", "zero_api.cpp", "offload.cpp", "validate.cpp"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -65,6 +65,55 @@ struct FusedParams {
   const zero_adam_scalars* sdev;  // device copy of the scalars, or NULL
 };
 
+// The scalars of a Muon step: one_minus_momentum = 1 - momentum (a binary32
+// subtraction).
+struct MuonScalars {
+  float momentum, one_minus_momentum;
+  int nesterov;
+};
+
+struct MomentumParams {
+  float* m;
+  uint16_t* u;          // BF16 direction out
+  const float* g;
+  const float* gscale;  // device scalar multiplying g, or NULL
+  int64_t n;
+  MuonScalars s;
+};
+
+// One owner's slice: g[r] already points at it.
+struct ReduceMomentumParams {
+  const uint16_t* g[ZERO_MAX_RANKS];
+  float w[ZERO_MAX_RANKS];
+  float* m;
+  uint16_t* u;
+  const float* gacc;    // accumulator added to the reduction, or NULL
+  int64_t n;
+  int n_ranks;
+  MuonScalars s;
+};
+
+struct MuonUpdateParams {
+  float* p;
+  uint16_t* b;
+  const uint16_t* o;    // BF16 update directions
+  const float* lr_dev;  // device learning rate, or NULL: lr
+  int64_t n;
+  float lr, wd;
+};
+
+// One Newton-Schulz call, checked; see newton_schulz.hip.
+struct NsParams {
+  const void* in;
+  uint16_t* out;
+  void* workspace;
+  const float* coefs;   // host, 3*steps
+  int64_t in_row, in_mat, out_row, out_mat;  // strides in elements
+  int64_t mats, rows, cols;
+  int steps, in_f32;
+  float scale;
+};
+
 struct GatherParams {
   const void* src[ZERO_MAX_RANKS];
   void* dst;
@@ -89,6 +138,16 @@ hipError_t launch_gather(const GatherParams& p, int n_shards, int path, hipStrea
 // Two passes: per-(block, shard) partial sums of squares, then one block
 // folds them in index order and derives the clip coefficient.
 hipError_t launch_norm(NormParams& p, bool vec, hipStream_t stream);
+
+// The Muon step's streaming kernels.  vec: FP32 pointers 16-byte and the BF16
+// output 8-byte aligned; BF16 inputs may have any alignment and n any length.
+hipError_t launch_momentum(const MomentumParams& p, bool vec, hipStream_t stream);
+hipError_t launch_reduce_momentum(const ReduceMomentumParams& p, bool vec, hipStream_t stream);
+hipError_t launch_muon_update(const MuonUpdateParams& p, bool vec, hipStream_t stream);
+
+// Newton-Schulz orthogonalisation: the workspace it needs and its launches.
+int64_t ns_workspace_bytes(int64_t mats, int64_t rows, int64_t cols);
+hipError_t launch_newton_schulz(const NsParams& p, hipStream_t stream);
 
 // Device address of the current device's partial-sum array for the norm
 // (kNormScratchDoubles doubles, 256-byte aligned).  Looked up once per device

@@ -405,4 +405,229 @@ int shard_layout(const int64_t* numels, int n_tensors, int n_shards, int64_t* ps
   return ZERO_OK;
 }
 
+int check_muon_hparams(const zero_muon_hparams* hp, Err& e) {
+  if (!hp) return set_err(e, ZERO_ERR_ARG, "muon: NULL hyper-parameters");
+  if (!(hp->momentum >= 0.0f && hp->momentum < 1.0f))
+    return set_err(e, ZERO_ERR_ARG, "muon: momentum must lie in [0, 1)");
+  if (hp->nesterov != 0 && hp->nesterov != 1)
+    return set_err(e, ZERO_ERR_ARG, "muon: nesterov must be 0 or 1");
+  return ZERO_OK;
+}
+
+// An optional device float: 4-byte aligned and outside the written ranges
+// (every workgroup reads it while others write).
+static int check_device_float(const float* p, const char* name, const Range* outs, int n_outs, Err& e) {
+  if (!p) return ZERO_OK;
+  if (reinterpret_cast<uintptr_t>(p) & 3u) return set_err(e, ZERO_ERR_ALIGN, "muon: %s not 4-byte aligned", name);
+  for (int i = 0; i < n_outs; ++i)
+    if (overlaps(range_of(p, 4), outs[i]))
+      return set_err(e, ZERO_ERR_ARG, "muon: %s overlaps a buffer the call writes", name);
+  return ZERO_OK;
+}
+
+int check_muon_momentum(const float* momentum, const uint16_t* direction_out, const float* grad,
+                        const float* grad_scale, int64_t n, const zero_muon_hparams* hp, Err& e) {
+  int st = check_muon_hparams(hp, e);
+  if (st) return st;
+  if (n < 0) return set_err(e, ZERO_ERR_ARG, "muon: n=%lld < 0", (long long)n);
+  if (n == 0) return ZERO_OK;  // touches no buffer; NULL pointers allowed
+  if (!momentum || !direction_out || !grad) return set_err(e, ZERO_ERR_ARG, "muon: NULL buffer");
+  if (mul_overflows(n, 4)) return set_err(e, ZERO_ERR_SIZE, "muon: n too large");
+  if ((reinterpret_cast<uintptr_t>(momentum) | reinterpret_cast<uintptr_t>(grad)) & 3u)
+    return set_err(e, ZERO_ERR_ALIGN, "muon: FP32 buffer not 4-byte aligned");
+  if (reinterpret_cast<uintptr_t>(direction_out) & 1u)
+    return set_err(e, ZERO_ERR_ALIGN, "muon: direction_out not 2-byte aligned");
+  const Range outs[2] = {range_of(momentum, n * 4), range_of(direction_out, n * 2)};
+  const Range in = range_of(grad, n * 4);
+  if (overlaps(outs[0], outs[1]) || overlaps(outs[0], in) || overlaps(outs[1], in))
+    return set_err(e, ZERO_ERR_ARG, "muon: momentum, direction and gradient overlap");
+  return check_device_float(grad_scale, "grad_scale", outs, 2, e);
+}
+
+int check_reduce_scatter_muon(const uint16_t* const* rank_grads, const float* rank_weights, int n_ranks,
+                              int64_t numel, int n_shards, float* const* momentum,
+                              uint16_t* const* direction_out, const float* const* grad_acc,
+                              const zero_muon_hparams* hp, Err& e) {
+  int st = check_muon_hparams(hp, e);
+  if (st) return st;
+  if (!rank_grads || !rank_weights || !momentum || !direction_out)
+    return set_err(e, ZERO_ERR_ARG, "reduce_scatter_muon: NULL pointer table or weights");
+  if (n_ranks < 1 || n_ranks > ZERO_MAX_RANKS)
+    return set_err(e, ZERO_ERR_ARG, "reduce_scatter_muon: n_ranks=%d outside [1,%d]", n_ranks, ZERO_MAX_RANKS);
+  if (n_shards < 1 || n_shards > ZERO_MAX_RANKS)
+    return set_err(e, ZERO_ERR_ARG, "reduce_scatter_muon: n_shards=%d outside [1,%d]", n_shards, ZERO_MAX_RANKS);
+  if (numel < 0) return set_err(e, ZERO_ERR_ARG, "reduce_scatter_muon: numel < 0");
+  if (numel % n_shards != 0)
+    return set_err(e, ZERO_ERR_SIZE, "reduce_scatter_muon: numel=%lld not divisible by n_shards=%d",
+                   (long long)numel, n_shards);
+  if (mul_overflows(numel, 4)) return set_err(e, ZERO_ERR_SIZE, "reduce_scatter_muon: numel too large");
+  if (numel == 0) return ZERO_OK;
+  const int64_t shard = numel / n_shards;
+  Range outs[ZERO_MAX_RANKS * 2], ins[ZERO_MAX_RANKS * 2];
+  int no = 0, ni = 0;
+  for (int r = 0; r < n_ranks; ++r) {
+    if (!rank_grads[r]) return set_err(e, ZERO_ERR_ARG, "reduce_scatter_muon: rank_grads[%d] is NULL", r);
+    if (reinterpret_cast<uintptr_t>(rank_grads[r]) & 1u)
+      return set_err(e, ZERO_ERR_ALIGN, "reduce_scatter_muon: rank_grads[%d] not 2-byte aligned", r);
+    ins[ni++] = range_of(rank_grads[r], numel * 2);
+  }
+  for (int k = 0; k < n_shards; ++k) {
+    if (!momentum[k] || !direction_out[k])
+      return set_err(e, ZERO_ERR_ARG, "reduce_scatter_muon: NULL momentum or direction of owner %d", k);
+    if (reinterpret_cast<uintptr_t>(momentum[k]) & 3u)
+      return set_err(e, ZERO_ERR_ALIGN, "reduce_scatter_muon: momentum[%d] not 4-byte aligned", k);
+    if (reinterpret_cast<uintptr_t>(direction_out[k]) & 1u)
+      return set_err(e, ZERO_ERR_ALIGN, "reduce_scatter_muon: direction_out[%d] not 2-byte aligned", k);
+    outs[no++] = range_of(momentum[k], shard * 4);
+    outs[no++] = range_of(direction_out[k], shard * 2);
+    if (grad_acc) {
+      if (!grad_acc[k]) return set_err(e, ZERO_ERR_ARG, "reduce_scatter_muon: grad_acc[%d] is NULL", k);
+      if (reinterpret_cast<uintptr_t>(grad_acc[k]) & 3u)
+        return set_err(e, ZERO_ERR_ALIGN, "reduce_scatter_muon: grad_acc[%d] not 4-byte aligned", k);
+      ins[ni++] = range_of(grad_acc[k], shard * 4);
+    }
+  }
+  for (int i = 0; i < no; ++i) {
+    for (int j = i + 1; j < no; ++j)
+      if (overlaps(outs[i], outs[j]))
+        return set_err(e, ZERO_ERR_ARG, "reduce_scatter_muon: two output buffers overlap");
+    for (int j = 0; j < ni; ++j)
+      if (overlaps(outs[i], ins[j]))
+        return set_err(e, ZERO_ERR_ARG, "reduce_scatter_muon: an output overlaps an input");
+  }
+  return ZERO_OK;
+}
+
+int check_muon_shard(const float* master, const uint16_t* bf16_out, const uint16_t* update,
+                     const float* lr_dev, int64_t n, const zero_muon_hparams* hp, Err& e) {
+  int st = check_muon_hparams(hp, e);
+  if (st) return st;
+  if (n < 0) return set_err(e, ZERO_ERR_ARG, "muon: n=%lld < 0", (long long)n);
+  if (n == 0) return ZERO_OK;  // touches no buffer; NULL pointers allowed
+  if (!master || !bf16_out || !update) return set_err(e, ZERO_ERR_ARG, "muon: NULL buffer");
+  if (mul_overflows(n, 4)) return set_err(e, ZERO_ERR_SIZE, "muon: n too large");
+  if (reinterpret_cast<uintptr_t>(master) & 3u)
+    return set_err(e, ZERO_ERR_ALIGN, "muon: master not 4-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(bf16_out) | reinterpret_cast<uintptr_t>(update)) & 1u)
+    return set_err(e, ZERO_ERR_ALIGN, "muon: BF16 buffer not 2-byte aligned");
+  const Range outs[2] = {range_of(master, n * 4), range_of(bf16_out, n * 2)};
+  const Range in = range_of(update, n * 2);
+  if (overlaps(outs[0], outs[1]) || overlaps(outs[0], in) || overlaps(outs[1], in))
+    return set_err(e, ZERO_ERR_ARG, "muon: master, working weights and update overlap");
+  return check_device_float(lr_dev, "lr_dev", outs, 2, e);
+}
+
+int check_ns_shape(int64_t n_mats, int64_t rows, int64_t cols, Err& e) {
+  if (n_mats < 0 || rows < 0 || cols < 0) return set_err(e, ZERO_ERR_ARG, "newton_schulz: negative size");
+  if (n_mats > ZERO_NS_MAX_MATS)
+    return set_err(e, ZERO_ERR_SIZE, "newton_schulz: n_mats=%lld above %d", (long long)n_mats, ZERO_NS_MAX_MATS);
+  if (rows > ZERO_NS_MAX_SIDE || cols > ZERO_NS_MAX_SIDE)
+    return set_err(e, ZERO_ERR_SIZE, "newton_schulz: a side above %d", ZERO_NS_MAX_SIDE);
+  // the workspace: at most 3*(rows + 64)*(cols + 64) + 3*(min side + 64)^2 two-byte values per matrix
+  if (n_mats > 0 && mul_overflows((rows + 64) * (cols + 64) * 16, n_mats))
+    return set_err(e, ZERO_ERR_SIZE, "newton_schulz: size overflow");
+  return ZERO_OK;
+}
+
+// The largest |p(s)| and |p(s)/s| of p(s) = a s + b s^3 + c s^5 over 0 <= s <= top.
+static void ns_step_bound(double a, double b, double c, double top, double* p_max, double* r_max) {
+  auto p = [&](double s) { return std::fabs(((c * s * s + b) * s * s + a) * s); };
+  auto r = [&](double x) { return std::fabs((c * x + b) * x + a); };
+  double pm = p(top), rm = std::fmax(r(0.0), r(top * top));
+  if (c != 0.0) {
+    const double x = -b / (2.0 * c);  // vertex of a + b x + c x^2, x = s^2
+    if (x > 0.0 && x < top * top) rm = std::fmax(rm, r(x));
+  }
+  // stationary points: a + 3 b x + 5 c x^2 = 0
+  double x[2] = {-1.0, -1.0};
+  if (c != 0.0) {
+    const double d = 9.0 * b * b - 20.0 * a * c;
+    if (d >= 0.0) {
+      x[0] = (-3.0 * b + std::sqrt(d)) / (10.0 * c);
+      x[1] = (-3.0 * b - std::sqrt(d)) / (10.0 * c);
+    }
+  } else if (b != 0.0) {
+    x[0] = -a / (3.0 * b);
+  }
+  for (double v : x)
+    if (v > 0.0 && v < top * top) pm = std::fmax(pm, p(std::sqrt(v)));
+  *p_max = pm;
+  *r_max = rm;
+}
+
+int check_ns_coefs(const float* coefs, int steps, Err& e) {
+  if (!coefs) return set_err(e, ZERO_ERR_ARG, "newton_schulz: NULL coefficients");
+  if (steps < 1 || steps > ZERO_NS_MAX_STEPS)
+    return set_err(e, ZERO_ERR_ARG, "newton_schulz: steps=%d outside [1,%d]", steps, ZERO_NS_MAX_STEPS);
+  // The singular values start in [0, 1].  The kernels hold X, A and C in FP16
+  // with fixed power-of-two scales that leave room for singular values up to
+  // ZERO_NS_MAX_SIGMA and a step's gain |p(s)/s| up to ZERO_NS_MAX_GAIN.
+  double top = 1.0;
+  for (int t = 0; t < steps; ++t) {
+    const double a = coefs[3 * t], b = coefs[3 * t + 1], c = coefs[3 * t + 2];
+    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c))
+      return set_err(e, ZERO_ERR_ARG, "newton_schulz: coefficients of step %d are not finite", t);
+    double p_max, r_max;
+    ns_step_bound(a, b, c, top, &p_max, &r_max);
+    if (!(p_max <= ZERO_NS_MAX_SIGMA) || !(r_max <= ZERO_NS_MAX_GAIN))
+      return set_err(e, ZERO_ERR_ARG, "newton_schulz: step %d takes singular values to %g with a gain of %g (limits %d and %d)",
+                     t, p_max, r_max, ZERO_NS_MAX_SIGMA, ZERO_NS_MAX_GAIN);
+    top = p_max;
+  }
+  return ZERO_OK;
+}
+
+// Bytes from a matrix stack's first element to the end of its last.
+static int64_t stack_bytes(int64_t mats, int64_t rows, int64_t cols, int64_t row_stride, int64_t mat_stride,
+                           int64_t elem) {
+  return ((mats - 1) * mat_stride + (rows - 1) * row_stride + cols) * elem;
+}
+
+static int check_ns_strides(const char* name, int64_t mats, int64_t rows, int64_t cols, int64_t row_stride,
+                            int64_t mat_stride, Err& e) {
+  if (rows > 1 && row_stride < cols)
+    return set_err(e, ZERO_ERR_SIZE, "newton_schulz: %s row stride %lld below cols", name, (long long)row_stride);
+  if (row_stride < 0 || mat_stride < 0 || mul_overflows(rows, row_stride) ||
+      mul_overflows(mats, mat_stride) || rows * row_stride > INT64_MAX / 16 - mats * mat_stride)
+    return set_err(e, ZERO_ERR_SIZE, "newton_schulz: %s strides out of range", name);
+  if (mats > 1 && mat_stride < (rows - 1) * row_stride + cols)
+    return set_err(e, ZERO_ERR_SIZE, "newton_schulz: %s matrices overlap", name);
+  return ZERO_OK;
+}
+
+int check_newton_schulz(const void* in, int in_dtype, int64_t in_row_stride, int64_t in_mat_stride,
+                        const uint16_t* out, int64_t out_row_stride, int64_t out_mat_stride,
+                        int64_t n_mats, int64_t rows, int64_t cols, const float* coefs, int steps,
+                        float scale, const void* workspace, int64_t workspace_bytes,
+                        int64_t workspace_need, Err& e) {
+  int st = check_ns_coefs(coefs, steps, e);
+  if (st) return st;
+  if (in_dtype != ZERO_BF16 && in_dtype != ZERO_FP32)
+    return set_err(e, ZERO_ERR_ARG, "newton_schulz: in_dtype=%d is neither ZERO_BF16 nor ZERO_FP32", in_dtype);
+  if (!std::isfinite(scale)) return set_err(e, ZERO_ERR_ARG, "newton_schulz: scale is not finite");
+  st = check_ns_shape(n_mats, rows, cols, e);
+  if (st) return st;
+  if (n_mats == 0 || rows == 0 || cols == 0) return ZERO_OK;  // touches no buffer; NULL pointers allowed
+  if (!in || !out || !workspace) return set_err(e, ZERO_ERR_ARG, "newton_schulz: NULL buffer");
+  st = check_ns_strides("input", n_mats, rows, cols, in_row_stride, in_mat_stride, e);
+  if (!st) st = check_ns_strides("output", n_mats, rows, cols, out_row_stride, out_mat_stride, e);
+  if (st) return st;
+  const int64_t esz = in_dtype == ZERO_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(in) & static_cast<uintptr_t>(esz - 1))
+    return set_err(e, ZERO_ERR_ALIGN, "newton_schulz: input not %d-byte aligned", (int)esz);
+  if (reinterpret_cast<uintptr_t>(out) & 1u)
+    return set_err(e, ZERO_ERR_ALIGN, "newton_schulz: output not 2-byte aligned");
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return set_err(e, ZERO_ERR_ALIGN, "newton_schulz: workspace not 256-byte aligned");
+  if (workspace_bytes < workspace_need)
+    return set_err(e, ZERO_ERR_SIZE, "newton_schulz: workspace of %lld bytes, %lld needed",
+                   (long long)workspace_bytes, (long long)workspace_need);
+  const Range ri = range_of(in, stack_bytes(n_mats, rows, cols, in_row_stride, in_mat_stride, esz));
+  const Range ro = range_of(out, stack_bytes(n_mats, rows, cols, out_row_stride, out_mat_stride, 2));
+  const Range rw = range_of(workspace, workspace_need);
+  if (overlaps(ri, ro) || overlaps(ri, rw) || overlaps(ro, rw))
+    return set_err(e, ZERO_ERR_ARG, "newton_schulz: input, output and workspace overlap");
+  return ZERO_OK;
+}
+
 }  // namespace zero

@@ -86,6 +86,26 @@ int check_grad_norm(const float* const* shards, int n_shards, int64_t shard_nume
                     const double* workspace, int64_t workspace_len, const double* norm_sq_out,
                     float max_norm, const float* clip_coef_out, Err& e);
 
+// The Muon step.  The momentum step's buffers and scalars, its fused form, the
+// owner update, and the Newton-Schulz call (workspace_need: the bytes the call
+// needs, from ns_workspace_bytes).
+int check_muon_hparams(const zero_muon_hparams* hp, Err& e);
+int check_muon_momentum(const float* momentum, const uint16_t* direction_out, const float* grad,
+                        const float* grad_scale, int64_t n, const zero_muon_hparams* hp, Err& e);
+int check_reduce_scatter_muon(const uint16_t* const* rank_grads, const float* rank_weights, int n_ranks,
+                              int64_t numel, int n_shards, float* const* momentum,
+                              uint16_t* const* direction_out, const float* const* grad_acc,
+                              const zero_muon_hparams* hp, Err& e);
+int check_muon_shard(const float* master, const uint16_t* bf16_out, const uint16_t* update,
+                     const float* lr_dev, int64_t n, const zero_muon_hparams* hp, Err& e);
+int check_ns_shape(int64_t n_mats, int64_t rows, int64_t cols, Err& e);
+int check_ns_coefs(const float* coefs, int steps, Err& e);
+int check_newton_schulz(const void* in, int in_dtype, int64_t in_row_stride, int64_t in_mat_stride,
+                        const uint16_t* out, int64_t out_row_stride, int64_t out_mat_stride,
+                        int64_t n_mats, int64_t rows, int64_t cols, const float* coefs, int steps,
+                        float scale, const void* workspace, int64_t workspace_bytes,
+                        int64_t workspace_need, Err& e);
+
 // Alignment tests for the kernels' vector paths.
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }

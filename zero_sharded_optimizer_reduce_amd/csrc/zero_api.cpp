@@ -419,4 +419,132 @@ int zero_all_gather_layer(const void* const* shards, int n_shards, int64_t shard
                     "zero_all_gather_layer");
 }
 
+// ---------------------------------------------------------------- Muon step
+static MuonScalars muon_scalars(const zero_muon_hparams* hp) {
+  MuonScalars s;
+  s.momentum = hp->momentum;
+  s.one_minus_momentum = 1.0f - hp->momentum;
+  s.nesterov = hp->nesterov;
+  return s;
+}
+
+int zero_muon_momentum(float* momentum, uint16_t* direction_out, const float* grad, const float* grad_scale,
+                       int64_t n, const zero_muon_hparams* hp, void* stream) {
+  TraceRange tr("zero_muon_momentum");
+  Err e;
+  int st = check_muon_momentum(momentum, direction_out, grad, grad_scale, n, hp, e);
+  if (st) return fail(st, e.msg);
+  if (n == 0) return ZERO_OK;
+  MomentumParams a;
+  memset(&a, 0, sizeof a);
+  a.m = momentum;
+  a.u = direction_out;
+  a.g = grad;
+  a.gscale = grad_scale;
+  a.n = n;
+  a.s = muon_scalars(hp);
+  const bool vec = aligned16(momentum) && aligned16(grad) && aligned8(direction_out);
+  set_path(vec);
+  return hip_status(launch_momentum(a, vec, static_cast<hipStream_t>(stream)), "zero_muon_momentum");
+}
+
+int zero_reduce_scatter_muon(const uint16_t* const* rank_grads, const float* rank_weights, int n_ranks,
+                             int64_t numel, int n_shards, float* const* momentum,
+                             uint16_t* const* direction_out, const float* const* grad_acc,
+                             const zero_muon_hparams* hp, void* stream) {
+  TraceRange tr("zero_reduce_scatter_muon");
+  Err e;
+  int st = check_reduce_scatter_muon(rank_grads, rank_weights, n_ranks, numel, n_shards, momentum,
+                                     direction_out, grad_acc, hp, e);
+  if (st) return fail(st, e.msg);
+  if (numel == 0) return ZERO_OK;
+  const int64_t shard = numel / n_shards;
+  bool all_vec = true;
+  // one launch per owner, as in the reduce-scatter: the tiles in flight stay
+  // within one owner's buffers
+  for (int k = 0; k < n_shards; ++k) {
+    ReduceMomentumParams p;
+    memset(&p, 0, sizeof p);
+    for (int r = 0; r < n_ranks; ++r) {
+      p.g[r] = rank_grads[r] + k * shard;
+      p.w[r] = rank_weights[r];
+    }
+    p.m = momentum[k];
+    p.u = direction_out[k];
+    p.gacc = grad_acc ? grad_acc[k] : nullptr;
+    p.n = shard;
+    p.n_ranks = n_ranks;
+    p.s = muon_scalars(hp);
+    const bool vec = aligned16(p.m) && aligned16(p.gacc) && aligned8(p.u);
+    all_vec = all_vec && vec;
+    st = hip_status(launch_reduce_momentum(p, vec, static_cast<hipStream_t>(stream)), "zero_reduce_scatter_muon");
+    if (st) return st;
+  }
+  set_path(all_vec);
+  return ZERO_OK;
+}
+
+int zero_muon_shard_step(float* master, uint16_t* bf16_out, const uint16_t* update, int64_t n,
+                         const zero_muon_hparams* hp, const float* lr_dev, void* stream) {
+  TraceRange tr("zero_muon_shard_step");
+  Err e;
+  int st = check_muon_shard(master, bf16_out, update, lr_dev, n, hp, e);
+  if (st) return fail(st, e.msg);
+  if (n == 0) return ZERO_OK;
+  MuonUpdateParams a;
+  memset(&a, 0, sizeof a);
+  a.p = master;
+  a.b = bf16_out;
+  a.o = update;
+  a.lr_dev = lr_dev;
+  a.n = n;
+  a.lr = hp->lr;
+  a.wd = hp->weight_decay;
+  const bool vec = aligned16(master) && aligned8(bf16_out);
+  set_path(vec);
+  return hip_status(launch_muon_update(a, vec, static_cast<hipStream_t>(stream)), "zero_muon_shard_step");
+}
+
+int zero_newton_schulz_workspace(int64_t n_mats, int64_t rows, int64_t cols, int64_t* bytes_out) {
+  Err e;
+  if (!bytes_out) return fail(ZERO_ERR_ARG, "newton_schulz: NULL bytes_out");
+  int st = check_ns_shape(n_mats, rows, cols, e);
+  if (st) return fail(st, e.msg);
+  *bytes_out = ns_workspace_bytes(n_mats, rows, cols);
+  return ZERO_OK;
+}
+
+int zero_newton_schulz(const void* in, int in_dtype, int64_t in_row_stride, int64_t in_mat_stride,
+                       uint16_t* out, int64_t out_row_stride, int64_t out_mat_stride, int64_t n_mats,
+                       int64_t rows, int64_t cols, const float* coefs, int steps, float scale,
+                       void* workspace, int64_t workspace_bytes, void* stream) {
+  TraceRange tr("zero_newton_schulz");
+  Err e;
+  int st = check_ns_shape(n_mats, rows, cols, e);
+  if (st) return fail(st, e.msg);
+  st = check_newton_schulz(in, in_dtype, in_row_stride, in_mat_stride, out, out_row_stride, out_mat_stride,
+                           n_mats, rows, cols, coefs, steps, scale, workspace, workspace_bytes,
+                           ns_workspace_bytes(n_mats, rows, cols), e);
+  if (st) return fail(st, e.msg);
+  if (n_mats == 0 || rows == 0 || cols == 0) return ZERO_OK;
+  NsParams p;
+  memset(&p, 0, sizeof p);
+  p.in = in;
+  p.out = out;
+  p.workspace = workspace;
+  p.coefs = coefs;
+  p.in_row = in_row_stride;
+  p.in_mat = in_mat_stride;
+  p.out_row = out_row_stride;
+  p.out_mat = out_mat_stride;
+  p.mats = n_mats;
+  p.rows = rows;
+  p.cols = cols;
+  p.steps = steps;
+  p.in_f32 = in_dtype == ZERO_FP32;
+  p.scale = scale;
+  set_path(true);
+  return hip_status(launch_newton_schulz(p, static_cast<hipStream_t>(stream)), "zero_newton_schulz");
+}
+
 }  // extern "C"
