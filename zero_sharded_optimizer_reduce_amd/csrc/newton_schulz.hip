@@ -60,7 +60,7 @@ __device__ __forceinline__ uint16_t bf16_rne(float x) {
 
 // ------------------------------------------------------------------ norm
 constexpr int kNormThreads = 256;
-constexpr int kNormParts = 1024;  // partial sums per matrix, at most
+constexpr int kNormParts = kNormThreads;  // partial sums per matrix, at most
 
 struct NsInput {
   const void* in;
@@ -131,24 +131,20 @@ __global__ __launch_bounds__(kNormThreads) void ns_norm_kernel(NsInput g, double
   if (threadIdx.x == 0) partials[static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = t;
 }
 
-// Per matrix kScaleX / norm = f * 2^e with f in [1/2, 1).  A zero matrix stays
-// zero; `add` makes everything NaN when the sum of squares is not finite.
+// kScaleX / norm = f * 2^e with f in [1/2, 1) from the sum of squares.  A zero
+// matrix stays zero; `add` makes everything NaN when the sum is not finite.
 struct NsScale {
   float f, add;
-  int e, unused;
+  int e;
 };
 
-__global__ __launch_bounds__(kNormThreads) void ns_scale_kernel(const double* partials, int parts, NsScale* scales) {
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < parts; i += kNormThreads) sum += partials[static_cast<int64_t>(blockIdx.x) * parts + i];
-  sum = block_sum(sum);
-  if (threadIdx.x != 0) return;
-  NsScale s = {1.0f, 0.0f, 0, 0};
+__device__ __forceinline__ NsScale scale_of(double sum) {
+  NsScale s = {1.0f, 0.0f, 0};
   if (sum > 0.0 && sum < __builtin_huge_val())
     s.f = static_cast<float>(frexp(static_cast<double>(kScaleX) / sqrt(sum), &s.e));
   else if (sum != 0.0)
     s.add = __builtin_nanf("");
-  scales[blockIdx.x] = s;
+  return s;
 }
 
 // ------------------------------------------------------------------ X
@@ -159,32 +155,43 @@ struct NsX {
   half_t* same;      // G's own orientation, rows x cols, pitch pad(cols)
   half_t* turned;    // cols x rows, pitch pad(rows)
   int64_t same_mat, turned_mat;
-  const NsScale* scales;
+  const double* partials;
+  int parts;
+  float* f;          // per matrix, for the products
 };
 
 constexpr int kTurn = 64;
 
-// One 64 x 64 tile to both copies; the padding is written as zeros.
+// One 64 x 64 tile to both copies; the padding is written as zeros.  Every
+// workgroup adds the partial sums up itself, while its tile is on its way.
 __global__ __launch_bounds__(kNormThreads) void ns_prepare_kernel(NsInput g, NsX x) {
   // 33 words a row: the eight rows a lane group gathers lie in different banks
   __shared__ uint32_t tile[kTurn][kTurn / 2 + 1];
   const int mat = blockIdx.z;
-  const NsScale s = x.scales[mat];
   const int r0 = blockIdx.y * kTurn, c0 = blockIdx.x * kTurn;
   const int pc = static_cast<int>(pad_up(g.cols)), pr = static_cast<int>(pad_up(g.rows));
   half_t* same = x.same + mat * x.same_mat;
   half_t* turned = x.turned + mat * x.turned_mat;
   const int64_t base = static_cast<int64_t>(mat) * g.mat;
   const int line = threadIdx.x >> 3, c = (threadIdx.x & 7) * 8;
+  constexpr int kLines = kTurn / (kNormThreads / 8);
+  f8 v[kLines];
 #pragma unroll
-  for (int i = line; i < kTurn; i += kNormThreads / 8) {
-    const int r = r0 + i;
-    f8 v = {};
-    if (r < g.rows) v = load8(g, base + static_cast<int64_t>(r) * g.row, c0 + c);
+  for (int n = 0; n < kLines; ++n) {
+    const int r = r0 + line + n * (kNormThreads / 8);
+    v[n] = f8{};
+    if (r < g.rows) v[n] = load8(g, base + static_cast<int64_t>(r) * g.row, c0 + c);
+  }
+  const NsScale s = scale_of(block_sum(
+      threadIdx.x < x.parts ? x.partials[static_cast<int64_t>(mat) * x.parts + threadIdx.x] : 0.0));
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) x.f[mat] = s.f;
+#pragma unroll
+  for (int n = 0; n < kLines; ++n) {
+    const int i = line + n * (kNormThreads / 8), r = r0 + i;
     h8 h;
 #pragma unroll
     for (int q = 0; q < 8; ++q)
-      h[q] = r < g.rows && c0 + c + q < g.cols ? static_cast<half_t>(ldexpf(v[q], s.e) + s.add) : half_t(0);
+      h[q] = r < g.rows && c0 + c + q < g.cols ? static_cast<half_t>(ldexpf(v[n][q], s.e) + s.add) : half_t(0);
     if (r < g.rows) *reinterpret_cast<h8*>(same + static_cast<int64_t>(r) * pc + c0 + c) = h;
     const u32x4 w = __builtin_bit_cast(u32x4, h);
 #pragma unroll
@@ -207,6 +214,7 @@ __global__ __launch_bounds__(kNormThreads) void ns_prepare_kernel(NsInput g, NsX
 // ------------------------------------------------------------------ products
 // D = alpha' P Q^T with P m x kk, Q n x kk (pitches p_ld, q_ld; kk a multiple of
 // kPad, the padding zero).
+enum Epilogue { kPlain, kPoly, kCarryOut, kCarryIn, kOut };
 struct Product {
   const half_t* p;
   const half_t* q;
@@ -223,7 +231,7 @@ struct Product {
   int d_ld, dt_ld;
   const half_t* add;        // polynomial: beta * add + diag * I joins (symmetric, pitch d_ld)
   float alpha, beta, diag;
-  const NsScale* scales;    // per-matrix factor f of alpha, or NULL
+  const float* f;           // per-matrix factor of alpha, or NULL
   int f_pow;
   uint16_t* out;            // BF16 result instead of d, dt
   int64_t out_row, out_mat;
@@ -316,6 +324,26 @@ __device__ __forceinline__ int xcd_order(int id, int n) {
   return xcd * each + (xcd < more ? xcd : more) + (id >> 3);
 }
 
+// 8 values down a column: the lane gets rows row + 8 * (lane >> 4) + 0..7 of column
+// col + (lane & 15).  The transposing LDS read hands lane j of 16 the component
+// j % 4 of the lanes j / 4 + 4 q, so each lane points at four columns of one row.
+__device__ __forceinline__ u32x4 transpose8(const void* at, const void* at4) {
+  u32x4 v = {};
+#ifdef __HIP_DEVICE_COMPILE__   // the builtin is unknown to the host pass
+  typedef short s4 __attribute__((ext_vector_type(4)));
+  typedef short s8 __attribute__((ext_vector_type(8)));
+  typedef __attribute__((address_space(3))) s4 lds_s4;
+  const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)at);
+  const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)at4);
+  v = __builtin_bit_cast(u32x4, s8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w});
+#endif
+  return v;
+}
+__device__ __forceinline__ u32x4 column_piece(const uint16_t* m, int pitch, int row, int col, int lane) {
+  const uint16_t* at = m + (row + (lane >> 4) * 8 + ((lane >> 2) & 3)) * pitch + col + (lane & 3) * 4;
+  return transpose8(at, at + 4 * pitch);
+}
+
 template <int NW>
 __device__ __forceinline__ float block_sum_f32(float x, float* part) {
 #pragma unroll
@@ -335,7 +363,7 @@ __device__ __forceinline__ float block_sum_f32(float x, float* part) {
 // on one half the wave reads the next one's fragments, and the loads are issued
 // evenly between the products (a wave issues in order: loads in a row
 // hold its products up while the CU takes them in, about 26 clocks each).
-template <int BM, int BN, int WR, int WC, bool SYM>
+template <int BM, int BN, int WR, int WC, bool SYM, int EPI>
 __global__ __launch_bounds__(WR * WC * 64) void ns_product_kernel(Product g) {
   constexpr int NW = WR * WC;
   constexpr int TM = BM / WR / 32, TN = BN / WC / 32;   // 32 x 32 blocks of a wave
@@ -383,7 +411,7 @@ __global__ __launch_bounds__(WR * WC * 64) void ns_product_kernel(Product g) {
 #pragma unroll
       for (int k = s * kProducts / n_loads; k < (s + 1) * kProducts / n_loads; ++k) {
         const int u = k / (TM * TN), i = (k - u * TM * TN) / TN, j = k % TN;
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(now.a[u][i], now.b[u][j], acc[i][j], 0, 0, 0);
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(now.b[u][j], now.a[u][i], acc[i][j], 0, 0, 0);
       }
       loads(s);
 #pragma unroll
@@ -424,73 +452,32 @@ __global__ __launch_bounds__(WR * WC * 64) void ns_product_kernel(Product g) {
   __builtin_amdgcn_s_waitcnt(wait_vm_lds(0));
   wave_barrier();   // nothing is on its way into LDS any more
 
-  // The lane's values of block (i, j): one column, rows 8*u + 4*(lane >> 5) + q.
+  // The lane's values of block (i, j): row lane & 31 of the block, columns 8 * u +
+  // 4 * (lane >> 5) + q (the products take Q's fragment first).
   float alpha = g.alpha;
-  if (g.scales) {
-    const float f = g.scales[mat].f;
+  if (g.f) {
+    const float f = g.f[mat];
     alpha *= g.f_pow == 2 ? f * f : f;
   }
-  const half_t* add = g.add ? g.add + mat * g.d_mat : nullptr;
   float gain = 0.0f;
-  if (g.carry_in) {
+  if constexpr (EPI == kCarryIn) {
     const half_t* c = g.p + mat * g.p_mat;
     float sum = 0.0f;
     for (int i = threadIdx.x; i < g.m; i += NW * 64) sum += static_cast<float>(c[static_cast<int64_t>(i) * g.p_ld + i]);
     gain = block_sum_f32<NW>(sum, reinterpret_cast<float*>(slot4)) * g.alpha / (static_cast<float>(g.m) * kScaleE);
   }
-  const int lr = (lane >> 5) << 2, lc = lane & 31;
+  const int lm = lane & 31, ln = (lane >> 5) << 2;
   const int wrow = row0 + wr * (BM / WR), wcol = col0 + wc * (BN / WC);
-  auto four = [&](int i, int j, int u) {   // four values, as the 16-bit words that are stored
-    const int r = wrow + i * 32 + u * 8 + lr, c = wcol + j * 32 + lc;
-    float v[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = acc[i][j][u * 4 + q] * alpha;
-    if (add && c < g.n && r < g.m) {
-      // add is symmetric: the lane's four rows of column c are four columns of row c
-      const h4 w = *reinterpret_cast<const h4*>(add + static_cast<int64_t>(c) * g.d_ld + r);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        v[q] += g.beta * static_cast<float>(w[q]);
-        if (r + q == c) v[q] += g.diag;
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (r + q >= g.m || c >= g.n) v[q] = 0.0f;
-    const int64_t at =
-        mat * g.carry_mat + (((static_cast<int64_t>(t) * TM + i) * TN + j) * 4 + u) * (NW * 256) + threadIdx.x * 4;
-    if (g.carry_in) {
-      const h4 w = *reinterpret_cast<const h4*>(g.carry_in + at);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] += gain * static_cast<float>(w[q]);
-    }
-    u16x4 o;
-    if (g.out) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) o[q] = bf16_rne(v[q]);
-    } else {
-      h4 h;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) h[q] = static_cast<half_t>(v[q]);
-      o = __builtin_bit_cast(u16x4, h);
-      if (g.carry_out) {
-        h4 w;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) w[q] = static_cast<half_t>((v[q] - static_cast<float>(h[q])) * kScaleE);
-        *reinterpret_cast<h4*>(g.carry_out + at) = w;
-      }
-    }
-    return o;
-  };
-
+  const bool edge = row0 + BM > g.m || col0 + BN > g.n;
   // Results pass through the wave's own part of LDS, kBand blocks of rows at a
-  // time, so that they leave as rows of 16-byte pieces.  A wave's LDS
-  // operations are carried out in order, so no barrier is needed.
-  constexpr int kBand = NW == 8 ? 1 : TM % 2 == 0 ? 2 : TM;
-  constexpr int kRows = kBand * 32, kCols = TN * 32;
-  static_assert(TM % kBand == 0, "whole bands");
+  // time, so that they leave as rows of 16-byte pieces; the transpose is read
+  // from there with transposing reads.  A wave's LDS operations are carried out
+  // in order, so no barrier is needed.
+  constexpr int kBand = TM % 2 == 0 ? 2 : TM;
+  constexpr int kRows = kBand * 32, kCols = TN * 32, kPitch = kCols + 8;
   constexpr int kPart = kSlot / (NW / 4);
-  static_assert(kRows * (kCols + 8) <= kPart && kCols * (kRows + 8) <= kPart, "a band fits the wave's part");
+  static_assert(TM % kBand == 0, "whole bands");
+  static_assert(kRows * kPitch <= kPart, "a band fits the wave's part");
   uint16_t* mine = reinterpret_cast<uint16_t*>((wave & 3) == 0 ? slot0 : (wave & 3) == 1 ? slot1 : (wave & 3) == 2 ? slot2 : slot3) +
                    (wave >> 2) * kPart;
   // A tile on the diagonal of a symmetric product: only what lies below the
@@ -498,22 +485,71 @@ __global__ __launch_bounds__(WR * WC * 64) void ns_product_kernel(Product g) {
   const bool diagonal = SYM && ti == tj;
 #pragma unroll
   for (int ib = 0; ib < TM; ib += kBand) {
-    u16x4 o[kBand][TN][4];
+    const int64_t carry = mat * g.carry_mat + static_cast<int64_t>(t) * (BM * BN) + threadIdx.x * 4;
+    // what joins the products: all loads of the band before the first use
+    h4 more[kBand][TN][4];
+    if constexpr (EPI == kPoly || EPI == kCarryIn) {
+#pragma unroll
+      for (int i = 0; i < kBand; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            if constexpr (EPI == kPoly) {
+              const int r = wrow + (ib + i) * 32 + lm, c = wcol + j * 32 + u * 8 + ln;
+              // past the edge: some other value, dropped below
+              more[i][j][u] = *reinterpret_cast<const h4*>(
+                  g.add + mat * g.d_mat + static_cast<int64_t>(r < g.m ? r : 0) * g.d_ld + (c < g.d_ld ? c : 0));
+            } else {
+              more[i][j][u] =
+                  *reinterpret_cast<const h4*>(g.carry_in + carry + (((ib + i) * TN + j) * 4 + u) * (NW * 256));
+            }
+          }
+    }
 #pragma unroll
     for (int i = 0; i < kBand; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) o[i][j][u] = four(ib + i, j, u);
-    constexpr int pitch = kCols + 8;
+        for (int u = 0; u < 4; ++u) {
+          const int r = wrow + (ib + i) * 32 + lm, c = wcol + j * 32 + u * 8 + ln;
+          float v[4];
 #pragma unroll
-    for (int i = 0; i < kBand; ++i)
+          for (int q = 0; q < 4; ++q) v[q] = acc[ib + i][j][u * 4 + q] * alpha;
+          if constexpr (EPI == kPoly) {
 #pragma unroll
-      for (int j = 0; j < TN; ++j)
+            for (int q = 0; q < 4; ++q) {
+              v[q] += g.beta * static_cast<float>(more[i][j][u][q]);
+              if (diagonal && r == c + q) v[q] += g.diag;
+            }
+          }
+          if constexpr (EPI == kCarryIn) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+            for (int q = 0; q < 4; ++q) v[q] += gain * static_cast<float>(more[i][j][u][q]);
+          }
+          if (edge) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) mine[(i * 32 + u * 8 + lr + q) * pitch + j * 32 + lc] = o[i][j][u][q];
+            for (int q = 0; q < 4; ++q)
+              if (r >= g.m || c + q >= g.n) v[q] = 0.0f;
+          }
+          u16x4 o;
+          if constexpr (EPI == kOut) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o[q] = bf16_rne(v[q]);
+          } else {
+            h4 h;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) h[q] = static_cast<half_t>(v[q]);
+            o = __builtin_bit_cast(u16x4, h);
+            if constexpr (EPI == kCarryOut) {
+              h4 w;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) w[q] = static_cast<half_t>((v[q] - static_cast<float>(h[q])) * kScaleE);
+              *reinterpret_cast<h4*>(g.carry_out + carry + (((ib + i) * TN + j) * 4 + u) * (NW * 256)) = w;
+            }
+          }
+          *reinterpret_cast<u16x4*>(mine + (i * 32 + lm) * kPitch + j * 32 + u * 8 + ln) = o;
+        }
     if (diagonal) {
 #pragma unroll
       for (int i = 0; i < kBand; ++i)
@@ -522,9 +558,9 @@ __global__ __launch_bounds__(WR * WC * 64) void ns_product_kernel(Product g) {
           if (wrow + (ib + i) * 32 == wcol + j * 32) {   // a block on the diagonal: its upper half from the lower
 #pragma unroll
             for (int u = 0; u < 16; ++u) {
-              const int r = (u >> 2) * 8 + lr + (u & 3);
-              const uint16_t low = mine[(i * 32 + lc) * pitch + j * 32 + r];
-              if (r < lc) mine[(i * 32 + r) * pitch + j * 32 + lc] = low;
+              const int c = (u >> 2) * 8 + ln + (u & 3);
+              const uint16_t low = mine[(i * 32 + c) * kPitch + j * 32 + lm];
+              if (c > lm) mine[(i * 32 + lm) * kPitch + j * 32 + c] = low;
             }
           }
     }
@@ -533,9 +569,9 @@ __global__ __launch_bounds__(WR * WC * 64) void ns_product_kernel(Product g) {
       const int at = k * 64 + lane;
       const int lrow = at / (kCols / 8), lcol = (at - lrow * (kCols / 8)) * 8;
       const int r = wrow + ib * 32 + lrow, c = wcol + lcol;
-      const u32x4 piece = *reinterpret_cast<const u32x4*>(mine + lrow * pitch + lcol);
+      const u32x4 piece = *reinterpret_cast<const u32x4*>(mine + lrow * kPitch + lcol);
       if (r >= g.m || (diagonal && (c >> 5) > (r >> 5))) continue;
-      if (!g.out) {
+      if constexpr (EPI != kOut) {
         if (c < g.d_ld) *reinterpret_cast<u32x4*>(g.d + mat * g.d_mat + static_cast<int64_t>(r) * g.d_ld + c) = piece;
       } else {
         uint16_t* dst = g.out + mat * g.out_mat + static_cast<int64_t>(r) * g.out_row + c;
@@ -548,66 +584,67 @@ __global__ __launch_bounds__(WR * WC * 64) void ns_product_kernel(Product g) {
         }
       }
     }
-    if (g.dt) {
-      constexpr int turned = kRows + 8;
+    if constexpr (EPI != kOut) {
+      if (g.dt) {
 #pragma unroll
-      for (int i = 0; i < kBand; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            *reinterpret_cast<u16x4*>(mine + (j * 32 + lc) * turned + i * 32 + u * 8 + lr) = o[i][j][u];
-#pragma unroll
-      for (int k = 0; k < kRows * kCols / 512; ++k) {
-        const int at = k * 64 + lane;
-        const int lcol = at / (kRows / 8), lrow = (at - lcol * (kRows / 8)) * 8;
-        const int c = wcol + lcol, r = wrow + ib * 32 + lrow;
-        const u32x4 piece = *reinterpret_cast<const u32x4*>(mine + lcol * turned + lrow);
-        if (c < g.n && r < g.dt_ld && !(diagonal && (c >> 5) >= (r >> 5)))
-          *reinterpret_cast<u32x4*>(g.dt + mat * g.dt_mat + static_cast<int64_t>(c) * g.dt_ld + r) = piece;
+        for (int k = 0; k < kRows * kCols / 512; ++k) {
+          // 16 columns, 8 rows of each 8 * (lane >> 4) rows on
+          const int lrow = k % kBand * 32, lcol = k / kBand * 16;
+          const u32x4 piece = column_piece(mine, kPitch, lrow, lcol, lane);
+          const int c = wcol + lcol + (lane & 15), r = wrow + ib * 32 + lrow + (lane >> 4) * 8;
+          if (c < g.n && r < g.dt_ld && !(diagonal && (c >> 5) >= (r >> 5)))
+            *reinterpret_cast<u32x4*>(g.dt + mat * g.dt_mat + static_cast<int64_t>(c) * g.dt_ld + r) = piece;
+        }
       }
     }
   }
-  // The padding past the last tile, as zeros.
-  if (g.d && col0 + BN >= g.n)
-    for (int c = col0 + BN + lane; c < g.d_ld; c += 64)
-      for (int r = row0 + wave; r < g.m && r < row0 + BM; r += NW)
-        g.d[mat * g.d_mat + static_cast<int64_t>(r) * g.d_ld + c] = 0;
-  if (g.dt && row0 + BM >= g.m)
-    for (int r = row0 + BM + lane; r < g.dt_ld; r += 64)
-      for (int c = col0 + wave; c < g.n && c < col0 + BN; c += NW)
-        g.dt[mat * g.dt_mat + static_cast<int64_t>(c) * g.dt_ld + r] = 0;
+  if constexpr (EPI != kOut) {
+    // The padding past the last tile, as zeros.
+    if (col0 + BN >= g.n)
+      for (int c = col0 + BN + lane; c < g.d_ld; c += 64)
+        for (int r = row0 + wave; r < g.m && r < row0 + BM; r += NW)
+          g.d[mat * g.d_mat + static_cast<int64_t>(r) * g.d_ld + c] = 0;
+    if (g.dt && row0 + BM >= g.m)
+      for (int r = row0 + BM + lane; r < g.dt_ld; r += 64)
+        for (int c = col0 + wave; c < g.n && c < col0 + BN; c += NW)
+          g.dt[mat * g.dt_mat + static_cast<int64_t>(c) * g.dt_ld + r] = 0;
+  }
 }
 
 // ------------------------------------------------------------------ launches
-template <int BM, int BN, int WR, int WC, bool SYM>
+template <int BM, int BN, int WR, int WC, bool SYM, int EPI>
 hipError_t product_tiles(Product g, int64_t mats, hipStream_t s) {
   const int tm = (g.m + BM - 1) / BM;
   g.tiles_n = (g.n + BN - 1) / BN;
   g.tiles = SYM ? tm * (tm + 1) / 2 : tm * g.tiles_n;
-  hipLaunchKernelGGL((ns_product_kernel<BM, BN, WR, WC, SYM>), dim3(static_cast<unsigned>(g.tiles * mats)),
+  hipLaunchKernelGGL((ns_product_kernel<BM, BN, WR, WC, SYM, EPI>), dim3(static_cast<unsigned>(g.tiles * mats)),
                      dim3(WR * WC * 64), 0, s, g);
   return hipGetLastError();
 }
 
 // The tile for a product, by its modelled time: rounds of one tile per CU, each
-// of the time measured for a summed index of 4096 (256 CUs busy) and a fixed
-// part.  256: 115 us; 192 (symmetric only): 72; 128: 38; 64: 16.  A symmetric
-// 4096 x 4096 product has 253 tiles of 192 (72 us) against 136 of 256 (110), a
-// full one 256 of 256 (115) against 1024 of 128 (150).
-template <bool SYM>
+// proportional to the summed index (us at 4096) and a fixed part, fitted to
+// launches at k = 128 to 4096 on MI355X.  Both sides of a choice, measured: a
+// symmetric 4096 x 4096 x 4096 product takes 82 us with 253 tiles of 192 and
+// 105 with 528 of 128; of 512 x 512 x 512, 32 at once, 22 and 17; of 777 x 777 x
+// 832, three at once, 18 with 192, 12 with 128 and 8 with 64.  A full 4096 x 4096
+// x 4096 product 131 with 256 and 157 with 128; 1024 x 4096 x 1024, two at once,
+// 31 and 27.
+template <bool SYM, int EPI>
 hipError_t product(const Product& g, int64_t mats, hipStream_t s) {
-  auto time = [&](int side, double us) {
+  auto time = [&](int side, double us, double fixed) {
     const int64_t tm = (g.m + side - 1) / side, tn = (g.n + side - 1) / side;
     const int64_t tiles = (SYM ? tm * (tm + 1) / 2 : tm * tn) * mats;
-    return static_cast<double>((tiles + 255) / 256) * (us * g.kk / 4096.0 + 4.0);
+    return static_cast<double>((tiles + 255) / 256) * (us * g.kk / 4096.0 + fixed);
   };
-  const double t256 = time(256, 115.0), t192 = SYM ? time(192, 72.0) : t256, t128 = time(128, 38.0), t64 = time(64, 16.0);
-  const double best = fmin(fmin(t256, t192), fmin(t128, t64));
-  if (t256 == best) return product_tiles<256, 256, 2, 4, SYM>(g, mats, s);
-  if (t192 == best) return product_tiles<192, 192, 2, 2, true>(g, mats, s);
-  if (t128 == best) return product_tiles<128, 128, 2, 2, SYM>(g, mats, s);
-  return product_tiles<64, 64, 2, 2, SYM>(g, mats, s);
+  const double large = SYM ? time(192, 72.0, 12.0) : time(256, 118.0, 10.0);
+  const double t128 = time(128, 36.0, 4.5), t64 = time(64, 14.5, 2.0);
+  if (t64 <= t128 && t64 <= large) return product_tiles<64, 64, 2, 2, SYM, EPI>(g, mats, s);
+  if (t128 <= large) return product_tiles<128, 128, 2, 2, SYM, EPI>(g, mats, s);
+  if constexpr (SYM)
+    return product_tiles<192, 192, 2, 2, SYM, EPI>(g, mats, s);
+  else
+    return product_tiles<256, 256, 2, 4, SYM, EPI>(g, mats, s);
 }
 
 // The workspace: partial sums and factors, two turns of X^T and one X, three
@@ -615,7 +652,7 @@ hipError_t product(const Product& g, int64_t mats, hipStream_t s) {
 struct Layout {
   int64_t k, l, kp, lp;
   int64_t e_mat;                                   // rounding errors of one matrix: whole tiles
-  int64_t partials, scales, x, xt[2], sq[3], e, bytes;  // byte offsets
+  int64_t partials, f, x, xt[2], sq[3], e, bytes;  // byte offsets
   Layout(int64_t mats, int64_t rows, int64_t cols) {
     k = rows < cols ? rows : cols;
     l = rows < cols ? cols : rows;
@@ -628,7 +665,7 @@ struct Layout {
       return o;
     };
     partials = take(mats * kNormParts * 8);
-    scales = take(mats * static_cast<int64_t>(sizeof(NsScale)));
+    f = take(mats * 4);
     x = take(mats * k * lp * 2);
     for (int64_t& o : xt) o = take(mats * l * kp * 2);
     for (int64_t& o : sq) o = take(mats * k * kp * 2);
@@ -638,6 +675,313 @@ struct Layout {
   }
 };
 
+// ------------------------------------------------------------------ small matrices
+// A matrix that fits one CU's LDS is taken through all its steps by one
+// workgroup in one launch: the general path's launches, about 4 us each however
+// small, would be nearly all of its time.  X (k x l, rows in order) and A, then
+// C, are kept as pairs of FP16 values, v = hi + lo (22 bits), and a product is
+// hi hi + hi lo + lo hi: matrix time is not what bounds these sizes, and small
+// matrices gain most from the bits (2.6e-3 to 1.7e-3 off at 32 x 32, the BF16
+// rounding of the result alone).  Step by step, in 16 x 16 blocks.
+struct SmallNs {
+  NsInput in;
+  uint16_t* out;
+  int64_t out_row, out_mat;
+  int k, l, lp, steps, tall;
+  float scale;
+  float coefs[3 * ZERO_NS_MAX_STEPS];
+};
+
+typedef float acc4 __attribute__((ext_vector_type(4)));
+
+// 8 values from `at` on.
+__device__ __forceinline__ h8 row8(const half_t* p, int at) { return *reinterpret_cast<const h8*>(p + at); }
+
+// Where element (row, col) of X lies, pitch XP a multiple of 128 values (256
+// bytes, the banks once): the 16-byte piece of a row is moved by a permutation of
+// row % 16, so that neither 16 rows' pieces of one column group nor the eight
+// rows a transposing read takes from two pieces meet in a bank.  (A row pitch of
+// 8 values more instead left half of the LDS time to conflicts: the 16 lanes
+// served together are not 16 neighbours.)
+__device__ __forceinline__ int fold(int row) {
+  return ((row & 1) << 1) | ((row & 2) << 1) | (((row ^ (row << 1)) & 8)) | ((row >> 2) & 1);
+}
+template <int XP>
+__device__ __forceinline__ int x_at(int row, int col) {
+  return row * XP + ((((col >> 3) ^ fold(row))) << 3) + (col & 7);
+}
+
+// The same for A and C, KP values wide.
+constexpr int small_pitch_s(int kp) { return kp <= 64 ? kp : 128; }
+template <int KP>
+__device__ __forceinline__ int s_at(int row, int col) {
+  const int f = KP == 32 ? (row >> 2) & 3 : KP == 64 ? (row >> 1) & 7 : fold(row);
+  return row * small_pitch_s(KP) + (((col >> 3) ^ f) << 3) + (col & 7);
+}
+
+// P Q^T of pairs, as three sums that do not wait for each other.
+struct Acc3 {
+  acc4 hh = {0, 0, 0, 0}, hl = {0, 0, 0, 0}, lh = {0, 0, 0, 0};
+  __device__ __forceinline__ void add(const h8& ph, const h8& pl, const h8& qh, const h8& ql) {
+    lh = __builtin_amdgcn_mfma_f32_16x16x32_f16(pl, qh, lh, 0, 0, 0);
+    hl = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph, ql, hl, 0, 0, 0);
+    hh = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph, qh, hh, 0, 0, 0);
+  }
+  __device__ __forceinline__ acc4 sum() const { return hh + (hl + lh); }
+};
+
+// 8 values down a column of X: rows k0 + 8 * (lane >> 4) + 0..7 of column c0 +
+// (lane & 15).
+template <int XP>
+__device__ __forceinline__ h8 column8(const half_t* m, int k0, int c0, int lane) {
+  const int row = k0 + (lane >> 4) * 8 + ((lane >> 2) & 3), col = c0 + (lane & 3) * 4;
+  return __builtin_bit_cast(h8, transpose8(m + x_at<XP>(row, col), m + x_at<XP>(row + 4, col)));
+}
+
+__device__ __forceinline__ void split(float v, half_t* hi, half_t* lo) {
+  *hi = static_cast<half_t>(v);
+  *lo = static_cast<half_t>(v - static_cast<float>(*hi));
+}
+
+__device__ __forceinline__ void split4(acc4 v, half_t* hi, half_t* lo) {
+  h4 h, l;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    h[q] = static_cast<half_t>(v[q]);
+    l[q] = static_cast<half_t>(v[q] - static_cast<float>(h[q]));
+  }
+  *reinterpret_cast<h4*>(hi) = h;
+  *reinterpret_cast<h4*>(lo) = l;
+}
+
+constexpr int kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64;
+// For the smallest A its blocks are fewer than the waves: the summed index of A
+// is then shared by `splits` waves, whose sums meet in LDS.
+constexpr int small_splits(int kp) { return kp * kp / 256 >= kSmallWaves ? 1 : kSmallWaves / (kp * kp / 256); }
+constexpr int small_lds(int kp, int xp) {
+  return (2 * kp * xp + 2 * kp * small_pitch_s(kp)) * 2 + (small_splits(kp) > 1 ? small_splits(kp) * kp * kp * 4 : 0);
+}
+constexpr int kLdsBytes = 160 * 1024;
+
+// XP, the pitch of X, is fixed so that a wave's addresses in X are few registers
+// and constants.
+template <int KP, int XP>
+__global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(SmallNs g) {
+  extern __shared__ __align__(16) half_t lds[];
+  const int lp = g.lp;
+  constexpr int sp = small_pitch_s(KP), kSplits = small_splits(KP);
+  half_t *xh = lds, *xl = xh + KP * XP, *sh = xl + KP * XP, *sl = sh + KP * sp;
+  double* part = reinterpret_cast<double*>(sh);   // before A is
+  float* sums = reinterpret_cast<float*>(sl + KP * sp);
+  const int wave = threadIdx.x >> 6;
+  int lane = threadIdx.x & 63;
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * g.in.mat;
+
+  const int per_row = (g.in.cols + 7) >> 3, groups = g.in.rows * per_row;
+  constexpr int kGroups = (KP * XP / 8 + kSmallThreads - 1) / kSmallThreads;   // of 8 input values
+  f8 v[kGroups];
+  double sum = 0.0;
+#pragma unroll
+  for (int n = 0; n < kGroups; ++n) {
+    const int i = threadIdx.x + n * kSmallThreads;
+    v[n] = f8{};
+    if (i < groups) {
+      const int r = i / per_row;
+      v[n] = load8(g.in, base + r * g.in.row, (i - r * per_row) * 8);
+    }
+  }
+  for (int i = threadIdx.x; i < KP * XP; i += kSmallThreads) reinterpret_cast<uint32_t*>(xh)[i] = 0;   // hi and lo
+#pragma unroll
+  for (int n = 0; n < kGroups; ++n)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sum += static_cast<double>(v[n][q]) * static_cast<double>(v[n][q]);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
+  if (lane == 0) part[wave] = sum;
+  __syncthreads();
+  sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < kSmallWaves; ++i) sum += part[i];
+  // a zero matrix stays zero, a sum that is not finite makes everything NaN
+  double mult = 0.0;
+  float add = 0.0f;
+  if (sum > 0.0 && sum < __builtin_huge_val())
+    mult = static_cast<double>(kScaleX) / sqrt(sum);
+  else if (sum != 0.0)
+    add = __builtin_nanf("");
+#pragma unroll
+  for (int n = 0; n < kGroups; ++n) {
+    const int i = threadIdx.x + n * kSmallThreads;
+    if (i < groups) {
+      const int r = i / per_row, c = (i - r * per_row) * 8;
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (c + q < g.in.cols) {
+          const int at = g.tall ? x_at<XP>(c + q, r) : x_at<XP>(r, c + q);
+          split(static_cast<float>(static_cast<double>(v[n][q]) * mult) + add, xh + at, xl + at);
+        }
+    }
+  }
+  __syncthreads();
+
+  constexpr int kSide = KP / 16, kBlocks = kSide * kSide, kMine = (kBlocks + kSmallWaves - 1) / kSmallWaves;
+  for (int t = 0; t < g.steps; ++t) {
+    const float a = g.coefs[3 * t], b = g.coefs[3 * t + 1], c = g.coefs[3 * t + 2];
+    asm volatile("" : "+v"(lane));   // the LDS addresses are formed in every step: all of them do not fit the registers
+    const int lr = lane & 15, lk = (lane >> 4) * 8, lq = (lane >> 4) * 4;   // a fragment's row, its first k; a result's first row
+    // A = X X^T, the wave's blocks
+    acc4 am[kMine];
+    if constexpr (kSplits > 1) {
+      const int blk = wave % kBlocks, part_k = wave / kBlocks;
+      const int bi = blk / kSide * 16, bj = blk % kSide * 16;
+      Acc3 s;
+#pragma unroll 2
+      for (int k0 = part_k * 32 + lk; k0 < lp; k0 += kSplits * 32)
+        s.add(row8(xh, x_at<XP>(bi + lr, k0)), row8(xl, x_at<XP>(bi + lr, k0)), row8(xh, x_at<XP>(bj + lr, k0)),
+              row8(xl, x_at<XP>(bj + lr, k0)));
+      const acc4 w = s.sum();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sums[(part_k * KP + bi + lq + q) * KP + bj + lr] = w[q];
+      __syncthreads();
+      am[0] = acc4{0, 0, 0, 0};
+      if (wave < kBlocks)
+#pragma unroll
+        for (int n = 0; n < kSplits; ++n)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) am[0][q] += sums[(n * KP + bi + lq + q) * KP + bj + lr];
+    } else {
+#pragma unroll
+      for (int n = 0; n < kMine; ++n) {
+        const int blk = wave + n * kSmallWaves;
+        Acc3 s;
+        if (blk < kBlocks) {
+          const int bi = blk / kSide * 16 + lr, bj = blk % kSide * 16 + lr;
+#pragma unroll 2
+          for (int k0 = lk; k0 < lp; k0 += 32)
+            s.add(row8(xh, x_at<XP>(bi, k0)), row8(xl, x_at<XP>(bi, k0)), row8(xh, x_at<XP>(bj, k0)),
+                  row8(xl, x_at<XP>(bj, k0)));
+        }
+        am[n] = s.sum();
+        __builtin_amdgcn_sched_barrier(0);   // one block's fragments at a time: all of them do not fit the registers
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < kMine; ++n) {
+      const int blk = wave + n * kSmallWaves;
+      if (blk < kBlocks) {
+        // symmetric: the lane's four rows of a column are stored as four columns of a row
+        const int at = s_at<KP>(blk % kSide * 16 + lr, blk / kSide * 16 + lq);
+        am[n] *= kScaleA / (kScaleX * kScaleX);
+        split4(am[n], sh + at, sl + at);
+      }
+    }
+    __syncthreads();
+    // C = a I + b A + c A A
+    acc4 sq[kMine];
+#pragma unroll
+    for (int n = 0; n < kMine; ++n) {
+      const int blk = wave + n * kSmallWaves;
+      Acc3 s;
+      if (blk < kBlocks) {
+        const int bi = blk / kSide * 16 + lr, bj = blk % kSide * 16 + lr;
+#pragma unroll
+        for (int k0 = 0; k0 < KP; k0 += 32)
+          s.add(row8(sh, s_at<KP>(bi, k0 + lk)), row8(sl, s_at<KP>(bi, k0 + lk)), row8(sh, s_at<KP>(bj, k0 + lk)),
+                row8(sl, s_at<KP>(bj, k0 + lk)));
+      }
+      sq[n] = s.sum();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    __syncthreads();   // A is read
+#pragma unroll
+    for (int n = 0; n < kMine; ++n) {
+      const int blk = wave + n * kSmallWaves;
+      if (blk < kBlocks) {
+        const int r = blk % kSide * 16 + lr, col = blk / kSide * 16 + lq;
+        acc4 w = c * (kScaleC / (kScaleA * kScaleA)) * sq[n] + b * (kScaleC / kScaleA) * am[n];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (r == col + q && r < g.k) w[q] += a * kScaleC;
+        split4(w, sh + s_at<KP>(r, col), sl + s_at<KP>(r, col));
+      }
+    }
+    __syncthreads();
+    // X = C X in place: a wave reads a block of columns whole before it writes it
+    const bool last = t == g.steps - 1;
+#pragma unroll 1
+    for (int c0 = wave * 16; c0 < lp; c0 += kSmallWaves * 16) {
+      asm volatile("" : "+v"(lane)::"memory");   // nor C, which is read again for every block of columns
+      const int lr = lane & 15, lk = (lane >> 4) * 8, lq = (lane >> 4) * 4;
+      h8 ph[KP / 32], pl[KP / 32];
+#pragma unroll
+      for (int k0 = 0; k0 < KP / 32; ++k0) {
+        ph[k0] = column8<XP>(xh, k0 * 32, c0, lane);
+        pl[k0] = column8<XP>(xl, k0 * 32, c0, lane);
+      }
+#pragma unroll
+      for (int bi = 0; bi < kSide; ++bi) {
+        Acc3 s;
+#pragma unroll
+        for (int k0 = 0; k0 < KP / 32; ++k0) {
+          const int at = s_at<KP>(bi * 16 + lr, k0 * 32 + lk);
+          s.add(ph[k0], pl[k0], row8(sh, at), row8(sl, at));
+        }
+        acc4 w = s.sum();   // of X^T C: four columns of row bi * 16 + lr
+        const int r = bi * 16 + lr, col = c0 + lq;
+        if (!last) {
+          split4(w * (1.0f / kScaleC), xh + x_at<XP>(r, col), xl + x_at<XP>(r, col));
+        } else if (r < g.k) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (col + q < g.l)
+              g.out[blockIdx.x * g.out_mat + (g.tall ? (col + q) * g.out_row + r : r * g.out_row + col + q)] =
+                  bf16_rne(w[q] * (g.scale / (kScaleC * kScaleX)));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <int KP, int XP>
+hipError_t small_launch(const SmallNs& g, int64_t mats, hipStream_t s) {
+  constexpr int bytes = small_lds(KP, XP);
+  static_assert(bytes <= kLdsBytes, "fits the LDS");
+  hipLaunchKernelGGL((ns_small_kernel<KP, XP>), dim3(static_cast<unsigned>(mats)), dim3(kSmallThreads), bytes, s, g);
+  return hipGetLastError();
+}
+
+// The pitch of X in the small kernel for a k x l matrix, 0 if it is not small.
+constexpr int kPitches[3][2] = {{256, 1024}, {256, 512}, {128, 256}};
+int small_pitch(int64_t k, int64_t l) {
+  if (k > 96) return 0;
+  for (int xp : kPitches[(k - 1) / 32])
+    if (l <= xp) return xp;
+  return 0;
+}
+
+hipError_t launch_small(const NsParams& p, const NsInput& in, hipStream_t s) {
+  SmallNs g = {};
+  g.in = in;
+  g.out = p.out;
+  g.out_row = p.out_row;
+  g.out_mat = p.out_mat;
+  g.tall = p.rows > p.cols;
+  g.k = static_cast<int>(g.tall ? p.cols : p.rows);
+  g.l = static_cast<int>(g.tall ? p.rows : p.cols);
+  g.lp = (g.l + 31) / 32 * 32;
+  g.steps = p.steps;
+  g.scale = p.scale;
+  for (int i = 0; i < 3 * p.steps; ++i) g.coefs[i] = p.coefs[i];
+  const bool narrow = small_pitch(g.k, g.l) == kPitches[(g.k - 1) / 32][0];
+  switch ((g.k + 31) / 32) {
+    case 1: return narrow ? small_launch<32, kPitches[0][0]>(g, p.mats, s) : small_launch<32, kPitches[0][1]>(g, p.mats, s);
+    case 2: return narrow ? small_launch<64, kPitches[1][0]>(g, p.mats, s) : small_launch<64, kPitches[1][1]>(g, p.mats, s);
+    default: return narrow ? small_launch<96, kPitches[2][0]>(g, p.mats, s) : small_launch<96, kPitches[2][1]>(g, p.mats, s);
+  }
+}
+
 }  // namespace
 
 int64_t ns_workspace_bytes(int64_t mats, int64_t rows, int64_t cols) {
@@ -646,6 +990,10 @@ int64_t ns_workspace_bytes(int64_t mats, int64_t rows, int64_t cols) {
 }
 
 hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
+  NsInput in{p.in, p.in_row, p.in_mat, static_cast<int>(p.rows), static_cast<int>(p.cols), p.in_f32, 0};
+  const int64_t per16 = p.in_f32 ? 4 : 8;
+  in.vec = (reinterpret_cast<uintptr_t>(p.in) & 15u) == 0 && p.in_row % per16 == 0 && p.in_mat % per16 == 0;
+  if (small_pitch(p.rows < p.cols ? p.rows : p.cols, p.rows < p.cols ? p.cols : p.rows)) return launch_small(p, in, s);
   const Layout w(p.mats, p.rows, p.cols);
   char* ws = static_cast<char*>(p.workspace);
   const bool tall = p.rows > p.cols;
@@ -655,28 +1003,24 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
   half_t* xt[2] = {reinterpret_cast<half_t*>(ws + w.xt[0]), reinterpret_cast<half_t*>(ws + w.xt[1])};
   half_t* sq[3] = {reinterpret_cast<half_t*>(ws + w.sq[0]), reinterpret_cast<half_t*>(ws + w.sq[1]),
                    reinterpret_cast<half_t*>(ws + w.sq[2])};
-  NsScale* scales = reinterpret_cast<NsScale*>(ws + w.scales);
+  float* f = reinterpret_cast<float*>(ws + w.f);
   half_t* e = reinterpret_cast<half_t*>(ws + w.e);
   const int64_t x_mat = w.k * w.lp, xt_mat = w.l * w.kp, sq_mat = w.k * w.kp;
 
-  NsInput in{p.in, p.in_row, p.in_mat, static_cast<int>(p.rows), static_cast<int>(p.cols), p.in_f32, 0};
-  const int64_t per16 = p.in_f32 ? 4 : 8;
-  in.vec = (reinterpret_cast<uintptr_t>(p.in) & 15u) == 0 && p.in_row % per16 == 0 && p.in_mat % per16 == 0;
   double* partials = reinterpret_cast<double*>(ws + w.partials);
   const int64_t rows4 = (p.rows + kNormThreads / 64 - 1) / (kNormThreads / 64);
   const int parts = static_cast<int>(rows4 < kNormParts ? rows4 : kNormParts);
   hipLaunchKernelGGL(ns_norm_kernel, dim3(parts, static_cast<unsigned>(p.mats)), dim3(kNormThreads), 0, s, in, partials);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(ns_scale_kernel, dim3(static_cast<unsigned>(p.mats)), dim3(kNormThreads), 0, s, partials, parts, scales);
-  err = hipGetLastError();
-  if (err != hipSuccess) return err;
   NsX nx;
   nx.same = tall ? xt[0] : x;
   nx.turned = tall ? x : xt[0];
   nx.same_mat = tall ? xt_mat : x_mat;
   nx.turned_mat = tall ? x_mat : xt_mat;
-  nx.scales = scales;
+  nx.partials = partials;
+  nx.parts = parts;
+  nx.f = f;
   hipLaunchKernelGGL(ns_prepare_kernel,
                      dim3(static_cast<unsigned>(pad_up(p.cols) / kTurn), static_cast<unsigned>(pad_up(p.rows) / kTurn),
                           static_cast<unsigned>(p.mats)),
@@ -700,7 +1044,8 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
     g.add = add;
     g.beta = beta;
     g.diag = diag;
-    return sym ? product<true>(g, p.mats, s) : product<false>(g, p.mats, s);
+    if (add) return product<true, kPoly>(g, p.mats, s);
+    return sym ? product<true, kPlain>(g, p.mats, s) : product<false, kPlain>(g, p.mats, s);
   };
   auto poly = [&](const half_t* a, half_t* d, int t) {
     const float* c = p.coefs + 3 * t;
@@ -719,16 +1064,15 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
     g.d_mat = g.dt_mat = sq_mat;
     g.d_ld = g.dt_ld = kp;
     g.alpha = kScaleA / (kScaleX * kScaleX);
-    g.scales = first ? scales : nullptr;
+    g.f = first ? f : nullptr;
     g.f_pow = 2;
-    return product<true>(g, p.mats, s);
+    return product<true, kPlain>(g, p.mats, s);
   };
   // X = C X from the transposed copy xt[from]: into x and xt[to], the last
   // step's into the output.
-  enum { kCarryOut = 1, kCarryIn = 2 };
-  auto apply = [&](const half_t* c, float c_scale, int from, bool first, int to, bool last, int carry) {
+  auto apply = [&](const half_t* c, float c_scale, int from, bool first, int to, bool last, Epilogue carry) {
     Product g = {};
-    g.scales = first ? scales : nullptr;
+    g.f = first ? f : nullptr;
     g.f_pow = 1;
     g.kk = kp;
     const bool turned = last && tall;   // the result's own orientation
@@ -754,10 +1098,13 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
       g.dt_mat = xt_mat;
       g.dt_ld = kp;
     }
-    g.carry_out = carry == kCarryOut ? e : nullptr;
-    g.carry_in = carry == kCarryIn ? e : nullptr;
+    g.carry_out = e;
+    g.carry_in = e;
     g.carry_mat = w.e_mat;
-    return product<false>(g, p.mats, s);
+    if (last) return product<false, kOut>(g, p.mats, s);
+    if (carry == kCarryOut) return product<false, kCarryOut>(g, p.mats, s);
+    if (carry == kCarryIn) return product<false, kCarryIn>(g, p.mats, s);
+    return product<false, kPlain>(g, p.mats, s);
   };
 
   // Every launch in order, until one fails.
@@ -784,7 +1131,7 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
   if (p.steps == 1) {
     run([&] { return gram(sq[0], true); });
     run([&] { return poly(sq[0], sq[1], 0); });
-    run([&] { return apply(sq[1], kScaleC, 0, true, 1, true, 0); });
+    run([&] { return apply(sq[1], kScaleC, 0, true, 1, true, kPlain); });
     return st;
   }
   // The first two steps together: X is still exact, and the second step's X
@@ -793,7 +1140,7 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
   t = 2;
   // X after two steps: its rounding errors are carried into the next product.
   const bool carries = p.steps >= 4 && !(wide && p.steps == 4);
-  run([&] { return apply(sq[0], kScaleQ, 0, true, 1, t == p.steps, carries ? kCarryOut : 0); });
+  run([&] { return apply(sq[0], kScaleQ, 0, true, 1, t == p.steps, carries ? kCarryOut : kPlain); });
   cur = 1;
   while (t < p.steps) {
     // The last two together where X is long: one product with X less for two
@@ -801,9 +1148,9 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
     if (wide && p.steps - t == 2) {
       pair(t, false);
       t += 2;
-      run([&] { return apply(sq[0], kScaleQ, cur, false, cur ^ 1, true, 0); });
+      run([&] { return apply(sq[0], kScaleQ, cur, false, cur ^ 1, true, kPlain); });
     } else {
-      const int carry = carries && t == 2 ? kCarryIn : 0;
+      const Epilogue carry = carries && t == 2 ? kCarryIn : kPlain;
       run([&] { return gram(sq[0], false); });
       run([&] { return poly(sq[0], sq[1], t); });
       ++t;
