@@ -19,11 +19,14 @@ from ._lib import AdamHparams, MuonHparams, check, load
 _BF16_LIKE = (torch.bfloat16, torch.int16, torch.uint16)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None)   # without torch.cuda's check that the runtime is up
+
+
 def _stream(stream) -> int:
     if stream is None:
         # the handle itself: building a torch.cuda.Stream object takes 2.7 us, a
         # third of a small call
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -32,10 +35,9 @@ def _stream(stream) -> int:
 def _dev(t: torch.Tensor, what: str, dtypes) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: expected a torch.Tensor")
-    d = t.get_device() if t.is_cuda else -1
-    if d < 0:
+    if not t.is_cuda:
         raise ValueError(f"{what}: must be a device tensor, got {t.device}")
-    if d != torch.cuda.current_device():
+    if t.get_device() != _current_device():   # a device tensor: the runtime is up
         raise ValueError(f"{what}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
     if t.dtype not in dtypes:
         raise TypeError(f"{what}: dtype {t.dtype} not in {dtypes}")
@@ -357,7 +359,7 @@ def zero_muon_momentum(momentum: torch.Tensor, direction_out: torch.Tensor, grad
     n = momentum.numel()
     ptrs = [_dev(momentum, "momentum", (torch.float32,)), _dev(direction_out, "direction_out", _BF16_LIKE),
             _dev(grad, "grad", (torch.float32,))]
-    if any(t.numel() != n for t in (direction_out, grad)):
+    if direction_out.numel() != n or grad.numel() != n:
         raise ValueError("zero_muon_momentum: all buffers must have the same numel")
     h = muon_hparams(hp)
     check(load().zero_muon_momentum(*ptrs, _one_float(grad_scale, "grad_scale"), n, C.byref(h), _stream(stream)),
@@ -448,7 +450,7 @@ def zero_muon_shard_step(master: torch.Tensor, bf16_out: torch.Tensor, update: t
     n = master.numel()
     ptrs = [_dev(master, "master", (torch.float32,)), _dev(bf16_out, "bf16_out", _BF16_LIKE),
             _dev(update, "update", _BF16_LIKE)]
-    if any(t.numel() != n for t in (bf16_out, update)):
+    if bf16_out.numel() != n or update.numel() != n:
         raise ValueError("zero_muon_shard_step: all buffers must have the same numel")
     h = muon_hparams(hp)
     check(load().zero_muon_shard_step(*ptrs, n, C.byref(h), _one_float(lr_dev, "lr_dev"), _stream(stream)),

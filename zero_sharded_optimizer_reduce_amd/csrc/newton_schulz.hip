@@ -31,6 +31,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "kernels.h"
 
@@ -214,6 +215,10 @@ __global__ __launch_bounds__(kNormThreads) void ns_prepare_kernel(NsInput g, NsX
 // ------------------------------------------------------------------ products
 // D = alpha' P Q^T with P m x kk, Q n x kk (pitches p_ld, q_ld; kk a multiple of
 // kPad, the padding zero).
+// kSym: a symmetric result, its tiles on and below the diagonal.  kRide: P = Q, and
+// the tiles on the diagonal ride: P's rows of diagonal tile i are those of tile
+// (i, i - 1), whose workgroup computes both.
+enum Shape { kFull, kSym, kRide };
 enum Epilogue { kPlain, kPoly, kCarryOut, kCarryIn, kOut };
 struct Product {
   const half_t* p;
@@ -256,20 +261,25 @@ template <int R, int NW>
 struct Stager {
   static constexpr int kN = R / 8 / NW;
   static_assert(kN * 8 * NW == R && kN % 2 == 0, "every wave moves the same number of pieces, an even one");
-  __amdgpu_buffer_rsrc_t rsrc;
-  int voff[2], step, wave;   // even and odd groups of 8 rows
-  __device__ __forceinline__ Stager(const half_t* mat, int ld, int row0, int wave_, int lane) : wave(wave_) {
-    rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<half_t*>(mat + static_cast<int64_t>(row0) * ld), 0, R * ld * 2,
-                                             0x00020000);
+  __amdgpu_buffer_rsrc_t rsrc, none;   // none: no bytes in range, a load through it reads nothing
+  int voff[2], step, wave, end;        // voff: even and odd groups of 8 rows
+  __device__ __forceinline__ Stager(const half_t* mat, int ld, int row0, int kk, int wave_, int lane)
+      : wave(wave_), end(kk) {
+    half_t* base = const_cast<half_t*>(mat + static_cast<int64_t>(row0) * ld);
+    rsrc = __builtin_amdgcn_make_buffer_rsrc(base, 0, R * ld * 2, 0x00020000);
+    none = __builtin_amdgcn_make_buffer_rsrc(base, 0, 0, 0x00020000);
     const int r = wave * kN * 8 + (lane >> 3);
     voff[0] = r * ld * 2 + ((lane & 7) ^ (lane >> 4)) * 16;
     voff[1] = voff[0] ^ 64;   // ld is a multiple of 64
     step = 8 * ld * 2;
   }
+  // A stage past the end is loaded too, so that the loads on their way can be
+  // counted, but from nowhere.
   __device__ __forceinline__ void one(half_t* lds, int k0, int i) const {
 #ifdef __HIP_DEVICE_COMPILE__   // the builtin is unknown to the host pass
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + (wave * kN + i) * 8 * kBk), 16, voff[i & 1],
-                                             k0 * 2 + i * step, 0, 0);
+    const bool live = k0 < end;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(live ? rsrc : none, (lds_void*)(lds + (wave * kN + i) * 8 * kBk), 16,
+                                             voff[i & 1], live ? k0 * 2 + i * step : 0, 0, 0);
 #endif
   }
   __device__ __forceinline__ void all(half_t* lds, int k0) const {
@@ -279,20 +289,24 @@ struct Stager {
 };
 
 // A wave's operands for half a stage: two 16-wide pieces of the summed index.
-template <int TM, int TN>
+// SECOND: the rows of P at the wave's columns too, for P P^T.
+template <int TM, int TN, bool SECOND>
 struct Frags {
-  static constexpr int kReads = 2 * (TM + TN);
-  h8 a[2][TM], b[2][TN];
-  // Read number n of kReads; at_p, at_q: the lane's byte offsets in a slot (see
-  // lane_at); half 0 or 1.
-  __device__ __forceinline__ void one(const half_t* p, const half_t* q, int at_p, int at_q, int half, int n) {
-    const int u = n / (TM + TN), i = n - u * (TM + TN);
+  static constexpr int kSets = TM + TN + (SECOND ? TN : 0), kReads = 2 * kSets;
+  h8 a[2][TM], b[2][TN], c[2][TN];
+  // Read number n of kReads; at_p, at_q, at_c: the lane's byte offsets in a slot
+  // (see lane_at); half 0 or 1.
+  __device__ __forceinline__ void one(const half_t* p, const half_t* q, int at_p, int at_q, int at_c, int half, int n) {
+    const int u = n / kSets, i = n - u * kSets, flip = half * 64 + u * 32;
+    auto read = [&](const half_t* m, int at, int block) {
+      return *reinterpret_cast<const h8*>(reinterpret_cast<const char*>(m) + (at ^ flip) + block * 32 * kBk * 2);
+    };
     if (i < TM)
-      a[u][i] = *reinterpret_cast<const h8*>(reinterpret_cast<const char*>(p) + (at_p ^ (half * 64 + u * 32)) +
-                                             i * 32 * kBk * 2);
+      a[u][i] = read(p, at_p, i);
+    else if (i < TM + TN)
+      b[u][i - TM] = read(q, at_q, i - TM);
     else
-      b[u][i - TM] = *reinterpret_cast<const h8*>(reinterpret_cast<const char*>(q) + (at_q ^ (half * 64 + u * 32)) +
-                                                  (i - TM) * 32 * kBk * 2);
+      c[u][i - TM - TN] = read(p, at_c, i - TM - TN);
   }
 };
 
@@ -344,6 +358,13 @@ __device__ __forceinline__ u32x4 column_piece(const uint16_t* m, int pitch, int 
   return transpose8(at, at + 4 * pitch);
 }
 
+// The first n of 8 values, the others zero.
+__device__ __forceinline__ u32x4 first(u32x4 v, int n) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = 2 * q + 1 < n ? v[q] : 2 * q < n ? v[q] & 0xFFFFu : 0u;
+  return v;
+}
+
 template <int NW>
 __device__ __forceinline__ float block_sum_f32(float x, float* part) {
 #pragma unroll
@@ -356,31 +377,54 @@ __device__ __forceinline__ float block_sum_f32(float x, float* part) {
   return t;
 }
 
-// One tile BM x BN by WR x WC waves.  SYM: lower tiles of a symmetric product.
+// One tile BM x BN by WR x WC waves.
 //
-// The loop over the summed index keeps one to one and a half stages on their
-// way to LDS and half a stage ahead in registers: while the matrix cores work
+// The loop over the summed index keeps one to one and a half stages (DEEP: four)
+// on their way to LDS and half a stage ahead in registers: while the matrix cores work
 // on one half the wave reads the next one's fragments, and the loads are issued
 // evenly between the products (a wave issues in order: loads in a row
 // hold its products up while the CU takes them in, about 26 clocks each).
-template <int BM, int BN, int WR, int WC, bool SYM, int EPI>
-__global__ __launch_bounds__(WR * WC * 64) void ns_product_kernel(Product g) {
+template <int BM, int BN, int WR, int WC, Shape SHAPE, Epilogue EPI, bool DEEP = false>
+__global__ __launch_bounds__(WR * WC * 64, BM <= 128 ? 2 : 1) void ns_product_kernel(Product g) {
   constexpr int NW = WR * WC;
   constexpr int TM = BM / WR / 32, TN = BN / WC / 32;   // 32 x 32 blocks of a wave
   constexpr int kSlot = (BM > BN ? BM : BN) * kBk;
-  // Five places for an operand's rows of one stage.  Separate arrays, so that
-  // the compiler can tell a load on its way into one from a read of another.
+  // Five places for an operand's rows of one stage, ten for the smallest tile: its
+  // stages are short, and four of them have to be on their way.  Separate arrays,
+  // so that the compiler can tell a load on its way into one from a read of another.
+  constexpr bool SYM = SHAPE != kFull;
   __shared__ __align__(16) half_t slot0[kSlot];
   __shared__ __align__(16) half_t slot1[kSlot];
   __shared__ __align__(16) half_t slot2[kSlot];
   __shared__ __align__(16) half_t slot3[kSlot];
   __shared__ __align__(16) half_t slot4[kSlot];
+  __shared__ __align__(16) half_t slot5[DEEP ? kSlot : 1];
+  __shared__ __align__(16) half_t slot6[DEEP ? kSlot : 1];
+  __shared__ __align__(16) half_t slot7[DEEP ? kSlot : 1];
+  __shared__ __align__(16) half_t slot8[DEEP ? kSlot : 1];
+  __shared__ __align__(16) half_t slot9[DEEP ? kSlot : 1];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int id = xcd_order(blockIdx.x, gridDim.x);
   const int mat = id / g.tiles;
   const int t = id - mat * g.tiles;
   int ti, tj;
-  if (SYM) {
+  bool rides = false;   // the tile of P P^T on the diagonal too
+  if (SHAPE == kRide) {
+    const int side = (g.m + BM - 1) / BM;
+    ti = static_cast<int>((sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
+    while (ti * (ti + 1) / 2 > t) --ti;
+    while ((ti + 1) * (ti + 2) / 2 <= t) ++ti;
+    tj = t - ti * (ti + 1) / 2;
+    rides = tj == ti++;
+    if (ti >= side) {                               // the only one on the diagonal, or of two the first
+      ti = tj = 0;
+      rides = false;
+    } else if (side > 2 && ti == side - 1 && tj == 0) {   // the first diagonal tile's place
+      ti = 0;
+      tj = side - 1;
+      rides = true;
+    }
+  } else if (SYM) {
     ti = static_cast<int>((sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
     while (ti * (ti + 1) / 2 > t) --ti;
     while ((ti + 1) * (ti + 2) / 2 <= t) ++ti;
@@ -390,68 +434,11 @@ __global__ __launch_bounds__(WR * WC * 64) void ns_product_kernel(Product g) {
     tj = t - ti * g.tiles_n;
   }
   const int row0 = ti * BM, col0 = tj * BN;
-  const Stager<BM, NW> sp(g.p + mat * g.p_mat, g.p_ld, row0, wave, lane);
-  const Stager<BN, NW> sq(g.q + mat * g.q_mat, g.q_ld, col0, wave, lane);
+  const Stager<BM, NW> sp(g.p + mat * g.p_mat, g.p_ld, row0, g.kk, wave, lane);
+  const Stager<BN, NW> sq(g.q + mat * g.q_mat, g.q_ld, col0, g.kk, wave, lane);
   const int wr = wave / WC, wc = wave - wr * WC;
   int at_p = lane_at(wr * (BM / WR), lane), at_q = lane_at(wc * (BN / WC), lane);
-  f16 acc[TM][TN] = {};
-  Frags<TM, TN> f0, f1;
   constexpr int kP = Stager<BM, NW>::kN, kQ = Stager<BN, NW>::kN;
-  constexpr int kProducts = 2 * TM * TN, kReads = Frags<TM, TN>::kReads;
-  auto past_end = [&](int k) { return k < g.kk ? k : g.kk - kBk; };   // the last stage again, never read
-  // Half a stage: the products of `now`, and between them, evenly, the reads of
-  // `then` and the loads of one operand.  The compiler keeps the groups apart.
-  auto half = [&](const auto& loads, int n_loads, const Frags<TM, TN>& now, Frags<TM, TN>& then, const half_t* p,
-                  const half_t* q, int which) {
-    // Addresses are formed anew: kept over the loop for every slot they would
-    // not fit the registers.
-    asm volatile("" : "+v"(at_p), "+v"(at_q));
-#pragma unroll
-    for (int s = 0; s < n_loads; ++s) {
-#pragma unroll
-      for (int k = s * kProducts / n_loads; k < (s + 1) * kProducts / n_loads; ++k) {
-        const int u = k / (TM * TN), i = (k - u * TM * TN) / TN, j = k % TN;
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(now.b[u][j], now.a[u][i], acc[i][j], 0, 0, 0);
-      }
-      loads(s);
-#pragma unroll
-      for (int k = s * kReads / n_loads; k < (s + 1) * kReads / n_loads; ++k) then.one(p, q, at_p, at_q, which, k);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  // One stage: P and Q rows in p0 and q0, the next stage's in p1 and q1; the
-  // stage after that goes to p2 and, once every wave has read this one, p0.
-  auto stage = [&](half_t* p0, half_t* q0, half_t* p1, half_t* q1, half_t* p2, int k0) {
-    const int k2 = past_end(k0 + 2 * kBk);
-    half([&](int s) { sp.one(p2, k2, s); }, kP, f0, f1, p0, q0, 1);
-    // the next stage has arrived (all but p2's loads), and this one is read
-    __builtin_amdgcn_s_waitcnt(wait_vm_lds(kP));
-    wave_barrier();
-    half([&](int s) { sq.one(p0, k2, s); }, kQ, f1, f0, p1, q1, 0);
-  };
-  sp.all(slot0, 0);
-  sq.all(slot1, 0);
-  sp.all(slot2, past_end(kBk));
-  sq.all(slot3, past_end(kBk));
-  __builtin_amdgcn_s_waitcnt(wait_vm(kP + kQ));
-  wave_barrier();
-#pragma unroll
-  for (int k = 0; k < kReads; ++k) f0.one(slot0, slot1, at_p, at_q, 0, k);
-  for (int k0 = 0;;) {
-    stage(slot0, slot1, slot2, slot3, slot4, k0);
-    if ((k0 += kBk) >= g.kk) break;
-    stage(slot2, slot3, slot4, slot0, slot1, k0);
-    if ((k0 += kBk) >= g.kk) break;
-    stage(slot4, slot0, slot1, slot2, slot3, k0);
-    if ((k0 += kBk) >= g.kk) break;
-    stage(slot1, slot2, slot3, slot4, slot0, k0);
-    if ((k0 += kBk) >= g.kk) break;
-    stage(slot3, slot4, slot0, slot1, slot2, k0);
-    if ((k0 += kBk) >= g.kk) break;
-  }
-  __builtin_amdgcn_s_waitcnt(wait_vm_lds(0));
-  wave_barrier();   // nothing is on its way into LDS any more
-
   // The lane's values of block (i, j): row lane & 31 of the block, columns 8 * u +
   // 4 * (lane >> 5) + q (the products take Q's fragment first).
   float alpha = g.alpha;
@@ -459,20 +446,13 @@ __global__ __launch_bounds__(WR * WC * 64) void ns_product_kernel(Product g) {
     const float f = g.f[mat];
     alpha *= g.f_pow == 2 ? f * f : f;
   }
-  float gain = 0.0f;
-  if constexpr (EPI == kCarryIn) {
-    const half_t* c = g.p + mat * g.p_mat;
-    float sum = 0.0f;
-    for (int i = threadIdx.x; i < g.m; i += NW * 64) sum += static_cast<float>(c[static_cast<int64_t>(i) * g.p_ld + i]);
-    gain = block_sum_f32<NW>(sum, reinterpret_cast<float*>(slot4)) * g.alpha / (static_cast<float>(g.m) * kScaleE);
-  }
   const int lm = lane & 31, ln = (lane >> 5) << 2;
-  const int wrow = row0 + wr * (BM / WR), wcol = col0 + wc * (BN / WC);
-  const bool edge = row0 + BM > g.m || col0 + BN > g.n;
   // Results pass through the wave's own part of LDS, kBand blocks of rows at a
   // time, so that they leave as rows of 16-byte pieces; the transpose is read
   // from there with transposing reads.  A wave's LDS operations are carried out
-  // in order, so no barrier is needed.
+  // in order, so no barrier is needed.  (Piece by piece, each read waited for
+  // before its store, and the diagonal's blocks mirrored in LDS first, a 128 tile's
+  // results took 4.7 us where they take 3.2, in 10.7 us for 1024 x 1024 x 1024.)
   constexpr int kBand = TM % 2 == 0 ? 2 : TM;
   constexpr int kRows = kBand * 32, kCols = TN * 32, kPitch = kCols + 8;
   constexpr int kPart = kSlot / (NW / 4);
@@ -482,169 +462,316 @@ __global__ __launch_bounds__(WR * WC * 64) void ns_product_kernel(Product g) {
                    (wave >> 2) * kPart;
   // A tile on the diagonal of a symmetric product: only what lies below the
   // diagonal of its 32 x 32 blocks is kept, as for the tiles.
-  const bool diagonal = SYM && ti == tj;
+  auto write = [&](const f16 (&acc)[TM][TN], int row0, int col0, float gain) {
+    const int wrow = row0 + wr * (BM / WR), wcol = col0 + wc * (BN / WC);
+    const bool diagonal = SYM && row0 == col0;
 #pragma unroll
-  for (int ib = 0; ib < TM; ib += kBand) {
-    const int64_t carry = mat * g.carry_mat + static_cast<int64_t>(t) * (BM * BN) + threadIdx.x * 4;
-    // what joins the products: all loads of the band before the first use
-    h4 more[kBand][TN][4];
-    if constexpr (EPI == kPoly || EPI == kCarryIn) {
+    for (int ib = 0; ib < TM; ib += kBand) {
+      const int64_t carry = mat * g.carry_mat + static_cast<int64_t>(t) * (BM * BN) + threadIdx.x * 4;
+      // what joins the products: all loads of the band before the first use
+      h4 more[kBand][TN][4];
+      if constexpr (EPI == kPoly || EPI == kCarryIn) {
+#pragma unroll
+        for (int i = 0; i < kBand; ++i)
+#pragma unroll
+          for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              if constexpr (EPI == kPoly) {
+                const int r = wrow + (ib + i) * 32 + lm, c = wcol + j * 32 + u * 8 + ln;
+                // past the edge: some other value, dropped below
+                more[i][j][u] = *reinterpret_cast<const h4*>(
+                    g.add + mat * g.d_mat + static_cast<int64_t>(r < g.m ? r : 0) * g.d_ld + (c < g.d_ld ? c : 0));
+              } else {
+                more[i][j][u] =
+                    *reinterpret_cast<const h4*>(g.carry_in + carry + (((ib + i) * TN + j) * 4 + u) * (NW * 256));
+              }
+            }
+      }
 #pragma unroll
       for (int i = 0; i < kBand; ++i)
 #pragma unroll
         for (int j = 0; j < TN; ++j)
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
+            float v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = acc[ib + i][j][u * 4 + q] * alpha;
             if constexpr (EPI == kPoly) {
-              const int r = wrow + (ib + i) * 32 + lm, c = wcol + j * 32 + u * 8 + ln;
-              // past the edge: some other value, dropped below
-              more[i][j][u] = *reinterpret_cast<const h4*>(
-                  g.add + mat * g.d_mat + static_cast<int64_t>(r < g.m ? r : 0) * g.d_ld + (c < g.d_ld ? c : 0));
+#pragma unroll
+              for (int q = 0; q < 4; ++q) v[q] += g.beta * static_cast<float>(more[i][j][u][q]);
+              if (i == j && diagonal && wr == wc) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  if (lm == u * 8 + ln + q) v[q] += g.diag;
+              }
+            }
+            if constexpr (EPI == kCarryIn) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) v[q] += gain * static_cast<float>(more[i][j][u][q]);
+            }
+            u16x4 o;
+            if constexpr (EPI == kOut) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) o[q] = bf16_rne(v[q]);
             } else {
-              more[i][j][u] =
-                  *reinterpret_cast<const h4*>(g.carry_in + carry + (((ib + i) * TN + j) * 4 + u) * (NW * 256));
+              h4 h;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) h[q] = static_cast<half_t>(v[q]);
+              o = __builtin_bit_cast(u16x4, h);
+              if constexpr (EPI == kCarryOut) {
+                h4 w;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) w[q] = static_cast<half_t>((v[q] - static_cast<float>(h[q])) * kScaleE);
+                *reinterpret_cast<h4*>(g.carry_out + carry + (((ib + i) * TN + j) * 4 + u) * (NW * 256)) = w;
+              }
+            }
+            *reinterpret_cast<u16x4*>(mine + (i * 32 + lm) * kPitch + j * 32 + u * 8 + ln) = o;
+          }
+      static_assert(!SYM || (kBand == TM && TM == TN && WR == WC), "the diagonal's blocks are (i, i)");
+      // Out, kStep pieces at a time: all reads of LDS before the first store.
+      constexpr int kPieces = kRows * kCols / 512, kStep = kPieces % 8 == 0 ? 8 : kPieces % 6 == 0 ? 6 : kPieces;
+      const int brow = wrow + ib * 32;
+      if constexpr (EPI == kOut) {
+        uint16_t* out = g.out + mat * g.out_mat + static_cast<int64_t>(brow) * g.out_row + wcol;
+#pragma unroll 1
+        for (int k0 = 0; k0 < kPieces; k0 += kStep) {
+          u32x4 piece[kStep];
+#pragma unroll
+          for (int k = 0; k < kStep; ++k) {
+            const int at = (k0 + k) * 64 + lane, r = at / (kCols / 8), c = (at - r * (kCols / 8)) * 8;
+            piece[k] = *reinterpret_cast<const u32x4*>(mine + r * kPitch + c);
+          }
+#pragma unroll
+          for (int k = 0; k < kStep; ++k) {
+            const int at = (k0 + k) * 64 + lane, r = at / (kCols / 8), c = (at - r * (kCols / 8)) * 8;
+            uint16_t* dst = out + r * g.out_row + c;
+            if (brow + r >= g.m) continue;
+            if (g.out_vec && wcol + c + 8 <= g.n) {
+              *reinterpret_cast<u32x4*>(dst) = piece[k];
+            } else {
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                if (wcol + c + q < g.n) dst[q] = static_cast<uint16_t>(piece[k][q >> 1] >> ((q & 1) * 16));
             }
           }
-    }
-#pragma unroll
-    for (int i = 0; i < kBand; ++i)
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int r = wrow + (ib + i) * 32 + lm, c = wcol + j * 32 + u * 8 + ln;
-          float v[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = acc[ib + i][j][u * 4 + q] * alpha;
-          if constexpr (EPI == kPoly) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              v[q] += g.beta * static_cast<float>(more[i][j][u][q]);
-              if (diagonal && r == c + q) v[q] += g.diag;
-            }
-          }
-          if constexpr (EPI == kCarryIn) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] += gain * static_cast<float>(more[i][j][u][q]);
-          }
-          if (edge) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (r >= g.m || c + q >= g.n) v[q] = 0.0f;
-          }
-          u16x4 o;
-          if constexpr (EPI == kOut) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) o[q] = bf16_rne(v[q]);
-          } else {
-            h4 h;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) h[q] = static_cast<half_t>(v[q]);
-            o = __builtin_bit_cast(u16x4, h);
-            if constexpr (EPI == kCarryOut) {
-              h4 w;
-#pragma unroll
-              for (int q = 0; q < 4; ++q) w[q] = static_cast<half_t>((v[q] - static_cast<float>(h[q])) * kScaleE);
-              *reinterpret_cast<h4*>(g.carry_out + carry + (((ib + i) * TN + j) * 4 + u) * (NW * 256)) = w;
-            }
-          }
-          *reinterpret_cast<u16x4*>(mine + (i * 32 + lm) * kPitch + j * 32 + u * 8 + ln) = o;
         }
-    if (diagonal) {
-#pragma unroll
-      for (int i = 0; i < kBand; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-          if (wrow + (ib + i) * 32 == wcol + j * 32) {   // a block on the diagonal: its upper half from the lower
-#pragma unroll
-            for (int u = 0; u < 16; ++u) {
-              const int c = (u >> 2) * 8 + ln + (u & 3);
-              const uint16_t low = mine[(i * 32 + c) * kPitch + j * 32 + lm];
-              if (c > lm) mine[(i * 32 + lm) * kPitch + j * 32 + c] = low;
-            }
-          }
-    }
-#pragma unroll
-    for (int k = 0; k < kRows * kCols / 512; ++k) {
-      const int at = k * 64 + lane;
-      const int lrow = at / (kCols / 8), lcol = (at - lrow * (kCols / 8)) * 8;
-      const int r = wrow + ib * 32 + lrow, c = wcol + lcol;
-      const u32x4 piece = *reinterpret_cast<const u32x4*>(mine + lrow * kPitch + lcol);
-      if (r >= g.m || (diagonal && (c >> 5) > (r >> 5))) continue;
-      if constexpr (EPI != kOut) {
-        if (c < g.d_ld) *reinterpret_cast<u32x4*>(g.d + mat * g.d_mat + static_cast<int64_t>(r) * g.d_ld + c) = piece;
       } else {
-        uint16_t* dst = g.out + mat * g.out_mat + static_cast<int64_t>(r) * g.out_row + c;
-        if (g.out_vec && c + 8 <= g.n) {
-          *reinterpret_cast<u32x4*>(dst) = piece;
-        } else {
+        half_t* d = g.d + mat * g.d_mat + static_cast<int64_t>(brow) * g.d_ld + wcol;
+#pragma unroll 1
+        for (int k0 = 0; k0 < kPieces; k0 += kStep) {
+          u32x4 piece[kStep];
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            if (c + q < g.n) dst[q] = static_cast<uint16_t>(piece[q >> 1] >> ((q & 1) * 16));
+          for (int k = 0; k < kStep; ++k) {
+            const int at = (k0 + k) * 64 + lane, r = at / (kCols / 8), c = (at - r * (kCols / 8)) * 8;
+            piece[k] = *reinterpret_cast<const u32x4*>(mine + r * kPitch + c);
+          }
+#pragma unroll
+          for (int k = 0; k < kStep; ++k) {
+            const int at = (k0 + k) * 64 + lane, r = at / (kCols / 8), c = (at - r * (kCols / 8)) * 8;
+            if (wcol + c + 8 > g.n) piece[k] = first(piece[k], g.n - wcol - c);
+            if (brow + r < g.m && wcol + c < g.d_ld && !(diagonal && (wcol + c) >> 5 >= (brow + r) >> 5))
+              *reinterpret_cast<u32x4*>(d + r * g.d_ld + c) = piece[k];
+          }
+        }
+        if (g.dt) {
+          half_t* dt = g.dt + mat * g.dt_mat + static_cast<int64_t>(wcol) * g.dt_ld + brow;
+#pragma unroll 1
+          for (int k0 = 0; k0 < kPieces; k0 += kStep) {
+            // 16 columns, 8 rows of each 8 * (lane >> 4) rows on
+            u32x4 piece[kStep];
+#pragma unroll
+            for (int k = 0; k < kStep; ++k)
+              piece[k] = column_piece(mine, kPitch, (k0 + k) % kBand * 32, (k0 + k) / kBand * 16, lane);
+            if (diagonal && wr == wc) {   // in a block on the diagonal the upper half comes from the lower
+#pragma unroll
+              for (int k = 0; k < kStep; ++k) {
+                const int c = (k0 + k) / kBand * 16 + (lane & 15), r = (k0 + k) % kBand * 32 + (lane >> 4) * 8;
+                const u32x4 row = *reinterpret_cast<const u32x4*>(mine + c * kPitch + r);
+                if (c >> 5 == r >> 5) {
+                  const u32x4 low = first(row, c - r);
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) {
+                    const uint32_t keep = (r + 2 * q >= c ? 0xFFFFu : 0u) | (r + 2 * q + 1 >= c ? 0xFFFF0000u : 0u);
+                    piece[k][q] = (piece[k][q] & keep) | low[q];
+                  }
+                }
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < kStep; ++k) {
+              const int c = (k0 + k) / kBand * 16 + (lane & 15), r = (k0 + k) % kBand * 32 + (lane >> 4) * 8;
+              if (brow + r + 8 > g.m) piece[k] = first(piece[k], g.m - brow - r);
+              if (wcol + c < g.n && brow + r < g.dt_ld && !(diagonal && (wcol + c) >> 5 > (brow + r) >> 5))
+                *reinterpret_cast<u32x4*>(dt + c * g.dt_ld + r) = piece[k];
+            }
+          }
         }
       }
     }
-    if constexpr (EPI != kOut) {
-      if (g.dt) {
+  };
+
+  // The whole tile; every wave has the same loads and barriers.
+  auto tile = [&](auto second) {
+    constexpr bool SECOND = decltype(second)::value;
+    using Set = Frags<TM, TN, SECOND>;
+    constexpr int kProducts = 2 * TM * TN, kReads = Set::kReads;
+    Set f0, f1;
+    f16 acc[TM][TN] = {}, acc2[TM][TN] = {};
+    int at_c = at_p - wr * (BM / WR) * kBk * 2 + wc * (BN / WC) * kBk * 2;
+    // Half a stage: the products of `now`, and between them, evenly, the reads of
+    // `then` and the loads of one operand.  The compiler keeps the groups apart.
+    auto half = [&](const auto& loads, int n_loads, const Set& now, Set& then, const half_t* p, const half_t* q,
+                    int which) {
+      // Addresses are formed anew: kept over the loop for every slot they would
+      // not fit the registers.
+      asm volatile("" : "+v"(at_p), "+v"(at_q), "+v"(at_c));
 #pragma unroll
-        for (int k = 0; k < kRows * kCols / 512; ++k) {
-          // 16 columns, 8 rows of each 8 * (lane >> 4) rows on
-          const int lrow = k % kBand * 32, lcol = k / kBand * 16;
-          const u32x4 piece = column_piece(mine, kPitch, lrow, lcol, lane);
-          const int c = wcol + lcol + (lane & 15), r = wrow + ib * 32 + lrow + (lane >> 4) * 8;
-          if (c < g.n && r < g.dt_ld && !(diagonal && (c >> 5) >= (r >> 5)))
-            *reinterpret_cast<u32x4*>(g.dt + mat * g.dt_mat + static_cast<int64_t>(c) * g.dt_ld + r) = piece;
+      for (int s = 0; s < n_loads; ++s) {
+#pragma unroll
+        for (int k = s * kProducts / n_loads; k < (s + 1) * kProducts / n_loads; ++k) {
+          const int u = k / (TM * TN), i = (k - u * TM * TN) / TN, j = k % TN;
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(now.b[u][j], now.a[u][i], acc[i][j], 0, 0, 0);
+          if constexpr (SECOND)
+            acc2[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(now.c[u][j], now.a[u][i], acc2[i][j], 0, 0, 0);
         }
+        loads(s);
+#pragma unroll
+        for (int k = s * kReads / n_loads; k < (s + 1) * kReads / n_loads; ++k) then.one(p, q, at_p, at_q, at_c, which, k);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    int k0 = 0;
+    if constexpr (DEEP) {
+      // One stage: its rows in p0 and q0, the next one's in p1 and q1; Q of four
+      // stages on goes where the last stage's was, P of five stages on, once every
+      // wave has read this one, to p0.
+      auto stage = [&](half_t* p0, half_t* q0, half_t* p1, half_t* q1, half_t* q4) {
+        half([&](int s) { sq.one(q4, k0 + 4 * kBk, s); }, kQ, f0, f1, p0, q0, 1);
+        __builtin_amdgcn_s_waitcnt(wait_vm_lds(3 * (kP + kQ)));   // the next stage has arrived, and this one is read
+        wave_barrier();
+        half([&](int s) { sp.one(p0, k0 + 5 * kBk, s); }, kP, f1, f0, p1, q1, 0);
+        return (k0 += kBk) < g.kk;
+      };
+      sp.all(slot0, 0);
+      sq.all(slot5, 0);
+      sp.all(slot1, kBk);
+      sq.all(slot6, kBk);
+      sp.all(slot2, 2 * kBk);
+      sq.all(slot7, 2 * kBk);
+      sp.all(slot3, 3 * kBk);
+      sq.all(slot8, 3 * kBk);
+      sp.all(slot4, 4 * kBk);
+      __builtin_amdgcn_s_waitcnt(wait_vm(4 * kP + 3 * kQ));
+      wave_barrier();
+#pragma unroll
+      for (int k = 0; k < kReads; ++k) f0.one(slot0, slot5, at_p, at_q, at_c, 0, k);
+      while (stage(slot0, slot5, slot1, slot6, slot9) && stage(slot1, slot6, slot2, slot7, slot5) &&
+             stage(slot2, slot7, slot3, slot8, slot6) && stage(slot3, slot8, slot4, slot9, slot7) &&
+             stage(slot4, slot9, slot0, slot5, slot8)) {
+      }
+    } else {
+      // One stage: P and Q rows in p0 and q0, the next stage's in p1 and q1; the
+      // stage after that goes to p2 and, once every wave has read this one, p0.
+      auto stage = [&](half_t* p0, half_t* q0, half_t* p1, half_t* q1, half_t* p2) {
+        half([&](int s) { sp.one(p2, k0 + 2 * kBk, s); }, kP, f0, f1, p0, q0, 1);
+        // the next stage has arrived (all but p2's loads), and this one is read
+        __builtin_amdgcn_s_waitcnt(wait_vm_lds(kP));
+        wave_barrier();
+        half([&](int s) { sq.one(p0, k0 + 2 * kBk, s); }, kQ, f1, f0, p1, q1, 0);
+        return (k0 += kBk) < g.kk;
+      };
+      sp.all(slot0, 0);
+      sq.all(slot1, 0);
+      sp.all(slot2, kBk);
+      sq.all(slot3, kBk);
+      __builtin_amdgcn_s_waitcnt(wait_vm(kP + kQ));
+      wave_barrier();
+#pragma unroll
+      for (int k = 0; k < kReads; ++k) f0.one(slot0, slot1, at_p, at_q, at_c, 0, k);
+      while (stage(slot0, slot1, slot2, slot3, slot4) && stage(slot2, slot3, slot4, slot0, slot1) &&
+             stage(slot4, slot0, slot1, slot2, slot3) && stage(slot1, slot2, slot3, slot4, slot0) &&
+             stage(slot3, slot4, slot0, slot1, slot2)) {
       }
     }
-  }
-  if constexpr (EPI != kOut) {
-    // The padding past the last tile, as zeros.
-    if (col0 + BN >= g.n)
-      for (int c = col0 + BN + lane; c < g.d_ld; c += 64)
-        for (int r = row0 + wave; r < g.m && r < row0 + BM; r += NW)
-          g.d[mat * g.d_mat + static_cast<int64_t>(r) * g.d_ld + c] = 0;
-    if (g.dt && row0 + BM >= g.m)
-      for (int r = row0 + BM + lane; r < g.dt_ld; r += 64)
-        for (int c = col0 + wave; c < g.n && c < col0 + BN; c += NW)
-          g.dt[mat * g.dt_mat + static_cast<int64_t>(c) * g.dt_ld + r] = 0;
+    __builtin_amdgcn_s_waitcnt(wait_vm_lds(0));
+    wave_barrier();   // nothing is on its way into LDS any more
+    float gain = 0.0f;
+    if constexpr (EPI == kCarryIn) {
+      const half_t* c = g.p + mat * g.p_mat;
+      float sum = 0.0f;
+      for (int i = threadIdx.x; i < g.m; i += NW * 64) sum += static_cast<float>(c[static_cast<int64_t>(i) * g.p_ld + i]);
+      gain = block_sum_f32<NW>(sum, reinterpret_cast<float*>(slot4)) * g.alpha / (static_cast<float>(g.m) * kScaleE);
+    }
+    write(acc, row0, col0, gain);
+    if constexpr (SECOND) write(acc2, row0, row0, gain);
+  };
+  const bool second = rides && wr >= wc;   // above the diagonal nothing is kept
+  if constexpr (SHAPE == kRide) {
+    if (second)
+      tile(std::true_type());
+    else
+      tile(std::false_type());
+  } else {
+    tile(std::false_type());
   }
 }
 
 // ------------------------------------------------------------------ launches
-template <int BM, int BN, int WR, int WC, bool SYM, int EPI>
+// Workgroups per matrix.
+int64_t tile_count(const Product& g, int side, Shape shape) {
+  const int64_t tm = (g.m + side - 1) / side, tn = (g.n + side - 1) / side;
+  if (shape == kFull) return tm * tn;
+  return shape == kSym ? tm * (tm + 1) / 2 : tm > 2 ? tm * (tm - 1) / 2 : tm;
+}
+
+template <int BM, int BN, int WR, int WC, Shape SHAPE, Epilogue EPI, bool DEEP = false>
 hipError_t product_tiles(Product g, int64_t mats, hipStream_t s) {
-  const int tm = (g.m + BM - 1) / BM;
   g.tiles_n = (g.n + BN - 1) / BN;
-  g.tiles = SYM ? tm * (tm + 1) / 2 : tm * g.tiles_n;
-  hipLaunchKernelGGL((ns_product_kernel<BM, BN, WR, WC, SYM, EPI>), dim3(static_cast<unsigned>(g.tiles * mats)),
+  g.tiles = static_cast<int>(tile_count(g, BM, SHAPE));
+  hipLaunchKernelGGL((ns_product_kernel<BM, BN, WR, WC, SHAPE, EPI, DEEP>), dim3(static_cast<unsigned>(g.tiles * mats)),
                      dim3(WR * WC * 64), 0, s, g);
   return hipGetLastError();
 }
 
-// The tile for a product, by its modelled time: rounds of one tile per CU, each
-// proportional to the summed index (us at 4096) and a fixed part, fitted to
-// launches at k = 128 to 4096 on MI355X.  Both sides of a choice, measured: a
-// symmetric 4096 x 4096 x 4096 product takes 82 us with 253 tiles of 192 and
-// 105 with 528 of 128; of 512 x 512 x 512, 32 at once, 22 and 17; of 777 x 777 x
-// 832, three at once, 18 with 192, 12 with 128 and 8 with 64.  A full 4096 x 4096
-// x 4096 product 131 with 256 and 157 with 128; 1024 x 4096 x 1024, two at once,
-// 31 and 27.
-template <bool SYM, int EPI>
+// The tile for a product, by its modelled time: rounds of 256 tiles, one per CU,
+// each with a part proportional to the summed index (us at 4096) and a fixed one,
+// and the launch's own; fitted to launches at k = 256 to 4096 on MI355X.  Both
+// sides of some choices, measured: a symmetric 4096 x 4096 x 4096 product takes
+// 80 us with 253 tiles of 192 and 108 with 528 of 128; of 512 x 512 x 512, 32 at
+// once, 21 with 192, 15 with 128 and 18 with 64; of 777 x 777 x 832, three at
+// once, 19, 13 and 10.  A full 4096 x 4096 x 4096 product 126 with 256 and 161 with
+// 128; 1024 x 4096 x 1024, two at once, 33 and 28.
+template <Shape SHAPE, Epilogue EPI>
 hipError_t product(const Product& g, int64_t mats, hipStream_t s) {
-  auto time = [&](int side, double us, double fixed) {
-    const int64_t tm = (g.m + side - 1) / side, tn = (g.n + side - 1) / side;
-    const int64_t tiles = (SYM ? tm * (tm + 1) / 2 : tm * tn) * mats;
-    return static_cast<double>((tiles + 255) / 256) * (us * g.kk / 4096.0 + fixed);
+  constexpr Shape kOwn = SHAPE == kRide ? kSym : SHAPE;
+  auto time = [&](int side, double us, double fixed, double launch) {
+    return static_cast<double>((tile_count(g, side, kOwn) * mats + 255) / 256) * (us * g.kk / 4096.0 + fixed) + launch;
   };
-  const double large = SYM ? time(192, 72.0, 12.0) : time(256, 118.0, 10.0);
-  const double t128 = time(128, 36.0, 4.5), t64 = time(64, 14.5, 2.0);
-  if (t64 <= t128 && t64 <= large) return product_tiles<64, 64, 2, 2, SYM, EPI>(g, mats, s);
-  if (t128 <= large) return product_tiles<128, 128, 2, 2, SYM, EPI>(g, mats, s);
-  if constexpr (SYM)
-    return product_tiles<192, 192, 2, 2, SYM, EPI>(g, mats, s);
+  const double large = SHAPE != kFull ? time(192, 66.0, 11.0, 2.0) : time(256, 115.0, 11.0, 2.0);
+  const double t128 = time(128, 32.0, 3.0, 3.0), t64 = time(64, 14.0, 1.6, 1.5);
+  if (t64 <= t128 && t64 <= large) {
+    if constexpr (SHAPE == kRide) {
+      // The tiles on the diagonal ride where that saves a round (1152 of 512 x 512 x
+      // 512: 16 us without, 14 with; 300 of 1536 x 1536 x 4096, two rounds either way,
+      // 27 and 28).  A long sum: more stages on their way, for fewer workgroups per
+      // CU (2 of 1024 x 1024 x 4096: 29 and 23 us; of 1024 x 1024 x 1024, 8.5 and 8.7).
+      auto rounds = [&](Shape shape) { return (tile_count(g, 64, shape) * mats + 255) / 256; };
+      const bool ride = rounds(kRide) < rounds(kSym);
+      if constexpr (EPI == kPlain) {
+        if (g.kk > 1024)
+          return ride ? product_tiles<64, 64, 2, 2, kRide, EPI, true>(g, mats, s)
+                      : product_tiles<64, 64, 2, 2, kSym, EPI, true>(g, mats, s);
+      }
+      if (ride) return product_tiles<64, 64, 2, 2, kRide, EPI>(g, mats, s);
+    }
+    return product_tiles<64, 64, 2, 2, kOwn, EPI>(g, mats, s);
+  }
+  if (t128 <= large) return product_tiles<128, 128, 2, 2, kOwn, EPI>(g, mats, s);
+  if constexpr (SHAPE != kFull)
+    return product_tiles<192, 192, 2, 2, kOwn, EPI>(g, mats, s);
   else
-    return product_tiles<256, 256, 2, 4, SYM, EPI>(g, mats, s);
+    return product_tiles<256, 256, 2, 4, kOwn, EPI>(g, mats, s);
 }
 
 // The workspace: partial sums and factors, two turns of X^T and one X, three
@@ -1044,8 +1171,8 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
     g.add = add;
     g.beta = beta;
     g.diag = diag;
-    if (add) return product<true, kPoly>(g, p.mats, s);
-    return sym ? product<true, kPlain>(g, p.mats, s) : product<false, kPlain>(g, p.mats, s);
+    if (add) return product<kRide, kPoly>(g, p.mats, s);
+    return sym ? product<kSym, kPlain>(g, p.mats, s) : product<kFull, kPlain>(g, p.mats, s);
   };
   auto poly = [&](const half_t* a, half_t* d, int t) {
     const float* c = p.coefs + 3 * t;
@@ -1066,7 +1193,7 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
     g.alpha = kScaleA / (kScaleX * kScaleX);
     g.f = first ? f : nullptr;
     g.f_pow = 2;
-    return product<true, kPlain>(g, p.mats, s);
+    return product<kRide, kPlain>(g, p.mats, s);
   };
   // X = C X from the transposed copy xt[from]: into x and xt[to], the last
   // step's into the output.
@@ -1101,10 +1228,10 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
     g.carry_out = e;
     g.carry_in = e;
     g.carry_mat = w.e_mat;
-    if (last) return product<false, kOut>(g, p.mats, s);
-    if (carry == kCarryOut) return product<false, kCarryOut>(g, p.mats, s);
-    if (carry == kCarryIn) return product<false, kCarryIn>(g, p.mats, s);
-    return product<false, kPlain>(g, p.mats, s);
+    if (last) return product<kFull, kOut>(g, p.mats, s);
+    if (carry == kCarryOut) return product<kFull, kCarryOut>(g, p.mats, s);
+    if (carry == kCarryIn) return product<kFull, kCarryIn>(g, p.mats, s);
+    return product<kFull, kPlain>(g, p.mats, s);
   };
 
   // Every launch in order, until one fails.
