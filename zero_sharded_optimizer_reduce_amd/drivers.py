@@ -14,18 +14,26 @@ arithmetic step runs in the HIP kernels of libzero.
                     slide, note 原 N47)
 * OffloadStep       host-resident gradient shard through two device slots (blog,
                     section 分片放到 CPU：两个缓冲就够)
+* MuonStep          matrices updated along an orthogonalised momentum instead of
+                    Adam's quotient: reduce-scatter with the momentum step ->
+                    all-gather of directions -> Newton-Schulz per matrix -> owner
+                    updates -> all-gather (the state the blog's byte ledger gives
+                    an optimizer with a first moment only)
 * GraphedStep       a ShardedStep captured once into a HIP graph and replayed
                     every step, the step's Adam scalars read from device memory
 """
 from __future__ import annotations
 
-from typing import Optional, Sequence
+import math
+from typing import Callable, Optional, Sequence, Tuple
 
 import torch
 
-from .api import (ADAM_SCALARS_FLOATS, ZeroOffload, adam_scalars_tensor, zero_adam_scalars_fetch,
-                  zero_adam_shard_step, zero_adam_shard_step_dev, zero_all_gather_layer, zero_reduce_scatter,
-                  zero_reduce_scatter_adam, zero_reduce_scatter_adam_dev, zero_shard_layout)
+from .api import (ADAM_SCALARS_FLOATS, NS_COEFS, ZeroOffload, adam_scalars_tensor, zero_adam_scalars_fetch,
+                  zero_adam_shard_step, zero_adam_shard_step_dev, zero_all_gather_layer, zero_grad_norm_sq_no_alloc,
+                  zero_muon_momentum, zero_muon_shard_step, zero_newton_schulz, zero_newton_schulz_workspace,
+                  zero_reduce_scatter, zero_reduce_scatter_adam, zero_reduce_scatter_adam_dev,
+                  zero_reduce_scatter_muon, zero_shard_layout)
 
 
 def _empty(n, dtype, device):
@@ -131,6 +139,98 @@ class GraphedStep:
             self._events[t // self.EVENT_EVERY] = ev
         self._t = t + 1
         return self.st.view[: self.st.psi]
+
+
+class MuonStep:
+    """Matrices of the given (rows, cols), one after the other in a flat unit that
+    is padded and split into N owner shards as ShardedStep's.  Owner k holds the
+    FP32 master and momentum and the BF16 working shard.
+
+    A step moves the momentum and gathers the owners' BF16 directions, since a
+    matrix may lie in several shards; each matrix is orthogonalised once (equal
+    neighbours as one stack) and the owners apply their parts.  scale(rows, cols):
+    the factor on a matrix's orthogonalised direction, by default sqrt(max(1,
+    rows / cols)).  Nothing is allocated after the construction and the first
+    clipped step, so a step can be captured into a graph."""
+
+    def __init__(self, shapes: Sequence[Tuple[int, int]], n_ranks: int, device="cuda", coefs=NS_COEFS,
+                 scale: Optional[Callable[[int, int], float]] = None):
+        self.shapes = [(int(r), int(c)) for r, c in shapes]
+        self.n = n_ranks
+        self.psi, self.psi_pad, self.shard = zero_shard_layout([r * c for r, c in self.shapes], n_ranks)
+        self.device = torch.device(device)
+        S = self.shard
+        self.master = [_empty(S, torch.float32, device) for _ in range(n_ranks)]
+        self.momentum = [torch.zeros(S, dtype=torch.float32, device=device) for _ in range(n_ranks)]
+        self.direction = [_empty(S, torch.bfloat16, device) for _ in range(n_ranks)]
+        self.bf16 = [_empty(S, torch.bfloat16, device) for _ in range(n_ranks)]
+        self.directions = _empty(self.psi_pad, torch.bfloat16, device)
+        self.update_flat = torch.zeros(self.psi_pad, dtype=torch.bfloat16, device=device)   # the padding stays zero
+        self.view = _empty(self.psi_pad, torch.bfloat16, device)
+        self.coefs = coefs
+        scale = scale or (lambda rows, cols: math.sqrt(max(1.0, rows / cols)))
+        self.stacks = []   # (directions, updates, scale), [matrices, rows, cols] of equal neighbours
+        at = i = 0
+        while i < len(self.shapes):
+            rows, cols = self.shapes[i]
+            mats = 1
+            while i + mats < len(self.shapes) and self.shapes[i + mats] == (rows, cols):
+                mats += 1
+            end = at + mats * rows * cols
+            self.stacks.append((self.directions[at:end].view(mats, rows, cols),
+                                self.update_flat[at:end].view(mats, rows, cols), float(scale(rows, cols))))
+            at, i = end, i + mats
+        # one workspace, the stacks run one after the other
+        self.workspace = max((zero_newton_schulz_workspace(d) for d, _, _ in self.stacks), key=torch.Tensor.numel)
+        self.grad = self.norm_sq = self.clip = None   # of a clipped step
+
+    load_master = ShardedStep.load_master
+
+    def reduce_momentum(self, rank_grads, weights, hp, grad_acc=None, stream=None):
+        zero_reduce_scatter_muon(rank_grads, weights, self.momentum, self.direction, hp, grad_acc=grad_acc,
+                                 stream=stream)
+
+    def reduce_momentum_clipped(self, rank_grads, weights, hp, max_norm, stream=None):
+        """The momentum step on gradients whose norm over all owners is held to
+        max_norm: the coefficient stays on the device."""
+        if self.grad is None:
+            self.grad = [_empty(self.shard, torch.float32, self.device) for _ in range(self.n)]
+            self.norm_sq = _empty(1, torch.float64, self.device)
+            self.clip = _empty(1, torch.float32, self.device)
+        zero_reduce_scatter(rank_grads, weights, self.grad, stream=stream)
+        zero_grad_norm_sq_no_alloc(self.grad, self.norm_sq, max_norm, self.clip, stream=stream)
+        for k in range(self.n):
+            zero_muon_momentum(self.momentum[k], self.direction[k], self.grad[k], hp, grad_scale=self.clip,
+                               stream=stream)
+
+    def orthogonalise(self, stream=None):
+        zero_all_gather_layer(self.direction, self.directions, stream=stream)
+        for d, u, scale in self.stacks:
+            zero_newton_schulz(d, u, self.workspace, coefs=self.coefs, scale=scale, stream=stream)
+
+    def update(self, hp, lr_dev=None, stream=None):
+        for k in range(self.n):
+            zero_muon_shard_step(self.master[k], self.bf16[k],
+                                 self.update_flat[k * self.shard:(k + 1) * self.shard], hp, lr_dev=lr_dev,
+                                 stream=stream)
+
+    def all_gather(self, stream=None):
+        zero_all_gather_layer(self.bf16, self.view, stream=stream)
+
+    def step(self, rank_grads, weights, hp, grad_acc=None, max_norm: Optional[float] = None, lr_dev=None,
+             stream=None):
+        """grad_acc: the owners' accumulated gradients of earlier micro-batches, or
+        max_norm: the norm the reduced gradient is clipped to; not both."""
+        if max_norm is None:
+            self.reduce_momentum(rank_grads, weights, hp, grad_acc, stream)
+        elif grad_acc is None:
+            self.reduce_momentum_clipped(rank_grads, weights, hp, max_norm, stream)
+        else:
+            raise ValueError("MuonStep.step: grad_acc and max_norm together are not supported")
+        self.orthogonalise(stream)
+        self.update(hp, lr_dev, stream)
+        self.all_gather(stream)
+        return self.view[: self.psi]
 
 
 class BucketedOwnerStep:
