@@ -17,6 +17,7 @@ from . import _lib
 from ._lib import AdamHparams, MuonHparams, check, load
 
 _BF16_LIKE = (torch.bfloat16, torch.int16, torch.uint16)
+_FP32 = (torch.float32,)
 
 
 _current_device = getattr(torch._C, "_cuda_getDevice", None)   # without torch.cuda's check that the runtime is up
@@ -32,7 +33,7 @@ def _stream(stream) -> int:
     return stream.cuda_stream
 
 
-def _dev(t: torch.Tensor, what: str, dtypes) -> int:
+def _on_device(t: torch.Tensor, what: str, dtypes) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: expected a torch.Tensor")
     if not t.is_cuda:
@@ -41,9 +42,27 @@ def _dev(t: torch.Tensor, what: str, dtypes) -> int:
         raise ValueError(f"{what}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
     if t.dtype not in dtypes:
         raise TypeError(f"{what}: dtype {t.dtype} not in {dtypes}")
+
+
+def _dev(t: torch.Tensor, what: str, dtypes) -> int:
+    _on_device(t, what, dtypes)
     if not t.is_contiguous():
         raise ValueError(f"{what}: must be contiguous")
     return t.data_ptr()
+
+
+def _dev_table(ts: Sequence[torch.Tensor], what: str, dtypes, numel: int, wrong_size: str) -> C.Array:
+    """The pointers of equally long device tensors; their names are only formed
+    for a refusal."""
+    ptrs = []
+    for k, t in enumerate(ts):
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == _current_device()
+                and t.dtype in dtypes and t.is_contiguous()):
+            _dev(t, f"{what}[{k}]", dtypes)
+        if t.numel() != numel:
+            raise ValueError(wrong_size)
+        ptrs.append(t.data_ptr())
+    return (C.c_void_p * len(ptrs))(*ptrs)
 
 
 def _ptrs(ptrs) -> C.Array:
@@ -377,25 +396,21 @@ def zero_reduce_scatter_muon(rank_grads: Sequence[torch.Tensor], rank_weights, m
     if n_ranks < 1 or n_shards < 1:
         raise ValueError(f"{name}: need at least one rank and one owner")
     numel = rank_grads[0].numel()
-    gp = [_dev(g, f"rank_grads[{r}]", _BF16_LIKE) for r, g in enumerate(rank_grads)]
-    if any(g.numel() != numel for g in rank_grads):
-        raise ValueError(f"{name}: rank contributions differ in size")
+    grads = _dev_table(rank_grads, "rank_grads", _BF16_LIKE, numel, "zero_reduce_scatter_muon: rank contributions "
+                                                                    "differ in size")
     if numel % n_shards:
         raise ValueError(f"{name}: numel not divisible by the number of owners")
-    tables = []
-    for tname, ts, dt in (("momentum", momentum, (torch.float32,)), ("direction_out", direction_out, _BF16_LIKE),
-                          ("grad_acc", grad_acc, (torch.float32,))):
-        if ts is None:
-            tables.append(None)
-            continue
-        if len(ts) != n_shards or any(t.numel() != numel // n_shards for t in ts):
-            raise ValueError(f"{name}: {tname} needs {n_shards} tensors of {numel // n_shards} elements")
-        tables.append(_ptrs([_dev(t, f"{tname}[{k}]", dt) for k, t in enumerate(ts)]))
-    w = np.ascontiguousarray(np.asarray(rank_weights, dtype=np.float32))
-    if w.size != n_ranks:
+    if len(direction_out) != n_shards or (grad_acc is not None and len(grad_acc) != n_shards):
+        raise ValueError(f"{name}: one tensor per owner in each of momentum, direction_out and grad_acc")
+    part, size = numel // n_shards, "zero_reduce_scatter_muon: an owner's tensors need numel / owners elements"
+    m = _dev_table(momentum, "momentum", _FP32, part, size)
+    u = _dev_table(direction_out, "direction_out", _BF16_LIKE, part, size)
+    acc = None if grad_acc is None else _dev_table(grad_acc, "grad_acc", _FP32, part, size)
+    w = rank_weights.tolist() if hasattr(rank_weights, "tolist") else rank_weights
+    if len(w) != n_ranks:
         raise ValueError(f"{name}: one weight per rank")
     h = muon_hparams(hp)
-    check(load().zero_reduce_scatter_muon(_ptrs(gp), w.ctypes.data_as(_lib.FP), n_ranks, numel, n_shards, *tables,
+    check(load().zero_reduce_scatter_muon(grads, (C.c_float * n_ranks)(*w), n_ranks, numel, n_shards, m, u, acc,
                                           C.byref(h), _stream(stream)), name)
 
 
@@ -404,14 +419,14 @@ def _stack(t: torch.Tensor, what: str, dtypes):
     tensor whose rows are contiguous."""
     if not isinstance(t, torch.Tensor) or t.dim() not in (2, 3):
         raise TypeError(f"{what}: expected a 2-D or 3-D torch.Tensor")
-    v = t if t.dim() == 3 else t.unsqueeze(0)
-    if v.size(2) > 1 and v.stride(2) != 1:
+    _on_device(t, what, dtypes)
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2:
+        shape, stride = (1, *shape), (0, *stride)
+    mats, rows, cols = shape
+    if cols > 1 and stride[2] != 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
-    row = v.stride(1) if v.size(1) > 1 else v.size(2)
-    mat = v.stride(0) if v.size(0) > 1 else 0
-    # the checks that _dev makes of a contiguous tensor, on the first element's view
-    ptr = _dev(v[:1, :1, :1] if v.numel() else v.contiguous(), what, dtypes)
-    return ptr, v.size(0), v.size(1), v.size(2), row, mat
+    return t.data_ptr(), mats, rows, cols, stride[1] if rows > 1 else cols, stride[0] if mats > 1 else 0
 
 
 def zero_newton_schulz_workspace(g: torch.Tensor) -> torch.Tensor:
@@ -434,13 +449,14 @@ def zero_newton_schulz(g: torch.Tensor, out: torch.Tensor, workspace: torch.Tens
     op, omats, orows, ocols, orow, omat = _stack(out, "out", (torch.bfloat16,))
     if (mats, rows, cols) != (omats, orows, ocols):
         raise ValueError("zero_newton_schulz: out must have g's shape")
-    c = np.ascontiguousarray(np.asarray(coefs, dtype=np.float32))
-    if c.ndim != 2 or c.shape[1] != 3:
+    c = coefs.tolist() if hasattr(coefs, "tolist") else coefs
+    if any(not hasattr(abc, "__len__") or len(abc) != 3 for abc in c):
         raise ValueError("zero_newton_schulz: coefs needs one (a, b, c) per step")
+    flat = (C.c_float * (3 * len(c)))(*[v for abc in c for v in abc])
     wp = _dev(workspace, "workspace", (torch.uint8,))
     check(load().zero_newton_schulz(ip, _lib.ZERO_FP32 if g.dtype == torch.float32 else _lib.ZERO_BF16, irow, imat,
-                                    op, orow, omat, mats, rows, cols, c.ctypes.data_as(_lib.FP), c.shape[0],
-                                    float(scale), wp, workspace.numel(), _stream(stream)), "zero_newton_schulz")
+                                    op, orow, omat, mats, rows, cols, flat, len(c), float(scale), wp,
+                                    workspace.numel(), _stream(stream)), "zero_newton_schulz")
 
 
 def zero_muon_shard_step(master: torch.Tensor, bf16_out: torch.Tensor, update: torch.Tensor, hp,
