@@ -202,15 +202,32 @@ __global__ __launch_bounds__(kBlock) void muon_update_scalar_kernel(MuonUpdatePa
 }
 
 // -------------------------------------------------------------- launch shape
+// 64 lanes of 4 elements: one wave, the fewest requests that leave together.
+// Measured on shards of 54.5M elements (momentum, update) and 4 owners' 50.6M of
+// 4 ranks (fused): workgroups of 64, 128, 256 take 116, 117, 122 us; 98.6, 99.3,
+// 101.5 us; 563, 567, 567 us.
 constexpr int kMomentumBlock = 64;
 constexpr int kReduceMomentumBlock = 64;
 constexpr int kMuonUpdateBlock = 64;
+
+// Residency caps, as for the Adam update: the launches reserve this many bytes of
+// LDS so that 160 KiB / bytes workgroups are resident per CU.  With 40 to 60 KB of
+// loads on their way per CU the HBM keeps more row hits.  Measured without and with
+// the cap: momentum 115.8 and 113.2 us (6.59, 6.74 TB/s), update 98.5 and 97.6 us
+// (6.64, 6.70 TB/s; at 10 per CU 133 us); fused, TB/s with 1, 2, 4 and 8 ranks 6.62,
+// 6.54, 6.48, 6.32 without and 6.68, 6.67, 6.68, 6.64 with (accumulating 6.63, 6.58,
+// 6.41, 6.23 and 6.70, 6.74, 6.63, 6.63).  Other rank counts (3: 6.59) lose with any.
+constexpr unsigned kMomentumResidencyLds = 8 * 1024;     // 20 workgroups
+constexpr unsigned kMuonUpdateResidencyLds = 8 * 1024;
+constexpr unsigned reduce_momentum_residency_lds(int n_ranks) {
+  return n_ranks == 0 ? 0 : n_ranks == 1 ? 6 * 1024 : n_ranks == 2 ? 8 * 1024 : n_ranks == 4 ? 10 * 1024 : 16 * 1024;
+}
 
 template <bool SC>
 hipError_t momentum_launch(const MomentumParams& a, bool vec, hipStream_t s) {
   if (vec)
     hipLaunchKernelGGL((momentum_vec_kernel<SC, kMomentumBlock>), dim3(grid_x(a.n >> 2, 1, kMomentumBlock)),
-                       dim3(kMomentumBlock), 0, s, a);
+                       dim3(kMomentumBlock), kMomentumResidencyLds, s, a);
   else
     hipLaunchKernelGGL((momentum_scalar_kernel<SC>), dim3(grid_x(a.n, 1)), dim3(kBlock), 0, s, a);
   return hipGetLastError();
@@ -219,7 +236,8 @@ hipError_t momentum_launch(const MomentumParams& a, bool vec, hipStream_t s) {
 template <int N, bool ACC>
 hipError_t reduce_momentum_vec_launch(const ReduceMomentumParams& p, hipStream_t s) {
   hipLaunchKernelGGL((reduce_momentum_vec_kernel<N, ACC, kReduceMomentumBlock>),
-                     dim3(grid_x(p.n >> 2, 1, kReduceMomentumBlock)), dim3(kReduceMomentumBlock), 0, s, p);
+                     dim3(grid_x(p.n >> 2, 1, kReduceMomentumBlock)), dim3(kReduceMomentumBlock),
+                     reduce_momentum_residency_lds(N), s, p);
   return hipGetLastError();
 }
 
@@ -242,7 +260,7 @@ template <bool WD>
 hipError_t muon_update_launch(const MuonUpdateParams& a, bool vec, hipStream_t s) {
   if (vec)
     hipLaunchKernelGGL((muon_update_vec_kernel<WD, kMuonUpdateBlock>), dim3(grid_x(a.n >> 2, 1, kMuonUpdateBlock)),
-                       dim3(kMuonUpdateBlock), 0, s, a);
+                       dim3(kMuonUpdateBlock), kMuonUpdateResidencyLds, s, a);
   else
     hipLaunchKernelGGL((muon_update_scalar_kernel<WD>), dim3(grid_x(a.n, 1)), dim3(kBlock), 0, s, a);
   return hipGetLastError();
