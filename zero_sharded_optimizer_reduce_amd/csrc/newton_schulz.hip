@@ -1,13 +1,14 @@
 // gfx950 kernels of zero_newton_schulz: X = G/||G||_F, then per step
 //   A = X X^T,  C = a I + b A + c A A,  X = C X.
 //
-// Shapes.  k = the smaller side, l = the larger: X is taken k x l (a tall
-// input is its transpose), so A and C are k x k.  Every product is written
-// with both operands' summed index contiguous in memory, D = P Q^T: A = X X^T
-// and A A = A A^T as they stand, X' = C (X^T)^T from a second copy of X kept
-// transposed.  Products of commuting polynomials of one symmetric matrix are
-// symmetric: only tiles on and below the diagonal are computed, and written
-// twice.
+// Shapes.  k = the smaller side, l = the larger: X is kept k x l (a tall input
+// is turned on the way in and out), so A and C are k x k.  Products of the k x k
+// matrices and the Gram product have both operands' summed index contiguous in
+// memory, D = P Q^T: A = X X^T, and A A = A A^T since A is symmetric; C X takes X's
+// columns with transposing LDS reads, so one copy of X is all that is written
+// (a second, transposed one cost 6% of 32 x 512 x 1024, 2% of 2 x 14336 x 4096).
+// Products of commuting polynomials of one symmetric matrix are symmetric: only
+// tiles on and below the diagonal are computed, and written twice.
 //
 // Blocks of steps.  With C_0, C_1 polynomials of A, two steps are
 //   A' = C_0 A C_0,  C_1 = a I + b A' + c A' A',  X'' = (C_1 C_0) X:
@@ -153,9 +154,10 @@ __device__ __forceinline__ NsScale scale_of(double sum) {
 // bits in 11), and the factor f joins the products' scales, so that nothing is
 // lost before the first product.
 struct NsX {
-  half_t* same;      // G's own orientation, rows x cols, pitch pad(cols)
-  half_t* turned;    // cols x rows, pitch pad(rows)
-  int64_t same_mat, turned_mat;
+  half_t* x;         // k x l, pitch pad(l), pad(k) rows: those past k are zeros, here
+  half_t* next;      // and in the X that the steps write next
+  int64_t mat;
+  int tall;          // X is G^T
   const double* partials;
   int parts;
   float* f;          // per matrix, for the products
@@ -170,9 +172,9 @@ __global__ __launch_bounds__(kNormThreads) void ns_prepare_kernel(NsInput g, NsX
   __shared__ uint32_t tile[kTurn][kTurn / 2 + 1];
   const int mat = blockIdx.z;
   const int r0 = blockIdx.y * kTurn, c0 = blockIdx.x * kTurn;
-  const int pc = static_cast<int>(pad_up(g.cols)), pr = static_cast<int>(pad_up(g.rows));
-  half_t* same = x.same + mat * x.same_mat;
-  half_t* turned = x.turned + mat * x.turned_mat;
+  const int ld = static_cast<int>(pad_up(x.tall ? g.rows : g.cols));
+  half_t* out = x.x + mat * x.mat;
+  half_t* next = x.next + mat * x.mat;
   const int64_t base = static_cast<int64_t>(mat) * g.mat;
   const int line = threadIdx.x >> 3, c = (threadIdx.x & 7) * 8;
   constexpr int kLines = kTurn / (kNormThreads / 8);
@@ -193,22 +195,27 @@ __global__ __launch_bounds__(kNormThreads) void ns_prepare_kernel(NsInput g, NsX
 #pragma unroll
     for (int q = 0; q < 8; ++q)
       h[q] = r < g.rows && c0 + c + q < g.cols ? static_cast<half_t>(ldexpf(v[n][q], s.e) + s.add) : half_t(0);
-    if (r < g.rows) *reinterpret_cast<h8*>(same + static_cast<int64_t>(r) * pc + c0 + c) = h;
+    if (!x.tall) {
+      *reinterpret_cast<h8*>(out + static_cast<int64_t>(r) * ld + c0 + c) = h;
+      if (r >= g.rows) *reinterpret_cast<h8*>(next + static_cast<int64_t>(r) * ld + c0 + c) = h;
+    }
     const u32x4 w = __builtin_bit_cast(u32x4, h);
 #pragma unroll
     for (int q = 0; q < 4; ++q) tile[i][c / 2 + q] = w[q];
   }
+  if (!x.tall) return;
   __syncthreads();
 #pragma unroll
   for (int i = line; i < kTurn; i += kNormThreads / 8) {
-    if (c0 + i >= g.cols) continue;
     u32x4 w;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const uint32_t a = tile[c + 2 * q][i >> 1], b = tile[c + 2 * q + 1][i >> 1];
       w[q] = i & 1 ? (a >> 16) | (b & 0xFFFF0000u) : (a & 0xFFFFu) | (b << 16);
     }
-    *reinterpret_cast<u32x4*>(turned + static_cast<int64_t>(c0 + i) * pr + r0 + c) = w;
+    const int64_t at = static_cast<int64_t>(c0 + i) * ld + r0 + c;
+    *reinterpret_cast<u32x4*>(out + at) = w;
+    if (c0 + i >= g.cols) *reinterpret_cast<u32x4*>(next + at) = w;
   }
 }
 
@@ -218,7 +225,8 @@ __global__ __launch_bounds__(kNormThreads) void ns_prepare_kernel(NsInput g, NsX
 // kSym: a symmetric result, its tiles on and below the diagonal.  kRide: P = Q, and
 // the tiles on the diagonal ride: P's rows of diagonal tile i are those of tile
 // (i, i - 1), whose workgroup computes both.
-enum Shape { kFull, kSym, kRide };
+// kTimesX: Q^T is X itself, rows in order of the summed index.
+enum Shape { kFull, kSym, kRide, kTimesX };
 enum Epilogue { kPlain, kPoly, kCarryOut, kCarryIn, kOut };
 struct Product {
   const half_t* p;
@@ -227,20 +235,17 @@ struct Product {
   int p_ld, q_ld;
   int m, n, kk;
   int tiles_n, tiles;       // per matrix
-  // FP16 results: d row-major (columns n up to d_ld written, the padding as
-  // zeros) and dt its transpose; either may be NULL.  For a symmetric product
-  // both are the same matrix.
-  half_t* d;
-  half_t* dt;
-  int64_t d_mat, dt_mat;
-  int d_ld, dt_ld;
+  half_t* d;                // FP16 result, columns n up to d_ld written as zeros
+  int64_t d_mat;
+  int d_ld;
   const half_t* add;        // polynomial: beta * add + diag * I joins (symmetric, pitch d_ld)
   float alpha, beta, diag;
   const float* f;           // per-matrix factor of alpha, or NULL
   int f_pow;
-  uint16_t* out;            // BF16 result instead of d, dt
+  uint16_t* out;            // BF16 result instead of d
   int64_t out_row, out_mat;
   int out_vec;              // 16-byte stores are aligned
+  int out_turned;           // as its transpose
   half_t* carry_out;        // the FP16 roundings of d, in the lanes' own order, or NULL
   const half_t* carry_in;   // those of the X this product reads, or NULL
   int64_t carry_mat;
@@ -288,25 +293,89 @@ struct Stager {
   }
 };
 
+// Of X, rows [k0, k0 + 64) and columns [col0, col0 + C): 64 rows of 2 C bytes, from
+// which transposing reads take the columns.  Those read 64 bytes of four rows
+// together: the 64-byte piece c of row r lies at piece c ^ (r & 3) (C = 64, where
+// two rows fill the banks: c ^ ((r >> 1) & 1)).  Columns past the end hold the
+// next row; their results are dropped.
+template <int C, int NW>
+struct ColumnStager {
+  static constexpr int kRows = 512 / C, kN = 64 / kRows / NW;   // rows of one instruction, instructions of a wave
+  static_assert(kN * kRows * NW == 64 && (C != 256 || kN % 2 == 0), "every wave moves the same number of pieces");
+  half_t* base;
+  int voff[2], ld, wave, end;   // voff: even and odd instructions
+  __device__ __forceinline__ ColumnStager(const half_t* mat, int ld_, int col0, int kk, int wave_, int lane)
+      : base(const_cast<half_t*>(mat + col0)), ld(ld_), wave(wave_), end(kk) {
+    const int row = lane / (64 / kRows), piece = lane % (64 / kRows);
+#pragma unroll
+    for (int odd = 0; odd < 2; ++odd) {
+      const int r = row + (C == 256 ? 2 * odd : 0), s = C == 64 ? (r >> 1) & 1 : r & 3;
+      voff[odd] = (wave * kN * kRows + row) * ld * 2 + (((piece >> 2) ^ s) << 6) + (piece & 3) * 16;
+    }
+  }
+  __device__ __forceinline__ void one(half_t* lds, int k0, int i) const {
+#ifdef __HIP_DEVICE_COMPILE__
+    const bool live = k0 < end;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        __builtin_amdgcn_make_buffer_rsrc(base + static_cast<int64_t>(k0) * ld, 0, live ? kBk * ld * 2 : 0,
+                                          0x00020000),
+        (lds_void*)(lds + (wave * kN + i) * 512), 16, voff[i & 1], live ? i * kRows * ld * 2 : 0, 0, 0);
+#endif
+  }
+  __device__ __forceinline__ void all(half_t* lds, int k0) const {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) one(lds, k0, i);
+  }
+};
+// Byte offset in a slot of what the lane points a transposing read at: row 8 *
+// (lane >> 5) + ((lane >> 2) & 3), columns first + 16 * ((lane >> 4) & 1) + 4 * (lane & 3).
+template <int C>
+__device__ __forceinline__ int lane_at_column(int first, int lane) {
+  const int s = C == 64 ? (lane >> 3) & 1 : (lane >> 2) & 3;
+  return ((lane >> 5) * 8 + ((lane >> 2) & 3)) * C * 2 + (((first >> 5) ^ s) << 6) + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+}
+
+// 4 values down a column, twice: the transposing LDS read hands lane j of 16 the
+// component j % 4 of the lanes j / 4 + 4 q, so each lane points at four columns of
+// one row and lane j gets column j of four rows.
+__device__ __forceinline__ u32x4 transpose8(const void* at, const void* at4) {
+  u32x4 v = {};
+#ifdef __HIP_DEVICE_COMPILE__   // the builtin is unknown to the host pass
+  typedef short s4 __attribute__((ext_vector_type(4)));
+  typedef short s8 __attribute__((ext_vector_type(8)));
+  typedef __attribute__((address_space(3))) s4 lds_s4;
+  const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)at);
+  const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)at4);
+  v = __builtin_bit_cast(u32x4, s8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w});
+#endif
+  return v;
+}
 // A wave's operands for half a stage: two 16-wide pieces of the summed index.
-// SECOND: the rows of P at the wave's columns too, for P P^T.
-template <int TM, int TN, bool SECOND>
+// SECOND: the rows of P at the wave's columns too, for P P^T.  C: Q is C columns of
+// X (see ColumnStager), else 0.
+template <int TM, int TN, bool SECOND, int C>
 struct Frags {
   static constexpr int kSets = TM + TN + (SECOND ? TN : 0), kReads = 2 * kSets;
   h8 a[2][TM], b[2][TN], c[2][TN];
   // Read number n of kReads; at_p, at_q, at_c: the lane's byte offsets in a slot
-  // (see lane_at); half 0 or 1.
+  // (see lane_at, lane_at_column); half 0 or 1.
   __device__ __forceinline__ void one(const half_t* p, const half_t* q, int at_p, int at_q, int at_c, int half, int n) {
     const int u = n / kSets, i = n - u * kSets, flip = half * 64 + u * 32;
     auto read = [&](const half_t* m, int at, int block) {
       return *reinterpret_cast<const h8*>(reinterpret_cast<const char*>(m) + (at ^ flip) + block * 32 * kBk * 2);
     };
-    if (i < TM)
+    if (i < TM) {
       a[u][i] = read(p, at_p, i);
-    else if (i < TM + TN)
-      b[u][i - TM] = read(q, at_q, i - TM);
-    else
+    } else if (i < TM + TN) {
+      if constexpr (C > 0) {
+        const char* at = reinterpret_cast<const char*>(q) + (at_q ^ ((i - TM) << 6)) + (half * 32 + u * 16) * C * 2;
+        b[u][i - TM] = __builtin_bit_cast(h8, transpose8(at, at + 4 * C * 2));
+      } else {
+        b[u][i - TM] = read(q, at_q, i - TM);
+      }
+    } else {
       c[u][i - TM - TN] = read(p, at_c, i - TM - TN);
+    }
   }
 };
 
@@ -339,20 +408,7 @@ __device__ __forceinline__ int xcd_order(int id, int n) {
 }
 
 // 8 values down a column: the lane gets rows row + 8 * (lane >> 4) + 0..7 of column
-// col + (lane & 15).  The transposing LDS read hands lane j of 16 the component
-// j % 4 of the lanes j / 4 + 4 q, so each lane points at four columns of one row.
-__device__ __forceinline__ u32x4 transpose8(const void* at, const void* at4) {
-  u32x4 v = {};
-#ifdef __HIP_DEVICE_COMPILE__   // the builtin is unknown to the host pass
-  typedef short s4 __attribute__((ext_vector_type(4)));
-  typedef short s8 __attribute__((ext_vector_type(8)));
-  typedef __attribute__((address_space(3))) s4 lds_s4;
-  const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)at);
-  const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)at4);
-  v = __builtin_bit_cast(u32x4, s8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w});
-#endif
-  return v;
-}
+// col + (lane & 15).
 __device__ __forceinline__ u32x4 column_piece(const uint16_t* m, int pitch, int row, int col, int lane) {
   const uint16_t* at = m + (row + (lane >> 4) * 8 + ((lane >> 2) & 3)) * pitch + col + (lane & 3) * 4;
   return transpose8(at, at + 4 * pitch);
@@ -363,6 +419,17 @@ __device__ __forceinline__ u32x4 first(u32x4 v, int n) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) v[q] = 2 * q + 1 < n ? v[q] : 2 * q < n ? v[q] & 0xFFFFu : 0u;
   return v;
+}
+
+// The first n of 8 values to memory, which is 16-byte aligned if vec.
+__device__ __forceinline__ void store8(uint16_t* dst, u32x4 v, int vec, int n) {
+  if (vec && n >= 8) {
+    *reinterpret_cast<u32x4*>(dst) = v;
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < n) dst[q] = static_cast<uint16_t>(v[q >> 1] >> ((q & 1) * 16));
+  }
 }
 
 template <int NW>
@@ -392,7 +459,9 @@ __global__ __launch_bounds__(WR * WC * 64, BM <= 128 ? 2 : 1) void ns_product_ke
   // Five places for an operand's rows of one stage, ten for the smallest tile: its
   // stages are short, and four of them have to be on their way.  Separate arrays,
   // so that the compiler can tell a load on its way into one from a read of another.
-  constexpr bool SYM = SHAPE != kFull;
+  constexpr bool SYM = SHAPE == kSym || SHAPE == kRide;
+  constexpr int kColumns = SHAPE == kTimesX ? BN : 0;
+  static_assert(TN == 1 || TN == 2 || !kColumns, "a wave's 64-byte pieces are a power of two");
   __shared__ __align__(16) half_t slot0[kSlot];
   __shared__ __align__(16) half_t slot1[kSlot];
   __shared__ __align__(16) half_t slot2[kSlot];
@@ -435,10 +504,12 @@ __global__ __launch_bounds__(WR * WC * 64, BM <= 128 ? 2 : 1) void ns_product_ke
   }
   const int row0 = ti * BM, col0 = tj * BN;
   const Stager<BM, NW> sp(g.p + mat * g.p_mat, g.p_ld, row0, g.kk, wave, lane);
-  const Stager<BN, NW> sq(g.q + mat * g.q_mat, g.q_ld, col0, g.kk, wave, lane);
+  using QStager = std::conditional_t<SHAPE == kTimesX, ColumnStager<BN, NW>, Stager<BN, NW>>;
+  const QStager sq(g.q + mat * g.q_mat, g.q_ld, col0, g.kk, wave, lane);
   const int wr = wave / WC, wc = wave - wr * WC;
-  int at_p = lane_at(wr * (BM / WR), lane), at_q = lane_at(wc * (BN / WC), lane);
-  constexpr int kP = Stager<BM, NW>::kN, kQ = Stager<BN, NW>::kN;
+  int at_p = lane_at(wr * (BM / WR), lane);
+  int at_q = SHAPE == kTimesX ? lane_at_column<BN>(wc * (BN / WC), lane) : lane_at(wc * (BN / WC), lane);
+  constexpr int kP = Stager<BM, NW>::kN, kQ = QStager::kN;
   // The lane's values of block (i, j): row lane & 31 of the block, columns 8 * u +
   // 4 * (lane >> 5) + q (the products take Q's fragment first).
   float alpha = g.alpha;
@@ -533,6 +604,22 @@ __global__ __launch_bounds__(WR * WC * 64, BM <= 128 ? 2 : 1) void ns_product_ke
       constexpr int kPieces = kRows * kCols / 512, kStep = kPieces % 8 == 0 ? 8 : kPieces % 6 == 0 ? 6 : kPieces;
       const int brow = wrow + ib * 32;
       if constexpr (EPI == kOut) {
+        if (g.out_turned) {
+          uint16_t* out = g.out + mat * g.out_mat + static_cast<int64_t>(wcol) * g.out_row + brow;
+#pragma unroll 1
+          for (int k0 = 0; k0 < kPieces; k0 += kStep) {
+            u32x4 piece[kStep];
+#pragma unroll
+            for (int k = 0; k < kStep; ++k)
+              piece[k] = column_piece(mine, kPitch, (k0 + k) % kBand * 32, (k0 + k) / kBand * 16, lane);
+#pragma unroll
+            for (int k = 0; k < kStep; ++k) {
+              const int c = (k0 + k) / kBand * 16 + (lane & 15), r = (k0 + k) % kBand * 32 + (lane >> 4) * 8;
+              if (wcol + c < g.n) store8(out + c * g.out_row + r, piece[k], g.out_vec, g.m - brow - r);
+            }
+          }
+          continue;
+        }
         uint16_t* out = g.out + mat * g.out_mat + static_cast<int64_t>(brow) * g.out_row + wcol;
 #pragma unroll 1
         for (int k0 = 0; k0 < kPieces; k0 += kStep) {
@@ -545,15 +632,7 @@ __global__ __launch_bounds__(WR * WC * 64, BM <= 128 ? 2 : 1) void ns_product_ke
 #pragma unroll
           for (int k = 0; k < kStep; ++k) {
             const int at = (k0 + k) * 64 + lane, r = at / (kCols / 8), c = (at - r * (kCols / 8)) * 8;
-            uint16_t* dst = out + r * g.out_row + c;
-            if (brow + r >= g.m) continue;
-            if (g.out_vec && wcol + c + 8 <= g.n) {
-              *reinterpret_cast<u32x4*>(dst) = piece[k];
-            } else {
-#pragma unroll
-              for (int q = 0; q < 8; ++q)
-                if (wcol + c + q < g.n) dst[q] = static_cast<uint16_t>(piece[k][q >> 1] >> ((q & 1) * 16));
-            }
+            if (brow + r < g.m) store8(out + r * g.out_row + c, piece[k], g.out_vec, g.n - wcol - c);
           }
         }
       } else {
@@ -574,8 +653,8 @@ __global__ __launch_bounds__(WR * WC * 64, BM <= 128 ? 2 : 1) void ns_product_ke
               *reinterpret_cast<u32x4*>(d + r * g.d_ld + c) = piece[k];
           }
         }
-        if (g.dt) {
-          half_t* dt = g.dt + mat * g.dt_mat + static_cast<int64_t>(wcol) * g.dt_ld + brow;
+        if constexpr (SYM) {   // its transpose
+          half_t* dt = g.d + mat * g.d_mat + static_cast<int64_t>(wcol) * g.d_ld + brow;
 #pragma unroll 1
           for (int k0 = 0; k0 < kPieces; k0 += kStep) {
             // 16 columns, 8 rows of each 8 * (lane >> 4) rows on
@@ -602,8 +681,8 @@ __global__ __launch_bounds__(WR * WC * 64, BM <= 128 ? 2 : 1) void ns_product_ke
             for (int k = 0; k < kStep; ++k) {
               const int c = (k0 + k) / kBand * 16 + (lane & 15), r = (k0 + k) % kBand * 32 + (lane >> 4) * 8;
               if (brow + r + 8 > g.m) piece[k] = first(piece[k], g.m - brow - r);
-              if (wcol + c < g.n && brow + r < g.dt_ld && !(diagonal && (wcol + c) >> 5 > (brow + r) >> 5))
-                *reinterpret_cast<u32x4*>(dt + c * g.dt_ld + r) = piece[k];
+              if (wcol + c < g.n && brow + r < g.d_ld && !(diagonal && (wcol + c) >> 5 > (brow + r) >> 5))
+                *reinterpret_cast<u32x4*>(dt + c * g.d_ld + r) = piece[k];
             }
           }
         }
@@ -614,7 +693,7 @@ __global__ __launch_bounds__(WR * WC * 64, BM <= 128 ? 2 : 1) void ns_product_ke
   // The whole tile; every wave has the same loads and barriers.
   auto tile = [&](auto second) {
     constexpr bool SECOND = decltype(second)::value;
-    using Set = Frags<TM, TN, SECOND>;
+    using Set = Frags<TM, TN, SECOND, kColumns>;
     constexpr int kProducts = 2 * TM * TN, kReads = Set::kReads;
     Set f0, f1;
     f16 acc[TM][TN] = {}, acc2[TM][TN] = {};
@@ -721,7 +800,7 @@ __global__ __launch_bounds__(WR * WC * 64, BM <= 128 ? 2 : 1) void ns_product_ke
 // Workgroups per matrix.
 int64_t tile_count(const Product& g, int side, Shape shape) {
   const int64_t tm = (g.m + side - 1) / side, tn = (g.n + side - 1) / side;
-  if (shape == kFull) return tm * tn;
+  if (shape == kFull || shape == kTimesX) return tm * tn;
   return shape == kSym ? tm * (tm + 1) / 2 : tm > 2 ? tm * (tm - 1) / 2 : tm;
 }
 
@@ -748,7 +827,8 @@ hipError_t product(const Product& g, int64_t mats, hipStream_t s) {
   auto time = [&](int side, double us, double fixed, double launch) {
     return static_cast<double>((tile_count(g, side, kOwn) * mats + 255) / 256) * (us * g.kk / 4096.0 + fixed) + launch;
   };
-  const double large = SHAPE != kFull ? time(192, 66.0, 11.0, 2.0) : time(256, 115.0, 11.0, 2.0);
+  constexpr bool kTri = SHAPE == kSym || SHAPE == kRide;
+  const double large = kTri ? time(192, 66.0, 11.0, 2.0) : time(256, 115.0, 11.0, 2.0);
   const double t128 = time(128, 32.0, 3.0, 3.0), t64 = time(64, 14.0, 1.6, 1.5);
   if (t64 <= t128 && t64 <= large) {
     if constexpr (SHAPE == kRide) {
@@ -768,18 +848,18 @@ hipError_t product(const Product& g, int64_t mats, hipStream_t s) {
     return product_tiles<64, 64, 2, 2, kOwn, EPI>(g, mats, s);
   }
   if (t128 <= large) return product_tiles<128, 128, 2, 2, kOwn, EPI>(g, mats, s);
-  if constexpr (SHAPE != kFull)
+  if constexpr (kTri)
     return product_tiles<192, 192, 2, 2, kOwn, EPI>(g, mats, s);
   else
     return product_tiles<256, 256, 2, 4, kOwn, EPI>(g, mats, s);
 }
 
-// The workspace: partial sums and factors, two turns of X^T and one X, three
+// The workspace: partial sums and factors, X and the next X, three
 // k x k matrices, each for all matrices.
 struct Layout {
   int64_t k, l, kp, lp;
   int64_t e_mat;                                   // rounding errors of one matrix: whole tiles
-  int64_t partials, f, x, xt[2], sq[3], e, bytes;  // byte offsets
+  int64_t partials, f, x[2], sq[3], e, bytes;  // byte offsets
   Layout(int64_t mats, int64_t rows, int64_t cols) {
     k = rows < cols ? rows : cols;
     l = rows < cols ? cols : rows;
@@ -793,8 +873,7 @@ struct Layout {
     };
     partials = take(mats * kNormParts * 8);
     f = take(mats * 4);
-    x = take(mats * k * lp * 2);
-    for (int64_t& o : xt) o = take(mats * l * kp * 2);
+    for (int64_t& o : x) o = take(mats * kp * lp * 2);
     for (int64_t& o : sq) o = take(mats * k * kp * 2);
     e_mat = (k + kTile - 1) / kTile * kTile * ((l + kTile - 1) / kTile * kTile);
     e = take(mats * e_mat * 2);
@@ -1126,13 +1205,12 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
   const bool tall = p.rows > p.cols;
   const int k = static_cast<int>(w.k), l = static_cast<int>(w.l), kp = static_cast<int>(w.kp),
             lp = static_cast<int>(w.lp);
-  half_t* x = reinterpret_cast<half_t*>(ws + w.x);
-  half_t* xt[2] = {reinterpret_cast<half_t*>(ws + w.xt[0]), reinterpret_cast<half_t*>(ws + w.xt[1])};
+  half_t* x[2] = {reinterpret_cast<half_t*>(ws + w.x[0]), reinterpret_cast<half_t*>(ws + w.x[1])};
   half_t* sq[3] = {reinterpret_cast<half_t*>(ws + w.sq[0]), reinterpret_cast<half_t*>(ws + w.sq[1]),
                    reinterpret_cast<half_t*>(ws + w.sq[2])};
   float* f = reinterpret_cast<float*>(ws + w.f);
   half_t* e = reinterpret_cast<half_t*>(ws + w.e);
-  const int64_t x_mat = w.k * w.lp, xt_mat = w.l * w.kp, sq_mat = w.k * w.kp;
+  const int64_t x_mat = w.kp * w.lp, sq_mat = w.k * w.kp;
 
   double* partials = reinterpret_cast<double*>(ws + w.partials);
   const int64_t rows4 = (p.rows + kNormThreads / 64 - 1) / (kNormThreads / 64);
@@ -1141,10 +1219,10 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   NsX nx;
-  nx.same = tall ? xt[0] : x;
-  nx.turned = tall ? x : xt[0];
-  nx.same_mat = tall ? xt_mat : x_mat;
-  nx.turned_mat = tall ? x_mat : xt_mat;
+  nx.x = x[0];
+  nx.next = x[1];
+  nx.mat = x_mat;
+  nx.tall = tall;
   nx.partials = partials;
   nx.parts = parts;
   nx.f = f;
@@ -1161,12 +1239,11 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
     Product g = {};
     g.p = u;
     g.q = v;
-    g.p_mat = g.q_mat = g.d_mat = g.dt_mat = sq_mat;
-    g.p_ld = g.q_ld = g.d_ld = g.dt_ld = kp;
+    g.p_mat = g.q_mat = g.d_mat = sq_mat;
+    g.p_ld = g.q_ld = g.d_ld = kp;
     g.m = g.n = k;
     g.kk = kp;
     g.d = d;
-    g.dt = sym ? d : nullptr;
     g.alpha = alpha;
     g.add = add;
     g.beta = beta;
@@ -1180,58 +1257,55 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
   };
 
   // A = X X^T of the stored X (first: still short of the factor f)
-  auto gram = [&](half_t* d, bool first) {
+  auto gram = [&](const half_t* from, half_t* d, bool first) {
     Product g = {};
-    g.p = g.q = x;
+    g.p = g.q = from;
     g.p_mat = g.q_mat = x_mat;
     g.p_ld = g.q_ld = lp;
     g.m = g.n = k;
     g.kk = lp;
-    g.d = g.dt = d;
-    g.d_mat = g.dt_mat = sq_mat;
-    g.d_ld = g.dt_ld = kp;
+    g.d = d;
+    g.d_mat = sq_mat;
+    g.d_ld = kp;
     g.alpha = kScaleA / (kScaleX * kScaleX);
     g.f = first ? f : nullptr;
     g.f_pow = 2;
     return product<kRide, kPlain>(g, p.mats, s);
   };
-  // X = C X from the transposed copy xt[from]: into x and xt[to], the last
-  // step's into the output.
-  auto apply = [&](const half_t* c, float c_scale, int from, bool first, int to, bool last, Epilogue carry) {
+  // X = C X into the other X, the last step's into the output.
+  auto apply = [&](const half_t* c, float c_scale, int from, bool first, bool last, Epilogue carry) {
     Product g = {};
     g.f = first ? f : nullptr;
     g.f_pow = 1;
+    g.p = c;
+    g.p_mat = sq_mat;
+    g.p_ld = kp;
+    g.q = x[from];
+    g.q_mat = x_mat;
+    g.q_ld = lp;
+    g.m = k;
+    g.n = l;
     g.kk = kp;
-    const bool turned = last && tall;   // the result's own orientation
-    g.p = turned ? xt[from] : c;
-    g.q = turned ? c : xt[from];
-    g.p_mat = turned ? xt_mat : sq_mat;
-    g.q_mat = turned ? sq_mat : xt_mat;
-    g.p_ld = g.q_ld = kp;
-    g.m = turned ? l : k;
-    g.n = turned ? k : l;
     if (last) {
       g.alpha = p.scale / (c_scale * kScaleX);
       g.out = p.out;
       g.out_row = p.out_row;
       g.out_mat = p.out_mat;
       g.out_vec = (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0 && p.out_row % 8 == 0 && p.out_mat % 8 == 0;
+      g.out_turned = tall;
     } else {
       g.alpha = 1.0f / c_scale;
-      g.d = x;
+      g.d = x[from ^ 1];
       g.d_mat = x_mat;
       g.d_ld = lp;
-      g.dt = xt[to];
-      g.dt_mat = xt_mat;
-      g.dt_ld = kp;
     }
     g.carry_out = e;
     g.carry_in = e;
     g.carry_mat = w.e_mat;
-    if (last) return product<kFull, kOut>(g, p.mats, s);
-    if (carry == kCarryOut) return product<kFull, kCarryOut>(g, p.mats, s);
-    if (carry == kCarryIn) return product<kFull, kCarryIn>(g, p.mats, s);
-    return product<kFull, kPlain>(g, p.mats, s);
+    if (last) return product<kTimesX, kOut>(g, p.mats, s);
+    if (carry == kCarryOut) return product<kTimesX, kCarryOut>(g, p.mats, s);
+    if (carry == kCarryIn) return product<kTimesX, kCarryIn>(g, p.mats, s);
+    return product<kTimesX, kPlain>(g, p.mats, s);
   };
 
   // Every launch in order, until one fails.
@@ -1240,8 +1314,8 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
     if (st == hipSuccess) st = launch();
   };
   // Steps t and t + 1 as one product with X: its factor C' C into sq[0].
-  auto pair = [&](int t, bool first) {
-    run([&] { return gram(sq[0], first); });
+  auto pair = [&](int t, int from, bool first) {
+    run([&] { return gram(x[from], sq[0], first); });
     run([&] { return poly(sq[0], sq[1], t); });
     run([&] { return square(true, sq[1], sq[0], sq[2], 1.0f / kScaleC, nullptr, 0, 0); });   // C A
     run([&] { return square(true, sq[1], sq[2], sq[0], 1.0f / kScaleC, nullptr, 0, 0); });   // A' = C (C A)^T
@@ -1256,32 +1330,32 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
   const bool wide = l >= 2 * k;
   int t = 0, cur = 0;
   if (p.steps == 1) {
-    run([&] { return gram(sq[0], true); });
+    run([&] { return gram(x[0], sq[0], true); });
     run([&] { return poly(sq[0], sq[1], 0); });
-    run([&] { return apply(sq[1], kScaleC, 0, true, 1, true, kPlain); });
+    run([&] { return apply(sq[1], kScaleC, 0, true, true, kPlain); });
     return st;
   }
   // The first two steps together: X is still exact, and the second step's X
   // need not be rounded.
-  pair(0, true);
+  pair(0, 0, true);
   t = 2;
   // X after two steps: its rounding errors are carried into the next product.
   const bool carries = p.steps >= 4 && !(wide && p.steps == 4);
-  run([&] { return apply(sq[0], kScaleQ, 0, true, 1, t == p.steps, carries ? kCarryOut : kPlain); });
+  run([&] { return apply(sq[0], kScaleQ, 0, true, t == p.steps, carries ? kCarryOut : kPlain); });
   cur = 1;
   while (t < p.steps) {
     // The last two together where X is long: one product with X less for two
     // more k x k products.
     if (wide && p.steps - t == 2) {
-      pair(t, false);
+      pair(t, cur, false);
       t += 2;
-      run([&] { return apply(sq[0], kScaleQ, cur, false, cur ^ 1, true, kPlain); });
+      run([&] { return apply(sq[0], kScaleQ, cur, false, true, kPlain); });
     } else {
       const Epilogue carry = carries && t == 2 ? kCarryIn : kPlain;
-      run([&] { return gram(sq[0], false); });
+      run([&] { return gram(x[cur], sq[0], false); });
       run([&] { return poly(sq[0], sq[1], t); });
       ++t;
-      run([&] { return apply(sq[1], kScaleC, cur, false, cur ^ 1, t == p.steps, carry); });
+      run([&] { return apply(sq[1], kScaleC, cur, false, t == p.steps, carry); });
     }
     cur ^= 1;
   }
