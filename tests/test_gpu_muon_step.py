@@ -155,6 +155,7 @@ def _ns_f64(g, scale):
 # with a long summed index; 128; 192 and 256.  Odd sides, so that tiles end inside.
 @pytest.mark.parametrize("mats,rows,cols", [(2, 515, 530), (7, 517, 650), (7, 650, 517), (7, 513, 1110), (1, 1030, 1027),
                                             (33, 511, 1021), (3, 777, 1301), (1, 1290, 4099), (1, 2047, 2050),
+                                            (1, 2900, 2910),
                                             (1, 4090, 4097), (1, 4300, 3990), (12, 1025, 3001),
                                             (12, 3001, 1025)])
 def test_newton_schulz_tiles(mats, rows, cols):

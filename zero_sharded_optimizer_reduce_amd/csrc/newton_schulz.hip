@@ -816,28 +816,29 @@ hipError_t product_tiles(Product g, int64_t mats, hipStream_t s) {
 // The tile for a product, by its modelled time: rounds of 256 tiles, one per CU,
 // each with a part proportional to the summed index (us at 4096) and a fixed one,
 // and the launch's own; fitted to launches at k = 256 to 4096 on MI355X.  Both
-// sides of some choices, measured: a symmetric 4096 x 4096 x 4096 product takes
-// 80 us with 253 tiles of 192 and 108 with 528 of 128; of 512 x 512 x 512, 32 at
-// once, 21 with 192, 15 with 128 and 18 with 64; of 777 x 777 x 832, three at
-// once, 19, 13 and 10.  A full 4096 x 4096 x 4096 product 126 with 256 and 161 with
-// 128; 1024 x 4096 x 1024, two at once, 33 and 28.
+// sides of some choices, measured over whole calls with the symmetric products'
+// tiles forced: 32 of 512 x 1024 take 338 us with 64, 347 with 128, 400 with 192;
+// 3 of 777 x 1301, 189, 225, 321; 3000 x 3000, 1069, 847, 865; 4096 x 4096, 2240,
+// 1693, 1430.  With C X's forced: 2 of 1024 x 4096, 319 with 64, 259 with 128, 269
+// with 256; 4096 x 4096, 2193, 1554, 1416.
 template <Shape SHAPE, Epilogue EPI>
 hipError_t product(const Product& g, int64_t mats, hipStream_t s) {
   constexpr Shape kOwn = SHAPE == kRide ? kSym : SHAPE;
-  auto time = [&](int side, double us, double fixed, double launch) {
-    return static_cast<double>((tile_count(g, side, kOwn) * mats + 255) / 256) * (us * g.kk / 4096.0 + fixed) + launch;
+  constexpr bool kTri = kOwn == kSym;
+  auto rounds = [&](int side, Shape shape) { return (tile_count(g, side, shape) * mats + 255) / 256; };
+  const bool ride = SHAPE == kRide && rounds(64, kRide) < rounds(64, kSym);
+  auto time = [&](int64_t n, double us, double fixed, double launch) {
+    return static_cast<double>(n) * (us * g.kk / 4096.0 + fixed) + launch;
   };
-  constexpr bool kTri = SHAPE == kSym || SHAPE == kRide;
-  const double large = kTri ? time(192, 66.0, 11.0, 2.0) : time(256, 115.0, 11.0, 2.0);
-  const double t128 = time(128, 32.0, 3.0, 3.0), t64 = time(64, 14.0, 1.6, 1.5);
+  const double large = kTri ? time(rounds(192, kOwn), 66.0, 11.0, 2.0) : time(rounds(256, kOwn), 115.0, 11.0, 2.0);
+  const double t128 = time(rounds(128, kOwn), 32.0, 5.0, 3.0);
+  const double t64 = time(rounds(64, ride ? kRide : kOwn), 17.0, 1.2, 1.5);
   if (t64 <= t128 && t64 <= large) {
     if constexpr (SHAPE == kRide) {
       // The tiles on the diagonal ride where that saves a round (1152 of 512 x 512 x
       // 512: 16 us without, 14 with; 300 of 1536 x 1536 x 4096, two rounds either way,
       // 27 and 28).  A long sum: more stages on their way, for fewer workgroups per
       // CU (2 of 1024 x 1024 x 4096: 29 and 23 us; of 1024 x 1024 x 1024, 8.5 and 8.7).
-      auto rounds = [&](Shape shape) { return (tile_count(g, 64, shape) * mats + 255) / 256; };
-      const bool ride = rounds(kRide) < rounds(kSym);
       if constexpr (EPI == kPlain) {
         if (g.kk > 1024)
           return ride ? product_tiles<64, 64, 2, 2, kRide, EPI, true>(g, mats, s)
