@@ -894,7 +894,7 @@ struct SmallNs {
   NsInput in;
   uint16_t* out;
   int64_t out_row, out_mat;
-  int k, l, lp, steps, tall;
+  int k, l, lp, steps, tall, out_vec;
   float scale;
   float coefs[3 * ZERO_NS_MAX_STEPS];
 };
@@ -943,11 +943,6 @@ template <int XP>
 __device__ __forceinline__ h8 column8(const half_t* m, int k0, int c0, int lane) {
   const int row = k0 + (lane >> 4) * 8 + ((lane >> 2) & 3), col = c0 + (lane & 3) * 4;
   return __builtin_bit_cast(h8, transpose8(m + x_at<XP>(row, col), m + x_at<XP>(row + 4, col)));
-}
-
-__device__ __forceinline__ void split(float v, half_t* hi, half_t* lo) {
-  *hi = static_cast<half_t>(v);
-  *lo = static_cast<half_t>(v - static_cast<float>(*hi));
 }
 
 __device__ __forceinline__ void split4(acc4 v, half_t* hi, half_t* lo) {
@@ -1021,12 +1016,24 @@ __global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(SmallNs g) {
     const int i = threadIdx.x + n * kSmallThreads;
     if (i < groups) {
       const int r = i / per_row, c = (i - r * per_row) * 8;
+      h8 h, l;   // past the end: load8's zeros
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (c + q < g.in.cols) {
-          const int at = g.tall ? x_at<XP>(c + q, r) : x_at<XP>(r, c + q);
-          split(static_cast<float>(static_cast<double>(v[n][q]) * mult) + add, xh + at, xl + at);
-        }
+      for (int q = 0; q < 8; ++q) {
+        const float w = c + q < g.in.cols ? static_cast<float>(static_cast<double>(v[n][q]) * mult) + add : 0.0f;
+        h[q] = static_cast<half_t>(w);
+        l[q] = static_cast<half_t>(w - static_cast<float>(h[q]));
+      }
+      if (!g.tall) {
+        *reinterpret_cast<h8*>(xh + x_at<XP>(r, c)) = h;
+        *reinterpret_cast<h8*>(xl + x_at<XP>(r, c)) = l;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (c + q < g.in.cols) {
+            xh[x_at<XP>(c + q, r)] = h[q];
+            xl[x_at<XP>(c + q, r)] = l[q];
+          }
+      }
     }
   }
   __syncthreads();
@@ -1063,7 +1070,7 @@ __global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(SmallNs g) {
         Acc3 s;
         if (blk < kBlocks) {
           const int bi = blk / kSide * 16 + lr, bj = blk % kSide * 16 + lr;
-#pragma unroll 2
+#pragma unroll 4
           for (int k0 = lk; k0 < lp; k0 += 32)
             s.add(row8(xh, x_at<XP>(bi, k0)), row8(xl, x_at<XP>(bi, k0)), row8(xh, x_at<XP>(bj, k0)),
                   row8(xl, x_at<XP>(bj, k0)));
@@ -1134,20 +1141,36 @@ __global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(SmallNs g) {
           s.add(ph[k0], pl[k0], row8(sh, at), row8(sl, at));
         }
         acc4 w = s.sum();   // of X^T C: four columns of row bi * 16 + lr
-        const int r = bi * 16 + lr, col = c0 + lq;
+        const int at = x_at<XP>(bi * 16 + lr, c0 + lq);
         if (!last) {
-          split4(w * (1.0f / kScaleC), xh + x_at<XP>(r, col), xl + x_at<XP>(r, col));
-        } else if (r < g.k) {
+          split4(w * (1.0f / kScaleC), xh + at, xl + at);
+        } else {   // the result, BF16, in place of hi
+          u16x4 o;
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (col + q < g.l)
-              g.out[blockIdx.x * g.out_mat + (g.tall ? (col + q) * g.out_row + r : r * g.out_row + col + q)] =
-                  bf16_rne(w[q] * (g.scale / (kScaleC * kScaleX)));
+          for (int q = 0; q < 4; ++q) o[q] = bf16_rne(w[q] * (g.scale / (kScaleC * kScaleX)));
+          *reinterpret_cast<u16x4*>(xh + at) = o;
         }
-        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (KP > 64) __builtin_amdgcn_sched_barrier(0);
       }
     }
     __syncthreads();
+  }
+  // Out in 16-byte pieces.
+  uint16_t* out = g.out + blockIdx.x * g.out_mat;
+  if (!g.tall) {
+    const int pieces = lp >> 3;
+    for (int i = threadIdx.x; i < g.k * pieces; i += kSmallThreads) {
+      const int r = i / pieces, c = (i - r * pieces) * 8;
+      store8(out + r * g.out_row + c, *reinterpret_cast<const u32x4*>(xh + x_at<XP>(r, c)), g.out_vec, g.l - c);
+    }
+  } else {
+    for (int c0 = wave * 16; c0 < lp; c0 += kSmallWaves * 16)
+#pragma unroll
+      for (int k0 = 0; k0 < KP; k0 += 32) {
+        const int c = c0 + (lane & 15), r = k0 + (lane >> 4) * 8;
+        const u32x4 piece = __builtin_bit_cast(u32x4, column8<XP>(xh, k0, c0, lane));
+        if (c < g.l) store8(out + c * g.out_row + r, piece, g.out_vec, g.k - r);
+      }
   }
 }
 
@@ -1175,6 +1198,7 @@ hipError_t launch_small(const NsParams& p, const NsInput& in, hipStream_t s) {
   g.out_row = p.out_row;
   g.out_mat = p.out_mat;
   g.tall = p.rows > p.cols;
+  g.out_vec = (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0 && p.out_row % 8 == 0 && p.out_mat % 8 == 0;
   g.k = static_cast<int>(g.tall ? p.cols : p.rows);
   g.l = static_cast<int>(g.tall ? p.rows : p.cols);
   g.lp = (g.l + 31) / 32 * 32;
