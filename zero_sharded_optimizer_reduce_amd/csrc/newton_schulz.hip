@@ -992,7 +992,7 @@ __global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(SmallNs g) {
       v[n] = load8(g.in, base + r * g.in.row, (i - r * per_row) * 8);
     }
   }
-  for (int i = threadIdx.x; i < KP * XP; i += kSmallThreads) reinterpret_cast<uint32_t*>(xh)[i] = 0;   // hi and lo
+  for (int i = threadIdx.x; i < KP * XP / 4; i += kSmallThreads) reinterpret_cast<u32x4*>(xh)[i] = u32x4{};   // hi and lo
 #pragma unroll
   for (int n = 0; n < kGroups; ++n)
 #pragma unroll
@@ -1004,13 +1004,7 @@ __global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(SmallNs g) {
   sum = 0.0;
 #pragma unroll
   for (int i = 0; i < kSmallWaves; ++i) sum += part[i];
-  // a zero matrix stays zero, a sum that is not finite makes everything NaN
-  double mult = 0.0;
-  float add = 0.0f;
-  if (sum > 0.0 && sum < __builtin_huge_val())
-    mult = static_cast<double>(kScaleX) / sqrt(sum);
-  else if (sum != 0.0)
-    add = __builtin_nanf("");
+  const NsScale x = scale_of(sum);
 #pragma unroll
   for (int n = 0; n < kGroups; ++n) {
     const int i = threadIdx.x + n * kSmallThreads;
@@ -1019,7 +1013,7 @@ __global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(SmallNs g) {
       h8 h, l;   // past the end: load8's zeros
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        const float w = c + q < g.in.cols ? static_cast<float>(static_cast<double>(v[n][q]) * mult) + add : 0.0f;
+        const float w = c + q < g.in.cols ? ldexpf(v[n][q], x.e) * x.f + x.add : 0.0f;
         h[q] = static_cast<half_t>(w);
         l[q] = static_cast<half_t>(w - static_cast<float>(h[q]));
       }
