@@ -945,15 +945,12 @@ __device__ __forceinline__ h8 column8(const half_t* m, int k0, int c0, int lane)
   return __builtin_bit_cast(h8, transpose8(m + x_at<XP>(row, col), m + x_at<XP>(row + 4, col)));
 }
 
-__device__ __forceinline__ void split4(acc4 v, half_t* hi, half_t* lo) {
-  h4 h, l;
+__device__ __forceinline__ void split4(acc4 v, h4* hi, h4* lo) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    h[q] = static_cast<half_t>(v[q]);
-    l[q] = static_cast<half_t>(v[q] - static_cast<float>(h[q]));
+    (*hi)[q] = static_cast<half_t>(v[q]);
+    (*lo)[q] = static_cast<half_t>(v[q] - static_cast<float>((*hi)[q]));
   }
-  *reinterpret_cast<h4*>(hi) = h;
-  *reinterpret_cast<h4*>(lo) = l;
 }
 
 constexpr int kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64;
@@ -1032,16 +1029,42 @@ __global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(SmallNs g) {
   }
   __syncthreads();
 
-  constexpr int kSide = KP / 16, kBlocks = kSide * kSide, kMine = (kBlocks + kSmallWaves - 1) / kSmallWaves;
+  // The blocks on and below the diagonal, or, where the waves share them, all.
+  constexpr int kSide = KP / 16, kBlocks = kSplits > 1 ? kSide * kSide : kSide * (kSide + 1) / 2;
+  constexpr int kMine = (kBlocks + kSmallWaves - 1) / kSmallWaves;
+  auto block_row = [](int blk) {
+    return kSplits > 1 ? blk / kSide : (blk >= 1) + (blk >= 3) + (blk >= 6) + (blk >= 10) + (blk >= 15);
+  };
+  auto block_col = [&](int blk) {
+    const int bi = block_row(blk);
+    return kSplits > 1 ? blk % kSide : blk - bi * (bi + 1) / 2;
+  };
   for (int t = 0; t < g.steps; ++t) {
     const float a = g.coefs[3 * t], b = g.coefs[3 * t + 1], c = g.coefs[3 * t + 2];
     asm volatile("" : "+v"(lane));   // the LDS addresses are formed in every step: all of them do not fit the registers
     const int lr = lane & 15, lk = (lane >> 4) * 8, lq = (lane >> 4) * 4;   // a fragment's row, its first k; a result's first row
+    // A block (bi, bj) of A or C, symmetric: the lane's four rows of a column as four
+    // columns of a row, and, off the diagonal, as they are.
+    auto store = [&](acc4 w, int bi, int bj) {
+      const int at = s_at<KP>(bj + lr, bi + lq);
+      h4 h, l;
+      split4(w, &h, &l);
+      *reinterpret_cast<h4*>(sh + at) = h;
+      *reinterpret_cast<h4*>(sl + at) = l;
+      if (kSplits == 1 && bi != bj) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int to = s_at<KP>(bi + lq + q, bj + lr);
+          sh[to] = h[q];
+          sl[to] = l[q];
+        }
+      }
+    };
     // A = X X^T, the wave's blocks
     acc4 am[kMine];
     if constexpr (kSplits > 1) {
       const int blk = wave % kBlocks, part_k = wave / kBlocks;
-      const int bi = blk / kSide * 16, bj = blk % kSide * 16;
+      const int bi = block_row(blk) * 16, bj = block_col(blk) * 16;
       Acc3 s;
 #pragma unroll 2
       for (int k0 = part_k * 32 + lk; k0 < lp; k0 += kSplits * 32)
@@ -1063,7 +1086,7 @@ __global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(SmallNs g) {
         const int blk = wave + n * kSmallWaves;
         Acc3 s;
         if (blk < kBlocks) {
-          const int bi = blk / kSide * 16 + lr, bj = blk % kSide * 16 + lr;
+          const int bi = block_row(blk) * 16 + lr, bj = block_col(blk) * 16 + lr;
 #pragma unroll 4
           for (int k0 = lk; k0 < lp; k0 += 32)
             s.add(row8(xh, x_at<XP>(bi, k0)), row8(xl, x_at<XP>(bi, k0)), row8(xh, x_at<XP>(bj, k0)),
@@ -1077,10 +1100,8 @@ __global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(SmallNs g) {
     for (int n = 0; n < kMine; ++n) {
       const int blk = wave + n * kSmallWaves;
       if (blk < kBlocks) {
-        // symmetric: the lane's four rows of a column are stored as four columns of a row
-        const int at = s_at<KP>(blk % kSide * 16 + lr, blk / kSide * 16 + lq);
         am[n] *= kScaleA / (kScaleX * kScaleX);
-        split4(am[n], sh + at, sl + at);
+        store(am[n], block_row(blk) * 16, block_col(blk) * 16);
       }
     }
     __syncthreads();
@@ -1091,7 +1112,7 @@ __global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(SmallNs g) {
       const int blk = wave + n * kSmallWaves;
       Acc3 s;
       if (blk < kBlocks) {
-        const int bi = blk / kSide * 16 + lr, bj = blk % kSide * 16 + lr;
+        const int bi = block_row(blk) * 16 + lr, bj = block_col(blk) * 16 + lr;
 #pragma unroll
         for (int k0 = 0; k0 < KP; k0 += 32)
           s.add(row8(sh, s_at<KP>(bi, k0 + lk)), row8(sl, s_at<KP>(bi, k0 + lk)), row8(sh, s_at<KP>(bj, k0 + lk)),
@@ -1105,12 +1126,12 @@ __global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(SmallNs g) {
     for (int n = 0; n < kMine; ++n) {
       const int blk = wave + n * kSmallWaves;
       if (blk < kBlocks) {
-        const int r = blk % kSide * 16 + lr, col = blk / kSide * 16 + lq;
+        const int bi = block_row(blk) * 16, bj = block_col(blk) * 16, r = bj + lr, col = bi + lq;
         acc4 w = c * (kScaleC / (kScaleA * kScaleA)) * sq[n] + b * (kScaleC / kScaleA) * am[n];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           if (r == col + q && r < g.k) w[q] += a * kScaleC;
-        split4(w, sh + s_at<KP>(r, col), sl + s_at<KP>(r, col));
+        store(w, bi, bj);
       }
     }
     __syncthreads();
@@ -1137,7 +1158,7 @@ __global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(SmallNs g) {
         acc4 w = s.sum();   // of X^T C: four columns of row bi * 16 + lr
         const int at = x_at<XP>(bi * 16 + lr, c0 + lq);
         if (!last) {
-          split4(w * (1.0f / kScaleC), xh + at, xl + at);
+          split4(w * (1.0f / kScaleC), reinterpret_cast<h4*>(xh + at), reinterpret_cast<h4*>(xl + at));
         } else {   // the result, BF16, in place of hi
           u16x4 o;
 #pragma unroll
