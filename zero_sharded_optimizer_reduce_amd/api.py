@@ -51,6 +51,20 @@ def _dev(t: torch.Tensor, what: str, dtypes) -> int:
     return t.data_ptr()
 
 
+def _dev_same(numel: int, wrong_size: str, *tensors) -> list:
+    """The pointers of (tensor, name, dtypes), checked like _dev, without a call
+    for each that passes: 0.2 instead of 0.35 us."""
+    ptrs = []
+    for t, what, dtypes in tensors:
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == _current_device()
+                and t.dtype in dtypes and t.is_contiguous()):
+            _dev(t, what, dtypes)
+        if t.numel() != numel:
+            raise ValueError(wrong_size)
+        ptrs.append(t.data_ptr())
+    return ptrs
+
+
 def _dev_table(ts: Sequence[torch.Tensor], what: str, dtypes, numel: int, wrong_size: str) -> C.Array:
     """The pointers of equally long device tensors; their names are only formed
     for a refusal."""
@@ -376,10 +390,8 @@ def zero_muon_momentum(momentum: torch.Tensor, direction_out: torch.Tensor, grad
     (BF16) written; grad_scale: a one-element FP32 device tensor that multiplies
     the gradient (the clip coefficient)."""
     n = momentum.numel()
-    ptrs = [_dev(momentum, "momentum", (torch.float32,)), _dev(direction_out, "direction_out", _BF16_LIKE),
-            _dev(grad, "grad", (torch.float32,))]
-    if direction_out.numel() != n or grad.numel() != n:
-        raise ValueError("zero_muon_momentum: all buffers must have the same numel")
+    ptrs = _dev_same(n, "zero_muon_momentum: all buffers must have the same numel", (momentum, "momentum", _FP32),
+                     (direction_out, "direction_out", _BF16_LIKE), (grad, "grad", _FP32))
     h = muon_hparams(hp)
     check(load().zero_muon_momentum(*ptrs, _one_float(grad_scale, "grad_scale"), n, C.byref(h), _stream(stream)),
           "zero_muon_momentum")
@@ -464,10 +476,8 @@ def zero_muon_shard_step(master: torch.Tensor, bf16_out: torch.Tensor, update: t
     """Owner update: master (FP32) -= lr * (update + wd * master), bf16_out
     written; lr_dev: a one-element FP32 device tensor read in place of hp's lr."""
     n = master.numel()
-    ptrs = [_dev(master, "master", (torch.float32,)), _dev(bf16_out, "bf16_out", _BF16_LIKE),
-            _dev(update, "update", _BF16_LIKE)]
-    if bf16_out.numel() != n or update.numel() != n:
-        raise ValueError("zero_muon_shard_step: all buffers must have the same numel")
+    ptrs = _dev_same(n, "zero_muon_shard_step: all buffers must have the same numel", (master, "master", _FP32),
+                     (bf16_out, "bf16_out", _BF16_LIKE), (update, "update", _BF16_LIKE))
     h = muon_hparams(hp)
     check(load().zero_muon_shard_step(*ptrs, n, C.byref(h), _one_float(lr_dev, "lr_dev"), _stream(stream)),
           "zero_muon_shard_step")
