@@ -20,6 +20,7 @@ namespace {
 // rank's contribution starts anywhere.  gfx950 reads them with one 8-byte
 // load at any alignment, so the vector path needs no alignment of its inputs.
 typedef u32x2 u32x2_any __attribute__((aligned(2)));
+__device__ __forceinline__ u32x2 ld_nt_any(const u32x2_any* p) { return __builtin_nontemporal_load(p); }
 
 // The momentum step of one element: m' = b*m + (1-b)*g, direction u = m', or
 // with Nesterov's look-ahead u = (1-b)*g + b*m'.
@@ -116,7 +117,7 @@ __global__ __launch_bounds__(BS) void reduce_momentum_vec_kernel(ReduceMomentumP
       u32x2 x[NMAX];
 #pragma unroll
       for (int r = 0; r < NMAX; ++r)
-        if (r < n) x[r] = ld_nt(reinterpret_cast<const u32x2_any*>(p.g[r]) + i);
+        if (r < n) x[r] = ld_nt_any(reinterpret_cast<const u32x2_any*>(p.g[r]) + i);
       f32x4 m = ld_nt(M + i);
       f32x4 acc;
       if (ACC) acc = ld_nt(GA + i);
@@ -171,7 +172,7 @@ __global__ __launch_bounds__(BS) void muon_update_vec_kernel(MuonUpdateParams a)
       const int64_t len = tile_len(nvec - tile, BS);
       const TileOut<f32x4, true> oP(P + tile, len);
       const TileOut<u32x2, true> oB(B + tile, len);
-      const u32x2 o = ld_nt(O + i);
+      const u32x2 o = ld_nt_any(O + i);
       f32x4 p = ld_nt(P + i);
       p.x = update_elem<WD>(p.x, bf16_lo(o.x), lr, a.wd);
       p.y = update_elem<WD>(p.y, bf16_hi(o.x), lr, a.wd);

@@ -186,7 +186,7 @@ __global__ __launch_bounds__(kNormThreads) void ns_prepare_kernel(NsInput g, NsX
     if (r < g.rows) v[n] = load8(g, base + static_cast<int64_t>(r) * g.row, c0 + c);
   }
   const NsScale s = scale_of(block_sum(
-      threadIdx.x < x.parts ? x.partials[static_cast<int64_t>(mat) * x.parts + threadIdx.x] : 0.0));
+      static_cast<int>(threadIdx.x) < x.parts ? x.partials[static_cast<int64_t>(mat) * x.parts + threadIdx.x] : 0.0));
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) x.f[mat] = s.f;
 #pragma unroll
   for (int n = 0; n < kLines; ++n) {
