@@ -29,8 +29,9 @@ from typing import Callable, Optional, Sequence, Tuple
 
 import torch
 
+from ._lib import ZERO_NORM_BLOCKS
 from .api import (ADAM_SCALARS_FLOATS, NS_COEFS, ZeroOffload, adam_scalars_tensor, zero_adam_scalars_fetch,
-                  zero_adam_shard_step, zero_adam_shard_step_dev, zero_all_gather_layer, zero_grad_norm_sq_no_alloc,
+                  zero_adam_shard_step, zero_adam_shard_step_dev, zero_all_gather_layer, zero_grad_norm_sq,
                   zero_muon_momentum, zero_muon_shard_step, zero_newton_schulz, zero_newton_schulz_workspace,
                   zero_reduce_scatter, zero_reduce_scatter_adam, zero_reduce_scatter_adam_dev,
                   zero_reduce_scatter_muon, zero_shard_layout)
@@ -182,7 +183,7 @@ class MuonStep:
             at, i = end, i + mats
         # one workspace, the stacks run one after the other
         self.workspace = max((zero_newton_schulz_workspace(d) for d, _, _ in self.stacks), key=torch.Tensor.numel)
-        self.grad = self.norm_sq = self.clip = None   # of a clipped step
+        self.grad = self.norm_parts = self.norm_sq = self.clip = None   # of a clipped step
 
     load_master = ShardedStep.load_master
 
@@ -191,14 +192,16 @@ class MuonStep:
                                  stream=stream)
 
     def reduce_momentum_clipped(self, rank_grads, weights, hp, max_norm, stream=None):
-        """The momentum step on gradients whose norm over all owners is held to
-        max_norm: the coefficient stays on the device."""
+        """The momentum step on gradients whose norm over all owners of this unit is
+        held to max_norm: the coefficient stays on the device.  The norm's partial
+        sums are this object's own: steps of other units may overlap with it."""
         if self.grad is None:
             self.grad = [_empty(self.shard, torch.float32, self.device) for _ in range(self.n)]
+            self.norm_parts = _empty(self.n * ZERO_NORM_BLOCKS, torch.float64, self.device)
             self.norm_sq = _empty(1, torch.float64, self.device)
             self.clip = _empty(1, torch.float32, self.device)
         zero_reduce_scatter(rank_grads, weights, self.grad, stream=stream)
-        zero_grad_norm_sq_no_alloc(self.grad, self.norm_sq, max_norm, self.clip, stream=stream)
+        zero_grad_norm_sq(self.grad, self.norm_parts, self.norm_sq, max_norm, self.clip, stream=stream)
         for k in range(self.n):
             zero_muon_momentum(self.momentum[k], self.direction[k], self.grad[k], hp, grad_scale=self.clip,
                                stream=stream)
