@@ -393,11 +393,16 @@ int zero_newton_schulz_workspace(int64_t n_mats, int64_t rows, int64_t cols, int
  *                 zero_newton_schulz_workspace's answer; nothing in it carries
  *                 over between calls.
  * Arithmetic: the norm in FP64 (fixed order); the products on the matrix
- * cores with FP16 operands scaled by powers of two and FP32 accumulation.  With
- * five steps the result is 1.8e-3 to 2.1e-3 of its norm away from the exact one
- * on Gaussian matrices (rounding it to BF16 is 1.66e-3 of that, and all of it for
- * the small matrices one compute unit holds), and up to 5.2e-3 on matrices of
- * rank one.  Results are the same bits on every call with the same inputs.
+ * cores with FP16 operands scaled by powers of two and FP32 accumulation, an FP32
+ * input as pairs of FP16 values (22 bits).  With the five steps (3.4445, -4.7750,
+ * 2.0315) the result, for either input type, is 1.7e-3 to 2.1e-3 of its norm away
+ * from the exact one on Gaussian matrices (rounding it to BF16 is 1.66e-3 of that),
+ * up to 4e-3 on spectra that fall over three decades, up to 7e-3 on matrices of
+ * rank one or with half of the singular values next to nothing, and up to 2e-2 on
+ * matrices of a few distinct values, whose roundings agree and add up.  Small
+ * matrices, which one compute unit holds, are kept as pairs throughout: there the
+ * rounding to BF16 is all of it.  Results are the same bits on every call with the
+ * same inputs.
  * Errors: ZERO_ERR_ARG (NULL, negative sizes, in_dtype, steps, coefficients
  * that are not finite or break the bounds, a scale that is not finite,
  * overlapping buffers), ZERO_ERR_ALIGN, ZERO_ERR_SIZE (strides below the

@@ -12,8 +12,8 @@
 //
 // Blocks of steps.  With C_0, C_1 polynomials of A, two steps are
 //   A' = C_0 A C_0,  C_1 = a I + b A' + c A' A',  X'' = (C_1 C_0) X:
-// a Gram product and a product with X (3 k k l) less and three symmetric k x k
-// products (3 k k k) more than step by step.
+// a Gram product and a product with X (3 k k l) less and three k x k products (3 k k k,
+// 4 where the last of them is not symmetric) more than step by step.
 //
 // Rounding X after the first two steps costs most: the later steps raise what
 // the rounding adds in the directions of small singular values by up to a^3 =
@@ -27,6 +27,11 @@
 // number; products accumulate in FP32.  Rounding X, A and C to 11 bits moves
 // the result by about 1.2e-3 of its norm; the final rounding to BF16 alone is
 // 1.7e-3.  BF16 operands would move it by 1e-2.
+// An FP32 input rounded to FP16 would be noise in every direction, which the steps
+// raise by up to 3.44^5 = 484 where singular values are small: matrices of rank one
+// came out 1.4e-1 off.  The first product with X sums over the remainder too (6.9e-3;
+// 3 of 777 x 1301 197 us instead of 191, 4096 x 4096 1486 instead of 1360); the Gram
+// product need not: it loses no more than by its own rounding.
 #include <hip/hip_runtime.h>
 #include <hip/hip_fp16.h>
 
@@ -151,11 +156,12 @@ __device__ __forceinline__ NsScale scale_of(double sum) {
 
 // ------------------------------------------------------------------ X
 // X * kScaleX = f * (G * 2^e): the stored G * 2^e is exact for BF16 inputs (8
-// bits in 11), and the factor f joins the products' scales, so that nothing is
-// lost before the first product.
+// bits in 11), and of FP32 inputs the remainder is stored too (22 bits); the factor
+// f joins the products' scales, so that nothing is lost before the first product.
 struct NsX {
   half_t* x;         // k x l, pitch pad(l), pad(k) rows: those past k are zeros, here
   half_t* next;      // and in the X that the steps write next
+  half_t* low;       // what G * 2^e leaves of FP32 values, or NULL
   int64_t mat;
   int tall;          // X is G^T
   const double* partials;
@@ -165,8 +171,9 @@ struct NsX {
 
 constexpr int kTurn = 64;
 
-// One 64 x 64 tile to both copies; the padding is written as zeros.  Every
-// workgroup adds the partial sums up itself, while its tile is on its way.
+// One 64 x 64 tile; the padding is written as zeros.  Every workgroup adds the
+// partial sums up itself, while its tile is on its way.
+template <bool LOW>
 __global__ __launch_bounds__(kNormThreads) void ns_prepare_kernel(NsInput g, NsX x) {
   // 33 words a row: the eight rows a lane group gathers lie in different banks
   __shared__ uint32_t tile[kTurn][kTurn / 2 + 1];
@@ -175,6 +182,7 @@ __global__ __launch_bounds__(kNormThreads) void ns_prepare_kernel(NsInput g, NsX
   const int ld = static_cast<int>(pad_up(x.tall ? g.rows : g.cols));
   half_t* out = x.x + mat * x.mat;
   half_t* next = x.next + mat * x.mat;
+  half_t* low = LOW ? x.low + mat * x.mat : nullptr;
   const int64_t base = static_cast<int64_t>(mat) * g.mat;
   const int line = threadIdx.x >> 3, c = (threadIdx.x & 7) * 8;
   constexpr int kLines = kTurn / (kNormThreads / 8);
@@ -189,33 +197,41 @@ __global__ __launch_bounds__(kNormThreads) void ns_prepare_kernel(NsInput g, NsX
       static_cast<int>(threadIdx.x) < x.parts ? x.partials[static_cast<int64_t>(mat) * x.parts + threadIdx.x] : 0.0));
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) x.f[mat] = s.f;
 #pragma unroll
-  for (int n = 0; n < kLines; ++n) {
-    const int i = line + n * (kNormThreads / 8), r = r0 + i;
-    h8 h;
+  for (int half = 0; half < (LOW ? 2 : 1); ++half) {
+    half_t* to = half ? low : out;
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-      h[q] = r < g.rows && c0 + c + q < g.cols ? static_cast<half_t>(ldexpf(v[n][q], s.e) + s.add) : half_t(0);
-    if (!x.tall) {
-      *reinterpret_cast<h8*>(out + static_cast<int64_t>(r) * ld + c0 + c) = h;
-      if (r >= g.rows) *reinterpret_cast<h8*>(next + static_cast<int64_t>(r) * ld + c0 + c) = h;
+    for (int n = 0; n < kLines; ++n) {
+      const int i = line + n * (kNormThreads / 8), r = r0 + i;
+      h8 h;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float w = r < g.rows && c0 + c + q < g.cols ? ldexpf(v[n][q], s.e) + s.add : 0.0f;
+        const half_t hi = static_cast<half_t>(w);
+        h[q] = half ? static_cast<half_t>(w - static_cast<float>(hi)) : hi;
+      }
+      if (!x.tall) {
+        *reinterpret_cast<h8*>(to + static_cast<int64_t>(r) * ld + c0 + c) = h;
+        if (!half && r >= g.rows) *reinterpret_cast<h8*>(next + static_cast<int64_t>(r) * ld + c0 + c) = h;
+      }
+      const u32x4 w = __builtin_bit_cast(u32x4, h);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tile[i][c / 2 + q] = w[q];
     }
-    const u32x4 w = __builtin_bit_cast(u32x4, h);
+    if (!x.tall) continue;
+    __syncthreads();
 #pragma unroll
-    for (int q = 0; q < 4; ++q) tile[i][c / 2 + q] = w[q];
-  }
-  if (!x.tall) return;
-  __syncthreads();
+    for (int i = line; i < kTurn; i += kNormThreads / 8) {
+      u32x4 w;
 #pragma unroll
-  for (int i = line; i < kTurn; i += kNormThreads / 8) {
-    u32x4 w;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t a = tile[c + 2 * q][i >> 1], b = tile[c + 2 * q + 1][i >> 1];
-      w[q] = i & 1 ? (a >> 16) | (b & 0xFFFF0000u) : (a & 0xFFFFu) | (b << 16);
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t a = tile[c + 2 * q][i >> 1], b = tile[c + 2 * q + 1][i >> 1];
+        w[q] = i & 1 ? (a >> 16) | (b & 0xFFFF0000u) : (a & 0xFFFFu) | (b << 16);
+      }
+      const int64_t at = static_cast<int64_t>(c0 + i) * ld + r0 + c;
+      *reinterpret_cast<u32x4*>(to + at) = w;
+      if (!half && c0 + i >= g.cols) *reinterpret_cast<u32x4*>(next + at) = w;
     }
-    const int64_t at = static_cast<int64_t>(c0 + i) * ld + r0 + c;
-    *reinterpret_cast<u32x4*>(out + at) = w;
-    if (c0 + i >= g.cols) *reinterpret_cast<u32x4*>(next + at) = w;
+    if (LOW && !half) __syncthreads();   // the tile is read
   }
 }
 
@@ -226,12 +242,15 @@ __global__ __launch_bounds__(kNormThreads) void ns_prepare_kernel(NsInput g, NsX
 // the tiles on the diagonal ride: P's rows of diagonal tile i are those of tile
 // (i, i - 1), whose workgroup computes both.
 // kTimesX: Q^T is X itself, rows in order of the summed index.
+// SUMS: 2: Q is the pair q + q_lo of FP16 matrices, and the sum runs over q, then,
+// with P again, over q_lo.
 enum Shape { kFull, kSym, kRide, kTimesX };
 enum Epilogue { kPlain, kPoly, kCarryOut, kCarryIn, kOut };
 struct Product {
   const half_t* p;
   const half_t* q;
   int64_t p_mat, q_mat;
+  int64_t q_lo;             // elements from q to its low half
   int p_ld, q_ld;
   int m, n, kk;
   int tiles_n, tiles;       // per matrix
@@ -262,13 +281,13 @@ constexpr int kBk = 64;      // summed index per stage: rows of 128 bytes in LDS
 // cache line (rows of 64 bytes ran at 55 instead of 95 bytes/ns per CU).  Rows
 // past the matrix's end hold something else of the workspace, which ends
 // kTile rows after the last matrix; their results are dropped.
-template <int R, int NW>
+template <int R, int NW, int SUMS>
 struct Stager {
   static constexpr int kN = R / 8 / NW;
   static_assert(kN * 8 * NW == R && kN % 2 == 0, "every wave moves the same number of pieces, an even one");
   __amdgpu_buffer_rsrc_t rsrc, none;   // none: no bytes in range, a load through it reads nothing
   int voff[2], step, wave, end;        // voff: even and odd groups of 8 rows
-  __device__ __forceinline__ Stager(const half_t* mat, int ld, int row0, int kk, int wave_, int lane)
+  __device__ __forceinline__ Stager(const half_t* mat, int ld, int row0, int kk, int wave_, int lane, int64_t = 0)
       : wave(wave_), end(kk) {
     half_t* base = const_cast<half_t*>(mat + static_cast<int64_t>(row0) * ld);
     rsrc = __builtin_amdgcn_make_buffer_rsrc(base, 0, R * ld * 2, 0x00020000);
@@ -282,7 +301,8 @@ struct Stager {
   // counted, but from nowhere.
   __device__ __forceinline__ void one(half_t* lds, int k0, int i) const {
 #ifdef __HIP_DEVICE_COMPILE__   // the builtin is unknown to the host pass
-    const bool live = k0 < end;
+    const bool live = k0 < SUMS * end;
+    if (SUMS > 1 && k0 >= end) k0 -= end;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(live ? rsrc : none, (lds_void*)(lds + (wave * kN + i) * 8 * kBk), 16,
                                              voff[i & 1], live ? k0 * 2 + i * step : 0, 0, 0);
 #endif
@@ -298,14 +318,15 @@ struct Stager {
 // together: the 64-byte piece c of row r lies at piece c ^ (r & 3) (C = 64, where
 // two rows fill the banks: c ^ ((r >> 1) & 1)).  Columns past the end hold the
 // next row; their results are dropped.
-template <int C, int NW>
+template <int C, int NW, int SUMS>
 struct ColumnStager {
   static constexpr int kRows = 512 / C, kN = 64 / kRows / NW;   // rows of one instruction, instructions of a wave
   static_assert(kN * kRows * NW == 64 && (C != 256 || kN % 2 == 0), "every wave moves the same number of pieces");
   half_t* base;
+  int64_t lo;
   int voff[2], ld, wave, end;   // voff: even and odd instructions
-  __device__ __forceinline__ ColumnStager(const half_t* mat, int ld_, int col0, int kk, int wave_, int lane)
-      : base(const_cast<half_t*>(mat + col0)), ld(ld_), wave(wave_), end(kk) {
+  __device__ __forceinline__ ColumnStager(const half_t* mat, int ld_, int col0, int kk, int wave_, int lane, int64_t lo_)
+      : base(const_cast<half_t*>(mat + col0)), lo(lo_), ld(ld_), wave(wave_), end(kk) {
     const int row = lane / (64 / kRows), piece = lane % (64 / kRows);
 #pragma unroll
     for (int odd = 0; odd < 2; ++odd) {
@@ -315,10 +336,10 @@ struct ColumnStager {
   }
   __device__ __forceinline__ void one(half_t* lds, int k0, int i) const {
 #ifdef __HIP_DEVICE_COMPILE__
-    const bool live = k0 < end;
+    const bool live = k0 < SUMS * end, low = SUMS > 1 && k0 >= end;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        __builtin_amdgcn_make_buffer_rsrc(base + static_cast<int64_t>(k0) * ld, 0, live ? kBk * ld * 2 : 0,
-                                          0x00020000),
+        __builtin_amdgcn_make_buffer_rsrc(base + (low ? lo : 0) + static_cast<int64_t>(low ? k0 - end : k0) * ld, 0,
+                                          live ? kBk * ld * 2 : 0, 0x00020000),
         (lds_void*)(lds + (wave * kN + i) * 512), 16, voff[i & 1], live ? i * kRows * ld * 2 : 0, 0, 0);
 #endif
   }
@@ -456,7 +477,7 @@ __device__ __forceinline__ float block_sum_f32(float x, float* part) {
 // on one half the wave reads the next one's fragments, and the loads are issued
 // evenly between the products (a wave issues in order: loads in a row
 // hold its products up while the CU takes them in, about 26 clocks each).
-template <int BM, int BN, int WR, int WC, Shape SHAPE, Epilogue EPI, bool DEEP = false>
+template <int BM, int BN, int WR, int WC, Shape SHAPE, Epilogue EPI, bool DEEP, int SUMS>
 __global__ __launch_bounds__(WR * WC * 64, BM <= 128 ? 2 : 1) void ns_product_kernel(Product g) {
   constexpr int NW = WR * WC;
   constexpr int TM = BM / WR / 32, TN = BN / WC / 32;   // 32 x 32 blocks of a wave
@@ -508,13 +529,15 @@ __global__ __launch_bounds__(WR * WC * 64, BM <= 128 ? 2 : 1) void ns_product_ke
     tj = t - ti * g.tiles_n;
   }
   const int row0 = ti * BM, col0 = tj * BN;
-  const Stager<BM, NW> sp(g.p + mat * g.p_mat, g.p_ld, row0, g.kk, wave, lane);
-  using QStager = std::conditional_t<SHAPE == kTimesX, ColumnStager<BN, NW>, Stager<BN, NW>>;
-  const QStager sq(g.q + mat * g.q_mat, g.q_ld, col0, g.kk, wave, lane);
+  static_assert(SUMS == 1 || SHAPE == kTimesX, "pairs are X's");
+  using PStager = Stager<BM, NW, SUMS>;
+  const PStager sp(g.p + mat * g.p_mat, g.p_ld, row0, g.kk, wave, lane);
+  using QStager = std::conditional_t<SHAPE == kTimesX, ColumnStager<BN, NW, SUMS>, Stager<BN, NW, SUMS>>;
+  const QStager sq(g.q + mat * g.q_mat, g.q_ld, col0, g.kk, wave, lane, g.q_lo);
   const int wr = wave / WC, wc = wave - wr * WC;
   int at_p = lane_at(wr * (BM / WR), lane);
   int at_q = SHAPE == kTimesX ? lane_at_column<BN>(wc * (BN / WC), lane) : lane_at(wc * (BN / WC), lane);
-  constexpr int kP = Stager<BM, NW>::kN, kQ = QStager::kN;
+  constexpr int kP = PStager::kN, kQ = QStager::kN;
   // The lane's values of block (i, j): row lane & 31 of the block, columns 8 * u +
   // 4 * (lane >> 5) + q (the products take Q's fragment first).
   float alpha = g.alpha;
@@ -735,7 +758,7 @@ __global__ __launch_bounds__(WR * WC * 64, BM <= 128 ? 2 : 1) void ns_product_ke
         __builtin_amdgcn_s_waitcnt(wait_vm_lds(3 * (kP + kQ)));   // the next stage has arrived, and this one is read
         wave_barrier();
         half([&](int s) { sp.one(p0, k0 + 5 * kBk, s); }, kP, f1, f0, p1, q1, 0);
-        return (k0 += kBk) < g.kk;
+        return (k0 += kBk) < SUMS * g.kk;
       };
       sp.all(slot0, 0);
       sq.all(slot5, 0);
@@ -763,7 +786,7 @@ __global__ __launch_bounds__(WR * WC * 64, BM <= 128 ? 2 : 1) void ns_product_ke
         __builtin_amdgcn_s_waitcnt(wait_vm_lds(kP));
         wave_barrier();
         half([&](int s) { sq.one(p0, k0 + 2 * kBk, s); }, kQ, f1, f0, p1, q1, 0);
-        return (k0 += kBk) < g.kk;
+        return (k0 += kBk) < SUMS * g.kk;
       };
       sp.all(slot0, 0);
       sq.all(slot1, 0);
@@ -809,11 +832,11 @@ int64_t tile_count(const Product& g, int side, Shape shape) {
   return shape == kSym ? tm * (tm + 1) / 2 : tm > 2 ? tm * (tm - 1) / 2 : tm;
 }
 
-template <int BM, int BN, int WR, int WC, Shape SHAPE, Epilogue EPI, bool DEEP = false>
+template <int BM, int BN, int WR, int WC, Shape SHAPE, Epilogue EPI, bool DEEP = false, int SUMS = 1>
 hipError_t product_tiles(Product g, int64_t mats, hipStream_t s) {
   g.tiles_n = (g.n + BN - 1) / BN;
   g.tiles = static_cast<int>(tile_count(g, BM, SHAPE));
-  hipLaunchKernelGGL((ns_product_kernel<BM, BN, WR, WC, SHAPE, EPI, DEEP>), dim3(static_cast<unsigned>(g.tiles * mats)),
+  hipLaunchKernelGGL((ns_product_kernel<BM, BN, WR, WC, SHAPE, EPI, DEEP, SUMS>), dim3(static_cast<unsigned>(g.tiles * mats)),
                      dim3(WR * WC * 64), 0, s, g);
   return hipGetLastError();
 }
@@ -826,7 +849,9 @@ hipError_t product_tiles(Product g, int64_t mats, hipStream_t s) {
 // 3 of 777 x 1301, 189, 225, 321; 3000 x 3000, 1069, 847, 865; 4096 x 4096, 2240,
 // 1693, 1430.  With C X's forced: 2 of 1024 x 4096, 319 with 64, 259 with 128, 269
 // with 256; 4096 x 4096, 2193, 1554, 1416.
-template <Shape SHAPE, Epilogue EPI>
+// With SUMS 2 the choice is that of one sum: the roundings that a product hands to the
+// next lie in the order of its tiles.
+template <Shape SHAPE, Epilogue EPI, int SUMS = 1>
 hipError_t product(const Product& g, int64_t mats, hipStream_t s) {
   constexpr Shape kOwn = SHAPE == kRide ? kSym : SHAPE;
   constexpr bool kTri = kOwn == kSym;
@@ -851,21 +876,21 @@ hipError_t product(const Product& g, int64_t mats, hipStream_t s) {
       }
       if (ride) return product_tiles<64, 64, 2, 2, kRide, EPI>(g, mats, s);
     }
-    return product_tiles<64, 64, 2, 2, kOwn, EPI>(g, mats, s);
+    return product_tiles<64, 64, 2, 2, kOwn, EPI, false, SUMS>(g, mats, s);
   }
-  if (t128 <= large) return product_tiles<128, 128, 2, 2, kOwn, EPI>(g, mats, s);
+  if (t128 <= large) return product_tiles<128, 128, 2, 2, kOwn, EPI, false, SUMS>(g, mats, s);
   if constexpr (kTri)
-    return product_tiles<192, 192, 2, 2, kOwn, EPI>(g, mats, s);
+    return product_tiles<192, 192, 2, 2, kOwn, EPI, false, SUMS>(g, mats, s);
   else
-    return product_tiles<256, 256, 2, 4, kOwn, EPI>(g, mats, s);
+    return product_tiles<256, 256, 2, 4, kOwn, EPI, false, SUMS>(g, mats, s);
 }
 
-// The workspace: partial sums and factors, X and the next X, three
-// k x k matrices, each for all matrices.
+// The workspace: partial sums and factors, X and the next X, what FP32 inputs leave
+// of the first X, three k x k matrices, X's roundings, each for all matrices.
 struct Layout {
   int64_t k, l, kp, lp;
   int64_t e_mat;                                   // rounding errors of one matrix: whole tiles
-  int64_t partials, f, x[2], sq[3], e, bytes;  // byte offsets
+  int64_t partials, f, x[2], low, sq[3], e, bytes;  // byte offsets
   Layout(int64_t mats, int64_t rows, int64_t cols) {
     k = rows < cols ? rows : cols;
     l = rows < cols ? cols : rows;
@@ -880,6 +905,7 @@ struct Layout {
     partials = take(mats * kNormParts * 8);
     f = take(mats * 4);
     for (int64_t& o : x) o = take(mats * kp * lp * 2);
+    low = take(mats * kp * lp * 2);
     for (int64_t& o : sq) o = take(mats * k * kp * 2);
     e_mat = (k + kTile - 1) / kTile * kTile * ((l + kTile - 1) / kTile * kTile);
     e = take(mats * e_mat * 2);
@@ -1259,6 +1285,7 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
                    reinterpret_cast<half_t*>(ws + w.sq[2])};
   float* f = reinterpret_cast<float*>(ws + w.f);
   half_t* e = reinterpret_cast<half_t*>(ws + w.e);
+  half_t* low = p.in_f32 ? reinterpret_cast<half_t*>(ws + w.low) : nullptr;
   const int64_t x_mat = w.kp * w.lp, sq_mat = w.k * w.kp;
 
   double* partials = reinterpret_cast<double*>(ws + w.partials);
@@ -1270,15 +1297,18 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
   NsX nx;
   nx.x = x[0];
   nx.next = x[1];
+  nx.low = low;
   nx.mat = x_mat;
   nx.tall = tall;
   nx.partials = partials;
   nx.parts = parts;
   nx.f = f;
-  hipLaunchKernelGGL(ns_prepare_kernel,
-                     dim3(static_cast<unsigned>(pad_up(p.cols) / kTurn), static_cast<unsigned>(pad_up(p.rows) / kTurn),
-                          static_cast<unsigned>(p.mats)),
-                     dim3(kNormThreads), 0, s, in, nx);
+  const dim3 turns(static_cast<unsigned>(pad_up(p.cols) / kTurn), static_cast<unsigned>(pad_up(p.rows) / kTurn),
+                   static_cast<unsigned>(p.mats));
+  if (low)
+    hipLaunchKernelGGL(ns_prepare_kernel<true>, turns, dim3(kNormThreads), 0, s, in, nx);
+  else
+    hipLaunchKernelGGL(ns_prepare_kernel<false>, turns, dim3(kNormThreads), 0, s, in, nx);
   err = hipGetLastError();
   if (err != hipSuccess) return err;
 
@@ -1351,6 +1381,12 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
     g.carry_out = e;
     g.carry_in = e;
     g.carry_mat = w.e_mat;
+    if (first && low) {
+      g.q_lo = low - x[0];
+      if (last) return product<kTimesX, kOut, 2>(g, p.mats, s);
+      if (carry == kCarryOut) return product<kTimesX, kCarryOut, 2>(g, p.mats, s);
+      return product<kTimesX, kPlain, 2>(g, p.mats, s);
+    }
     if (last) return product<kTimesX, kOut>(g, p.mats, s);
     if (carry == kCarryOut) return product<kTimesX, kCarryOut>(g, p.mats, s);
     if (carry == kCarryIn) return product<kTimesX, kCarryIn>(g, p.mats, s);
