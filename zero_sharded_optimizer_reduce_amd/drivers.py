@@ -24,6 +24,7 @@ arithmetic step runs in the HIP kernels of libzero.
 """
 from __future__ import annotations
 
+import contextlib
 import math
 from typing import Callable, Optional, Sequence, Tuple
 
@@ -39,6 +40,14 @@ from .api import (ADAM_SCALARS_FLOATS, NS_COEFS, ZeroOffload, adam_scalars_tenso
 
 def _empty(n, dtype, device):
     return torch.empty(int(n), dtype=dtype, device=device)
+
+
+def _allocating_on(stream):
+    """Tensors made inside belong to `stream` (None: the current one): what the
+    allocator hands out may still be in use on the stream that it came back on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
 class ShardedStep:
@@ -196,10 +205,11 @@ class MuonStep:
         held to max_norm: the coefficient stays on the device.  The norm's partial
         sums are this object's own: steps of other units may overlap with it."""
         if self.grad is None:
-            self.grad = [_empty(self.shard, torch.float32, self.device) for _ in range(self.n)]
-            self.norm_parts = _empty(self.n * ZERO_NORM_BLOCKS, torch.float64, self.device)
-            self.norm_sq = _empty(1, torch.float64, self.device)
-            self.clip = _empty(1, torch.float32, self.device)
+            with _allocating_on(stream):
+                self.grad = [_empty(self.shard, torch.float32, self.device) for _ in range(self.n)]
+                self.norm_parts = _empty(self.n * ZERO_NORM_BLOCKS, torch.float64, self.device)
+                self.norm_sq = _empty(1, torch.float64, self.device)
+                self.clip = _empty(1, torch.float32, self.device)
         zero_reduce_scatter(rank_grads, weights, self.grad, stream=stream)
         zero_grad_norm_sq(self.grad, self.norm_parts, self.norm_sq, max_norm, self.clip, stream=stream)
         for k in range(self.n):
