@@ -538,16 +538,14 @@ static void ns_step_bound(double a, double b, double c, double top, double* p_ma
     const double x = -b / (2.0 * c);  // vertex of a + b x + c x^2, x = s^2
     if (x > 0.0 && x < top * top) rm = std::fmax(rm, r(x));
   }
-  // stationary points: a + 3 b x + 5 c x^2 = 0
+  // stationary points: a + 3 b x + 5 c x^2 = 0, from the root that adds up: with c
+  // next to 0 the other sum would lose the point near -a / 3b
   double x[2] = {-1.0, -1.0};
-  if (c != 0.0) {
-    const double d = 9.0 * b * b - 20.0 * a * c;
-    if (d >= 0.0) {
-      x[0] = (-3.0 * b + std::sqrt(d)) / (10.0 * c);
-      x[1] = (-3.0 * b - std::sqrt(d)) / (10.0 * c);
-    }
-  } else if (b != 0.0) {
-    x[0] = -a / (3.0 * b);
+  const double d = 9.0 * b * b - 20.0 * a * c;
+  if (d >= 0.0) {
+    const double q = -0.5 * (3.0 * b + std::copysign(std::sqrt(d), b));
+    if (c != 0.0) x[0] = q / (5.0 * c);
+    if (q != 0.0) x[1] = a / q;
   }
   for (double v : x)
     if (v > 0.0 && v < top * top) pm = std::fmax(pm, p(std::sqrt(v)));
