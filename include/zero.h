@@ -382,7 +382,9 @@ int zero_newton_schulz_workspace(int64_t n_mats, int64_t rows, int64_t cols, int
  * and the singular vectors stay.  The result does not depend on the input's
  * scale.  A matrix holding a NaN or an infinity gives NaN throughout.
  *   in            device, BF16 or FP32 (in_dtype), element (i, j) of matrix q
- *                 at in[q*in_mat_stride + i*in_row_stride + j].
+ *                 at in[q*in_mat_stride + i*in_row_stride + j].  No two
+ *                 elements may share a place; matrices may be column ranges
+ *                 of one wider buffer.
  *   out           device, BF16, laid out likewise with its own strides.
  *   coefs         host array of 3*steps floats, steps in [1, 16].  They must
  *                 keep the singular values (from [0, 1] on) within
@@ -405,8 +407,8 @@ int zero_newton_schulz_workspace(int64_t n_mats, int64_t rows, int64_t cols, int
  * same inputs.
  * Errors: ZERO_ERR_ARG (NULL, negative sizes, in_dtype, steps, coefficients
  * that are not finite or break the bounds, a scale that is not finite,
- * overlapping buffers), ZERO_ERR_ALIGN, ZERO_ERR_SIZE (strides below the
- * matrix's extent, sides above ZERO_NS_MAX_SIDE, more than ZERO_NS_MAX_MATS
+ * overlapping buffers), ZERO_ERR_ALIGN, ZERO_ERR_SIZE (strides with which
+ * elements share a place, sides above ZERO_NS_MAX_SIDE, more than ZERO_NS_MAX_MATS
  * matrices, a small workspace), ZERO_ERR_HIP. */
 int zero_newton_schulz(const void* in, int in_dtype, int64_t in_row_stride, int64_t in_mat_stride,
                        uint16_t* out, int64_t out_row_stride, int64_t out_mat_stride, int64_t n_mats,

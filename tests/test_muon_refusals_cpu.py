@@ -19,3 +19,54 @@ def test_a_maximum_inside_is_seen_whatever_the_last_coefficient(libzero, c):
     assert _call(libzero, coefs=(7.9, -7.9, c)) == -1
     assert b"singular values" in libzero.zero_last_error()
     assert _call(libzero, coefs=(5.0, -5.0, c)) == 0
+
+
+# ----------------------------------------------------------------- strides
+# A workspace of 256 bytes is refused after the strides have passed.
+def _strides(L, mats, rows, cols, irow, imat, orow=None, omat=None):
+    orow, omat = (cols, rows * cols) if orow is None else (orow, omat)
+    st = _call(L, mats=mats, rows=rows, cols=cols, irow=irow, imat=imat, orow=orow, omat=omat, nbytes=256)
+    assert st == -3
+    return L.zero_last_error().decode()
+
+
+def test_matrices_side_by_side_in_a_wider_buffer(libzero):
+    # heads, or gate and up, as column ranges of one buffer
+    assert "needed" in _strides(libzero, 2, 64, 96, 192, 96)
+    assert "needed" in _strides(libzero, 2, 64, 96, 96, 64 * 96, 192, 96)     # the output
+    assert "needed" in _strides(libzero, 32, 4096, 128, 32 * 128, 128)
+    assert "overlap" in _strides(libzero, 2, 64, 96, 191, 96)
+    assert "overlap" in _strides(libzero, 2, 64, 96, 192, 95)
+    assert "overlap" in _strides(libzero, 3, 64, 96, 192, 96)
+    assert "overlap" in _strides(libzero, 2, 64, 96, 96, 64 * 96, 192, 95)
+
+
+def _disjoint(mats, rows, cols, row, mat):
+    seen = set()
+    for q in range(mats):
+        for i in range(rows):
+            for j in range(cols):
+                at = q * mat + i * row + j
+                if at in seen:
+                    return False
+                seen.add(at)
+    return True
+
+
+def test_strides_pass_exactly_where_no_two_elements_meet(libzero):
+    for mats in (1, 2, 3, 4):
+        for rows in (1, 2, 3, 5):
+            for cols in (1, 2, 4):
+                for row in range(cols if rows > 1 else 0, 14):
+                    for mat in range(0, 34):
+                        msg = _strides(libzero, mats, rows, cols, row, mat)
+                        assert ("needed" in msg) == _disjoint(mats, rows, cols, row, mat), (mats, rows, cols, row, mat, msg)
+
+
+def test_strides_at_the_limits(libzero):
+    big = (1 << 62) // 70000
+    assert "needed" in _strides(libzero, 65535, 2, 3, 3 * 65535, 3)
+    assert "overlap" in _strides(libzero, 65535, 2, 3, 3 * 65535 - 1, 3)
+    for row, mat in ((big, 1), (1, big), (big, big), (1 << 62, 0), (0, 1 << 62), (1 << 62, 1 << 62)):
+        msg = _strides(libzero, 65535, 262144, 1, row, mat)
+        assert "overlap" in msg or "out of range" in msg or "below cols" in msg or "needed" in msg

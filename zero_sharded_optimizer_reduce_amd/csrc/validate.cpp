@@ -581,6 +581,23 @@ static int64_t stack_bytes(int64_t mats, int64_t rows, int64_t cols, int64_t row
   return ((mats - 1) * mat_stride + (rows - 1) * row_stride + cols) * elem;
 }
 
+// Whether two matrices share an element: matrices one after the other do not, nor,
+// say, column ranges of one wider buffer.  Matrix i's first row starts i * mat_stride
+// past that of matrix 0, whose rows start every row_stride >= cols and are cols long:
+// only the last row at or before it and the next one can come close.
+static bool matrices_meet(int64_t mats, int64_t rows, int64_t cols, int64_t row_stride, int64_t mat_stride) {
+  if (mats == 1) return false;
+  const int64_t last = (rows - 1) * row_stride;   // of matrix 0, its last row's start
+  for (int64_t i = 1; i < mats; ++i) {
+    const int64_t at = i * mat_stride;
+    if (at >= last + cols) return false;          // and so are all that follow
+    if (rows == 1) return true;
+    const int64_t row = at / row_stride, past = at - row * row_stride;
+    if (past < cols || (row + 1 < rows && row_stride - past < cols)) return true;
+  }
+  return false;
+}
+
 static int check_ns_strides(const char* name, int64_t mats, int64_t rows, int64_t cols, int64_t row_stride,
                             int64_t mat_stride, Err& e) {
   if (rows > 1 && row_stride < cols)
@@ -588,7 +605,7 @@ static int check_ns_strides(const char* name, int64_t mats, int64_t rows, int64_
   if (row_stride < 0 || mat_stride < 0 || mul_overflows(rows, row_stride) ||
       mul_overflows(mats, mat_stride) || rows * row_stride > INT64_MAX / 16 - mats * mat_stride)
     return set_err(e, ZERO_ERR_SIZE, "newton_schulz: %s strides out of range", name);
-  if (mats > 1 && mat_stride < (rows - 1) * row_stride + cols)
+  if (matrices_meet(mats, rows, cols, row_stride, mat_stride))
     return set_err(e, ZERO_ERR_SIZE, "newton_schulz: %s matrices overlap", name);
   return ZERO_OK;
 }
