@@ -389,7 +389,9 @@ int zero_newton_schulz_workspace(int64_t n_mats, int64_t rows, int64_t cols, int
  *   coefs         host array of 3*steps floats, steps in [1, 16].  They must
  *                 keep the singular values (from [0, 1] on) within
  *                 ZERO_NS_MAX_SIGMA and a step's gain |p(s)/s| within
- *                 ZERO_NS_MAX_GAIN.
+ *                 ZERO_NS_MAX_GAIN, with room for roundings: a set whose results
+ *                 reach values from which the next steps raise them further is
+ *                 refused (see below).
  *   scale         finite factor of the result.
  *   workspace     device, 256-byte aligned, workspace_bytes >=
  *                 zero_newton_schulz_workspace's answer; nothing in it carries
@@ -403,10 +405,21 @@ int zero_newton_schulz_workspace(int64_t n_mats, int64_t rows, int64_t cols, int
  * rank one or with half of the singular values next to nothing, and up to 2e-2 on
  * matrices of a few distinct values, whose roundings agree and add up.  Small
  * matrices, which one compute unit holds, are kept as pairs throughout: there the
- * rounding to BF16 is all of it.  Results are the same bits on every call with the
- * same inputs.
+ * rounding to BF16 is all of it.
+ * Other coefficients raise roundings more or less.  From them alone the library
+ * estimates by how much: over singular values from 2^-10 to 1, of the result's
+ * singular values, of its singular vectors, and in the directions of singular values
+ * next to nothing.  Where the estimate is not far above the five steps' (six of
+ * them, cubic steps up to ten, quintics that start near 4 s), errors stay below 2.5e-2.
+ * Where it is, every matrix is kept as pairs, for about three times the time: errors
+ * are the result's own rounding to BF16, at most 2^-8, and 2^-22 times the estimate.
+ * For singular values that is at most 2^-6, or the set is refused with ZERO_ERR_ARG.
+ * In the directions of singular values next to nothing it is the sum over the steps t
+ * of the products |a_t ... a_last|, whatever that is: many steps that each raise the
+ * smallest singular values raise the last bits of X as well.
+ * Results are the same bits on every call with the same inputs.
  * Errors: ZERO_ERR_ARG (NULL, negative sizes, in_dtype, steps, coefficients
- * that are not finite or break the bounds, a scale that is not finite,
+ * that are not finite, break the bounds or leave no room for roundings, a scale that is not finite,
  * overlapping buffers), ZERO_ERR_ALIGN, ZERO_ERR_SIZE (strides with which
  * elements share a place, sides above ZERO_NS_MAX_SIDE, more than ZERO_NS_MAX_MATS
  * matrices, a small workspace), ZERO_ERR_HIP. */

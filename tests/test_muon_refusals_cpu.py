@@ -70,3 +70,32 @@ def test_strides_at_the_limits(libzero):
     for row, mat in ((big, 1), (1, big), (big, big), (1 << 62, 0), (0, 1 << 62), (1 << 62, 1 << 62)):
         msg = _strides(libzero, 65535, 262144, 1, row, mat)
         assert "overlap" in msg or "out of range" in msg or "below cols" in msg or "needed" in msg
+
+
+# ------------------------------------------------- coefficients and roundings
+# Five steps, each the best quintic for the range that the last one leaves: results
+# reach 1.99, where the next polynomial's slope is 10.
+MINIMAX = ((8.28721201814563, -23.595886519098837, 17.300387312530933),
+           (4.107059111542203, -2.9478499167379106, 0.5448431082926601),
+           (3.9486908534822946, -2.908902115962949, 0.5518191394370137),
+           (3.3184196573706015, -2.488488024314874, 0.51004894012372),
+           (2.300652019954817, -1.6689039845749493, 0.4188073119525673))
+
+
+def _divided(by):
+    return [v for a, b, c in MINIMAX for v in (a / by, b / by ** 3, c / by ** 5)]
+
+
+def test_a_set_without_room_for_a_rounding_is_refused(libzero):
+    assert _call(libzero, coefs=_divided(1.0)) == -1
+    assert b"rounding" in libzero.zero_last_error()
+    for by in (1.01, 1.02, 1.05):
+        assert _call(libzero, coefs=_divided(by)) == 0
+    assert _call(libzero, coefs=_divided(1.0)[:3]) == 0      # what grows is the steps after the first
+
+
+@pytest.mark.parametrize("coefs", [(3.4445, -4.7750, 2.0315) * 16, (1.5, -0.5, 0.0) * 16, (1.875, -1.25, 0.375) * 16,
+                                   (3.4445, -4.7750, 2.0315) * 5 + (1.5, -0.5, 0.0) * 5, (1e-3, 0.0, 0.0),
+                                   (0.0, 0.0, 0.0) * 3, (-1.0, 0.0, 0.0) * 4, (5.125, -5.125, 0.0)])
+def test_sets_with_room_are_taken(libzero, coefs):
+    assert _call(libzero, coefs=coefs) == 0

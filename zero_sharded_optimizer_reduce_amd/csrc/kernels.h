@@ -111,6 +111,7 @@ struct NsParams {
   int64_t in_row, in_mat, out_row, out_mat;  // strides in elements
   int64_t mats, rows, cols;
   int steps, in_f32;
+  int pairs;            // operands as pairs of FP16 values; see check_ns_coefs
   float scale;
 };
 

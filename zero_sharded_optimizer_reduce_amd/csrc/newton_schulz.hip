@@ -32,6 +32,8 @@
 // came out 1.4e-1 off.  The first product with X sums over the remainder too (6.9e-3;
 // 3 of 777 x 1301 197 us instead of 191, 4096 x 4096 1486 instead of 1360); the Gram
 // product need not: it loses no more than by its own rounding.
+// Steps that raise roundings further (see check_ns_coefs) run one by one with X, A
+// and C as pairs of FP16 values, 22 bits, in three sums per product.
 #include <hip/hip_runtime.h>
 #include <hip/hip_fp16.h>
 
@@ -161,12 +163,13 @@ __device__ __forceinline__ NsScale scale_of(double sum) {
 struct NsX {
   half_t* x;         // k x l, pitch pad(l), pad(k) rows: those past k are zeros, here
   half_t* next;      // and in the X that the steps write next
-  half_t* low;       // what G * 2^e leaves of FP32 values, or NULL
   int64_t mat;
   int tall;          // X is G^T
   const double* partials;
   int parts;
   float* f;          // per matrix, for the products
+  half_t* low;       // what rounding G * 2^e left (nothing of BF16 values), or NULL
+  half_t* next_low;  // the next X's low half, or NULL
 };
 
 constexpr int kTurn = 64;
@@ -183,6 +186,7 @@ __global__ __launch_bounds__(kNormThreads) void ns_prepare_kernel(NsInput g, NsX
   half_t* out = x.x + mat * x.mat;
   half_t* next = x.next + mat * x.mat;
   half_t* low = LOW ? x.low + mat * x.mat : nullptr;
+  half_t* next_low = LOW && x.next_low ? x.next_low + mat * x.mat : nullptr;
   const int64_t base = static_cast<int64_t>(mat) * g.mat;
   const int line = threadIdx.x >> 3, c = (threadIdx.x & 7) * 8;
   constexpr int kLines = kTurn / (kNormThreads / 8);
@@ -196,22 +200,27 @@ __global__ __launch_bounds__(kNormThreads) void ns_prepare_kernel(NsInput g, NsX
   const NsScale s = scale_of(block_sum(
       static_cast<int>(threadIdx.x) < x.parts ? x.partials[static_cast<int64_t>(mat) * x.parts + threadIdx.x] : 0.0));
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) x.f[mat] = s.f;
+  h8 hi[kLines], lo[kLines];
+#pragma unroll
+  for (int n = 0; n < kLines; ++n)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const bool in = r0 + line + n * (kNormThreads / 8) < g.rows && c0 + c + q < g.cols;
+      const float w = in ? ldexpf(v[n][q], s.e) + s.add : 0.0f;
+      hi[n][q] = static_cast<half_t>(w);
+      lo[n][q] = static_cast<half_t>(w - static_cast<float>(hi[n][q]));
+    }
 #pragma unroll
   for (int half = 0; half < (LOW ? 2 : 1); ++half) {
     half_t* to = half ? low : out;
+    half_t* zeros = half ? next_low : next;
 #pragma unroll
     for (int n = 0; n < kLines; ++n) {
       const int i = line + n * (kNormThreads / 8), r = r0 + i;
-      h8 h;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float w = r < g.rows && c0 + c + q < g.cols ? ldexpf(v[n][q], s.e) + s.add : 0.0f;
-        const half_t hi = static_cast<half_t>(w);
-        h[q] = half ? static_cast<half_t>(w - static_cast<float>(hi)) : hi;
-      }
+      const h8 h = half ? lo[n] : hi[n];
       if (!x.tall) {
         *reinterpret_cast<h8*>(to + static_cast<int64_t>(r) * ld + c0 + c) = h;
-        if (!half && r >= g.rows) *reinterpret_cast<h8*>(next + static_cast<int64_t>(r) * ld + c0 + c) = h;
+        if (zeros && r >= g.rows) *reinterpret_cast<h8*>(zeros + static_cast<int64_t>(r) * ld + c0 + c) = h;
       }
       const u32x4 w = __builtin_bit_cast(u32x4, h);
 #pragma unroll
@@ -229,7 +238,7 @@ __global__ __launch_bounds__(kNormThreads) void ns_prepare_kernel(NsInput g, NsX
       }
       const int64_t at = static_cast<int64_t>(c0 + i) * ld + r0 + c;
       *reinterpret_cast<u32x4*>(to + at) = w;
-      if (!half && c0 + i >= g.cols) *reinterpret_cast<u32x4*>(next + at) = w;
+      if (zeros && c0 + i >= g.cols) *reinterpret_cast<u32x4*>(zeros + at) = w;
     }
     if (LOW && !half) __syncthreads();   // the tile is read
   }
@@ -242,15 +251,15 @@ __global__ __launch_bounds__(kNormThreads) void ns_prepare_kernel(NsInput g, NsX
 // the tiles on the diagonal ride: P's rows of diagonal tile i are those of tile
 // (i, i - 1), whose workgroup computes both.
 // kTimesX: Q^T is X itself, rows in order of the summed index.
-// SUMS: 2: Q is the pair q + q_lo of FP16 matrices, and the sum runs over q, then,
-// with P again, over q_lo.
+// SUMS: 2: Q is a pair of FP16 matrices, high + low, and the sum runs over P with the
+// high half, then with the low one.  3: P and the result are pairs too: high high +
+// high low + low high; the result's halves are written one after the other.
 enum Shape { kFull, kSym, kRide, kTimesX };
 enum Epilogue { kPlain, kPoly, kCarryOut, kCarryIn, kOut };
 struct Product {
   const half_t* p;
   const half_t* q;
   int64_t p_mat, q_mat;
-  int64_t q_lo;             // elements from q to its low half
   int p_ld, q_ld;
   int m, n, kk;
   int tiles_n, tiles;       // per matrix
@@ -268,6 +277,7 @@ struct Product {
   half_t* carry_out;        // the FP16 roundings of d, in the lanes' own order, or NULL
   const half_t* carry_in;   // those of the X this product reads, or NULL
   int64_t carry_mat;
+  int64_t p_lo, q_lo, d_lo, add_lo;   // elements from a matrix to its low half
 };
 
 constexpr int kTile = 256;    // the largest tile
@@ -281,15 +291,17 @@ constexpr int kBk = 64;      // summed index per stage: rows of 128 bytes in LDS
 // cache line (rows of 64 bytes ran at 55 instead of 95 bytes/ns per CU).  Rows
 // past the matrix's end hold something else of the workspace, which ends
 // kTile rows after the last matrix; their results are dropped.
-template <int R, int NW, int SUMS>
+// LOW: the sum that takes the operand's low half.
+template <int R, int NW, int SUMS, int LOW>
 struct Stager {
   static constexpr int kN = R / 8 / NW;
   static_assert(kN * 8 * NW == R && kN % 2 == 0, "every wave moves the same number of pieces, an even one");
   __amdgpu_buffer_rsrc_t rsrc, none;   // none: no bytes in range, a load through it reads nothing
+  half_t* base;
+  int64_t low;
   int voff[2], step, wave, end;        // voff: even and odd groups of 8 rows
-  __device__ __forceinline__ Stager(const half_t* mat, int ld, int row0, int kk, int wave_, int lane, int64_t = 0)
-      : wave(wave_), end(kk) {
-    half_t* base = const_cast<half_t*>(mat + static_cast<int64_t>(row0) * ld);
+  __device__ __forceinline__ Stager(const half_t* mat, int ld, int row0, int kk, int wave_, int lane, int64_t low_)
+      : base(const_cast<half_t*>(mat + static_cast<int64_t>(row0) * ld)), low(low_), wave(wave_), end(kk) {
     rsrc = __builtin_amdgcn_make_buffer_rsrc(base, 0, R * ld * 2, 0x00020000);
     none = __builtin_amdgcn_make_buffer_rsrc(base, 0, 0, 0x00020000);
     const int r = wave * kN * 8 + (lane >> 3);
@@ -302,9 +314,13 @@ struct Stager {
   __device__ __forceinline__ void one(half_t* lds, int k0, int i) const {
 #ifdef __HIP_DEVICE_COMPILE__   // the builtin is unknown to the host pass
     const bool live = k0 < SUMS * end;
-    if (SUMS > 1 && k0 >= end) k0 -= end;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(live ? rsrc : none, (lds_void*)(lds + (wave * kN + i) * 8 * kBk), 16,
-                                             voff[i & 1], live ? k0 * 2 + i * step : 0, 0, 0);
+    const int sum = SUMS == 1 || k0 < end ? 0 : SUMS == 2 || k0 < 2 * end ? 1 : 2;
+    k0 -= sum * end;
+    // (a choice between kept descriptors would put them into memory)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        LOW >= SUMS ? (live ? rsrc : none)
+                    : __builtin_amdgcn_make_buffer_rsrc(base + (sum == LOW ? low : 0), 0, live ? R / 8 * step : 0, 0x00020000),
+        (lds_void*)(lds + (wave * kN + i) * 8 * kBk), 16, voff[i & 1], live ? k0 * 2 + i * step : 0, 0, 0);
 #endif
   }
   __device__ __forceinline__ void all(half_t* lds, int k0) const {
@@ -336,9 +352,10 @@ struct ColumnStager {
   }
   __device__ __forceinline__ void one(half_t* lds, int k0, int i) const {
 #ifdef __HIP_DEVICE_COMPILE__
-    const bool live = k0 < SUMS * end, low = SUMS > 1 && k0 >= end;
+    const bool live = k0 < SUMS * end;
+    const int sum = SUMS == 1 || k0 < end ? 0 : SUMS == 2 || k0 < 2 * end ? 1 : 2;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        __builtin_amdgcn_make_buffer_rsrc(base + (low ? lo : 0) + static_cast<int64_t>(low ? k0 - end : k0) * ld, 0,
+        __builtin_amdgcn_make_buffer_rsrc(base + (sum == 1 ? lo : 0) + static_cast<int64_t>(k0 - sum * end) * ld, 0,
                                           live ? kBk * ld * 2 : 0, 0x00020000),
         (lds_void*)(lds + (wave * kN + i) * 512), 16, voff[i & 1], live ? i * kRows * ld * 2 : 0, 0, 0);
 #endif
@@ -529,10 +546,11 @@ __global__ __launch_bounds__(WR * WC * 64, BM <= 128 ? 2 : 1) void ns_product_ke
     tj = t - ti * g.tiles_n;
   }
   const int row0 = ti * BM, col0 = tj * BN;
-  static_assert(SUMS == 1 || SHAPE == kTimesX, "pairs are X's");
-  using PStager = Stager<BM, NW, SUMS>;
-  const PStager sp(g.p + mat * g.p_mat, g.p_ld, row0, g.kk, wave, lane);
-  using QStager = std::conditional_t<SHAPE == kTimesX, ColumnStager<BN, NW, SUMS>, Stager<BN, NW, SUMS>>;
+  static_assert(SHAPE != kRide || SUMS == 1, "a riding tile takes both operands from P's rows in LDS");
+  static_assert(SUMS != 3 || EPI == kPlain || EPI == kPoly || EPI == kOut, "pairs carry no roundings");
+  using PStager = Stager<BM, NW, SUMS, 2>;
+  const PStager sp(g.p + mat * g.p_mat, g.p_ld, row0, g.kk, wave, lane, g.p_lo);
+  using QStager = std::conditional_t<SHAPE == kTimesX, ColumnStager<BN, NW, SUMS>, Stager<BN, NW, SUMS, 1>>;
   const QStager sq(g.q + mat * g.q_mat, g.q_ld, col0, g.kk, wave, lane, g.q_lo);
   const int wr = wave / WC, wc = wave - wr * WC;
   int at_p = lane_at(wr * (BM / WR), lane);
@@ -560,15 +578,16 @@ __global__ __launch_bounds__(WR * WC * 64, BM <= 128 ? 2 : 1) void ns_product_ke
   uint16_t* mine = reinterpret_cast<uint16_t*>((wave & 3) == 0 ? slot0 : (wave & 3) == 1 ? slot1 : (wave & 3) == 2 ? slot2 : slot3) +
                    (wave >> 2) * kPart;
   // A tile on the diagonal of a symmetric product: only what lies below the
-  // diagonal of its 32 x 32 blocks is kept, as for the tiles.
-  auto write = [&](const f16 (&acc)[TM][TN], int row0, int col0, float gain) {
+  // diagonal of its 32 x 32 blocks is kept, as for the tiles.  low: the low half.
+  auto write = [&](const f16 (&acc)[TM][TN], int row0, int col0, float gain, auto low) {
+    constexpr bool LOW = decltype(low)::value;
     const int wrow = row0 + wr * (BM / WR), wcol = col0 + wc * (BN / WC);
     const bool diagonal = SYM && row0 == col0;
 #pragma unroll
     for (int ib = 0; ib < TM; ib += kBand) {
       const int64_t carry = mat * g.carry_mat + static_cast<int64_t>(t) * (BM * BN) + threadIdx.x * 4;
       // what joins the products: all loads of the band before the first use
-      h4 more[kBand][TN][4];
+      h4 more[kBand][TN][4], more_lo[kBand][TN][4];
       if constexpr (EPI == kPoly || EPI == kCarryIn) {
 #pragma unroll
         for (int i = 0; i < kBand; ++i)
@@ -579,8 +598,10 @@ __global__ __launch_bounds__(WR * WC * 64, BM <= 128 ? 2 : 1) void ns_product_ke
               if constexpr (EPI == kPoly) {
                 const int r = wrow + (ib + i) * 32 + lm, c = wcol + j * 32 + u * 8 + ln;
                 // past the edge: some other value, dropped below
-                more[i][j][u] = *reinterpret_cast<const h4*>(
-                    g.add + mat * g.d_mat + static_cast<int64_t>(r < g.m ? r : 0) * g.d_ld + (c < g.d_ld ? c : 0));
+                const half_t* at =
+                    g.add + mat * g.d_mat + static_cast<int64_t>(r < g.m ? r : 0) * g.d_ld + (c < g.d_ld ? c : 0);
+                more[i][j][u] = *reinterpret_cast<const h4*>(at);
+                if constexpr (SUMS == 3) more_lo[i][j][u] = *reinterpret_cast<const h4*>(at + g.add_lo);
               } else {
                 more[i][j][u] =
                     *reinterpret_cast<const h4*>(g.carry_in + carry + (((ib + i) * TN + j) * 4 + u) * (NW * 256));
@@ -598,7 +619,11 @@ __global__ __launch_bounds__(WR * WC * 64, BM <= 128 ? 2 : 1) void ns_product_ke
             for (int q = 0; q < 4; ++q) v[q] = acc[ib + i][j][u * 4 + q] * alpha;
             if constexpr (EPI == kPoly) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) v[q] += g.beta * static_cast<float>(more[i][j][u][q]);
+              for (int q = 0; q < 4; ++q) {
+                float a = static_cast<float>(more[i][j][u][q]);
+                if constexpr (SUMS == 3) a += static_cast<float>(more_lo[i][j][u][q]);
+                v[q] += g.beta * a;
+              }
               if (i == j && diagonal && wr == wc) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -616,7 +641,13 @@ __global__ __launch_bounds__(WR * WC * 64, BM <= 128 ? 2 : 1) void ns_product_ke
             } else {
               h4 h;
 #pragma unroll
-              for (int q = 0; q < 4; ++q) h[q] = static_cast<half_t>(v[q]);
+              for (int q = 0; q < 4; ++q) {
+                // Rounded to FP32 here: folded into the rounding to FP16 in one of the
+                // two passes, the halves would now and then be those of two values.
+                if constexpr (SUMS == 3) asm volatile("" : "+v"(v[q]));
+                h[q] = static_cast<half_t>(v[q]);
+                if constexpr (LOW) h[q] = static_cast<half_t>(v[q] - static_cast<float>(h[q]));
+              }
               o = __builtin_bit_cast(u16x4, h);
               if constexpr (EPI == kCarryOut) {
                 h4 w;
@@ -664,7 +695,7 @@ __global__ __launch_bounds__(WR * WC * 64, BM <= 128 ? 2 : 1) void ns_product_ke
           }
         }
       } else {
-        half_t* d = g.d + mat * g.d_mat + static_cast<int64_t>(brow) * g.d_ld + wcol;
+        half_t* d = g.d + (LOW ? g.d_lo : 0) + mat * g.d_mat + static_cast<int64_t>(brow) * g.d_ld + wcol;
 #pragma unroll 1
         for (int k0 = 0; k0 < kPieces; k0 += kStep) {
           u32x4 piece[kStep];
@@ -682,7 +713,7 @@ __global__ __launch_bounds__(WR * WC * 64, BM <= 128 ? 2 : 1) void ns_product_ke
           }
         }
         if constexpr (SYM) {   // its transpose
-          half_t* dt = g.d + mat * g.d_mat + static_cast<int64_t>(wcol) * g.d_ld + brow;
+          half_t* dt = g.d + (LOW ? g.d_lo : 0) + mat * g.d_mat + static_cast<int64_t>(wcol) * g.d_ld + brow;
 #pragma unroll 1
           for (int k0 = 0; k0 < kPieces; k0 += kStep) {
             // 16 columns, 8 rows of each 8 * (lane >> 4) rows on
@@ -810,8 +841,12 @@ __global__ __launch_bounds__(WR * WC * 64, BM <= 128 ? 2 : 1) void ns_product_ke
       for (int i = threadIdx.x; i < g.m; i += NW * 64) sum += static_cast<float>(c[static_cast<int64_t>(i) * g.p_ld + i]);
       gain = block_sum_f32<NW>(sum, reinterpret_cast<float*>(slot4)) * g.alpha / (static_cast<float>(g.m) * kScaleE);
     }
-    write(acc, row0, col0, gain);
-    if constexpr (SECOND) write(acc2, row0, row0, gain);
+    write(acc, row0, col0, gain, std::false_type());
+    if constexpr (SUMS == 3 && EPI != kOut) {
+      asm volatile("" : "+v"(alpha));   // the scaled sums are formed anew: kept, they would not fit the registers
+      write(acc, row0, col0, gain, std::true_type());
+    }
+    if constexpr (SECOND) write(acc2, row0, row0, gain, std::false_type());
   };
   const bool second = rides && wr >= wc;   // above the diagonal nothing is kept
   if constexpr (SHAPE == kRide) {
@@ -849,7 +884,7 @@ hipError_t product_tiles(Product g, int64_t mats, hipStream_t s) {
 // 3 of 777 x 1301, 189, 225, 321; 3000 x 3000, 1069, 847, 865; 4096 x 4096, 2240,
 // 1693, 1430.  With C X's forced: 2 of 1024 x 4096, 319 with 64, 259 with 128, 269
 // with 256; 4096 x 4096, 2193, 1554, 1416.
-// With SUMS 2 the choice is that of one sum: the roundings that a product hands to the
+// With two sums the choice is that of one: the roundings that a product hands to the
 // next lie in the order of its tiles.
 template <Shape SHAPE, Epilogue EPI, int SUMS = 1>
 hipError_t product(const Product& g, int64_t mats, hipStream_t s) {
@@ -858,7 +893,7 @@ hipError_t product(const Product& g, int64_t mats, hipStream_t s) {
   auto rounds = [&](int side, Shape shape) { return (tile_count(g, side, shape) * mats + 255) / 256; };
   const bool ride = SHAPE == kRide && rounds(64, kRide) < rounds(64, kSym);
   auto time = [&](int64_t n, double us, double fixed, double launch) {
-    return static_cast<double>(n) * (us * g.kk / 4096.0 + fixed) + launch;
+    return static_cast<double>(n) * (us * (SUMS == 3 ? 3 : 1) * g.kk / 4096.0 + fixed) + launch;
   };
   const double large = kTri ? time(rounds(192, kOwn), 66.0, 11.0, 2.0) : time(rounds(256, kOwn), 115.0, 11.0, 2.0);
   const double t128 = time(rounds(128, kOwn), 32.0, 5.0, 3.0);
@@ -885,12 +920,13 @@ hipError_t product(const Product& g, int64_t mats, hipStream_t s) {
     return product_tiles<256, 256, 2, 4, kOwn, EPI, false, SUMS>(g, mats, s);
 }
 
-// The workspace: partial sums and factors, X and the next X, what FP32 inputs leave
-// of the first X, three k x k matrices, X's roundings, each for all matrices.
+// The workspace: partial sums and factors, X and the next X, three k x k matrices, X's
+// roundings or the low half of the next X, the low half of X, a fourth k x k matrix,
+// each for all matrices.
 struct Layout {
   int64_t k, l, kp, lp;
   int64_t e_mat;                                   // rounding errors of one matrix: whole tiles
-  int64_t partials, f, x[2], low, sq[3], e, bytes;  // byte offsets
+  int64_t partials, f, x[2], sq[3], e, low, sq_low, bytes;  // byte offsets
   Layout(int64_t mats, int64_t rows, int64_t cols) {
     k = rows < cols ? rows : cols;
     l = rows < cols ? cols : rows;
@@ -905,10 +941,11 @@ struct Layout {
     partials = take(mats * kNormParts * 8);
     f = take(mats * 4);
     for (int64_t& o : x) o = take(mats * kp * lp * 2);
-    low = take(mats * kp * lp * 2);
     for (int64_t& o : sq) o = take(mats * k * kp * 2);
     e_mat = (k + kTile - 1) / kTile * kTile * ((l + kTile - 1) / kTile * kTile);
     e = take(mats * e_mat * 2);
+    low = take(mats * kp * lp * 2);
+    sq_low = take(mats * k * kp * 2);
     bytes = at + kTile * (lp > kp ? lp : kp) * 2;   // rows that the last tiles read past their matrix
   }
 };
@@ -1281,11 +1318,11 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
   const int k = static_cast<int>(w.k), l = static_cast<int>(w.l), kp = static_cast<int>(w.kp),
             lp = static_cast<int>(w.lp);
   half_t* x[2] = {reinterpret_cast<half_t*>(ws + w.x[0]), reinterpret_cast<half_t*>(ws + w.x[1])};
-  half_t* sq[3] = {reinterpret_cast<half_t*>(ws + w.sq[0]), reinterpret_cast<half_t*>(ws + w.sq[1]),
-                   reinterpret_cast<half_t*>(ws + w.sq[2])};
+  half_t* sq[4] = {reinterpret_cast<half_t*>(ws + w.sq[0]), reinterpret_cast<half_t*>(ws + w.sq[1]),
+                   reinterpret_cast<half_t*>(ws + w.sq[2]), reinterpret_cast<half_t*>(ws + w.sq_low)};
   float* f = reinterpret_cast<float*>(ws + w.f);
   half_t* e = reinterpret_cast<half_t*>(ws + w.e);
-  half_t* low = p.in_f32 ? reinterpret_cast<half_t*>(ws + w.low) : nullptr;
+  half_t* low = p.in_f32 || p.pairs ? reinterpret_cast<half_t*>(ws + w.low) : nullptr;
   const int64_t x_mat = w.kp * w.lp, sq_mat = w.k * w.kp;
 
   double* partials = reinterpret_cast<double*>(ws + w.partials);
@@ -1298,6 +1335,7 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
   nx.x = x[0];
   nx.next = x[1];
   nx.low = low;
+  nx.next_low = p.pairs ? e : nullptr;
   nx.mat = x_mat;
   nx.tall = tall;
   nx.partials = partials;
@@ -1351,6 +1389,16 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
     g.f_pow = 2;
     return product<kRide, kPlain>(g, p.mats, s);
   };
+  // The last product with X goes to the output.
+  auto result = [&](Product g, float c_scale) {
+    g.alpha = p.scale / (c_scale * kScaleX);
+    g.out = p.out;
+    g.out_row = p.out_row;
+    g.out_mat = p.out_mat;
+    g.out_vec = (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0 && p.out_row % 8 == 0 && p.out_mat % 8 == 0;
+    g.out_turned = tall;
+    return g;
+  };
   // X = C X into the other X, the last step's into the output.
   auto apply = [&](const half_t* c, float c_scale, int from, bool first, bool last, Epilogue carry) {
     Product g = {};
@@ -1366,12 +1414,7 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
     g.n = l;
     g.kk = kp;
     if (last) {
-      g.alpha = p.scale / (c_scale * kScaleX);
-      g.out = p.out;
-      g.out_row = p.out_row;
-      g.out_mat = p.out_mat;
-      g.out_vec = (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0 && p.out_row % 8 == 0 && p.out_mat % 8 == 0;
-      g.out_turned = tall;
+      g = result(g, c_scale);
     } else {
       g.alpha = 1.0f / c_scale;
       g.d = x[from ^ 1];
@@ -1398,6 +1441,64 @@ hipError_t launch_newton_schulz(const NsParams& p, hipStream_t s) {
   auto run = [&](auto&& launch) {
     if (st == hipSuccess) st = launch();
   };
+  if (p.pairs) {
+    // Step by step, every matrix a pair: A in sq[0] and sq[2], C in sq[1] and sq[3].
+    half_t* x_low[2] = {low, e};
+    for (int t = 0; t < p.steps; ++t) {
+      const int cur = t & 1;
+      const float* c = p.coefs + 3 * t;
+      Product a = {};
+      a.p = a.q = x[cur];
+      a.p_lo = a.q_lo = x_low[cur] - x[cur];
+      a.p_mat = a.q_mat = x_mat;
+      a.p_ld = a.q_ld = lp;
+      a.m = a.n = k;
+      a.kk = lp;
+      a.d = sq[0];
+      a.d_lo = sq[2] - sq[0];
+      a.d_mat = sq_mat;
+      a.d_ld = kp;
+      a.alpha = kScaleA / (kScaleX * kScaleX);
+      a.f = t == 0 ? f : nullptr;
+      a.f_pow = 2;
+      Product q = a;
+      q.p = q.q = q.add = sq[0];
+      q.p_lo = q.q_lo = q.add_lo = sq[2] - sq[0];
+      q.p_mat = q.q_mat = sq_mat;
+      q.p_ld = q.q_ld = q.kk = kp;
+      q.d = sq[1];
+      q.d_lo = sq[3] - sq[1];
+      q.alpha = c[2] * (kScaleC / (kScaleA * kScaleA));
+      q.beta = c[1] * (kScaleC / kScaleA);
+      q.diag = c[0] * kScaleC;
+      q.f = nullptr;
+      Product y = {};
+      y.p = sq[1];
+      y.p_lo = sq[3] - sq[1];
+      y.p_mat = sq_mat;
+      y.p_ld = y.kk = kp;
+      y.q = x[cur];
+      y.q_lo = x_low[cur] - x[cur];
+      y.q_mat = x_mat;
+      y.q_ld = lp;
+      y.m = k;
+      y.n = l;
+      y.f = t == 0 ? f : nullptr;
+      y.f_pow = 1;
+      y.alpha = 1.0f / kScaleC;
+      y.d = x[cur ^ 1];
+      y.d_lo = x_low[cur ^ 1] - x[cur ^ 1];
+      y.d_mat = x_mat;
+      y.d_ld = lp;
+      run([&] { return product<kSym, kPlain, 3>(a, p.mats, s); });
+      run([&] { return product<kSym, kPoly, 3>(q, p.mats, s); });
+      if (t < p.steps - 1)
+        run([&] { return product<kTimesX, kPlain, 3>(y, p.mats, s); });
+      else
+        run([&] { return product<kTimesX, kOut, 3>(result(y, kScaleC), p.mats, s); });
+    }
+    return st;
+  }
   // Steps t and t + 1 as one product with X: its factor C' C into sq[0].
   auto pair = [&](int t, int from, bool first) {
     run([&] { return gram(x[from], sq[0], first); });

@@ -553,7 +553,79 @@ static void ns_step_bound(double a, double b, double c, double top, double* p_ma
   *r_max = rm;
 }
 
-int check_ns_coefs(const float* coefs, int steps, Err& e) {
+// How far the steps raise roundings, in units of an operand's rounding (half a step,
+// relative), over singular values that start at 2^-10 to 1:
+//   value  a result's singular value, relative (at least to 1/8): each step's factor is
+//          off by as much of |a| + 2 |b| s^2 + 3 |c| s^4 (C and, twice, A), and what
+//          was there is taken on with the polynomial's slope;
+//   turn   a result's singular vectors: the factor's diagonal, |a|, or of the first two
+//          steps together |a a'|, is rounded entry by entry, against what the
+//          factor makes of s;
+//   rest   the directions of no singular value, where X's roundings lie, those of X
+//          after two steps carried (see newton_schulz.hip): the sum over the later
+//          X of the products of |a| that follow.
+struct NsRaised {
+  float value, turn, rest;
+};
+
+// In five steps the quintic 3.4445, -4.7750, 2.0315 raises roundings by (208, 24, 15),
+// in six by (300, 28, 56); five steps that start at 4.1 to 2.8 s, by (86, 55, 11).  With
+// one FP16 value (11 bits) per operand their results are at most 2.2e-2 off, over
+// spectra of every kind.  Seven quintics, (504, 31, 197): 5e-2.  Five steps that are
+// each the best for what the last one leaves, (663, 117, 10): 7e-2, and 2.5e-1 from
+// FP32.  The limits lie between.  With pairs of FP16 values (22 bits) the latter come
+// out within the result's rounding to BF16, for three times the products and their
+// step by step form: 4096 x 4096 in seven steps 5.2 ms instead of 1.84, 32 of
+// 512 x 1024 1.03 ms instead of 0.43.
+constexpr float kNsPairsValue = 500.0f, kNsPairsTurn = 64.0f, kNsPairsRest = 60.0f;
+// With 22 bits this much is 2^-6 of the result.  Sixteen quintics raise by 1.1e4; a set
+// that takes singular values to where the next polynomial's slope is 10, and so on, by
+// 2.9e5: there a single rounding decides whether the results grow.
+constexpr float kNsMostRaised = 65536.0f;
+
+// Singular values 2^(-10 i / 63).
+struct NsSamples {
+  static constexpr int kCount = 64;
+  float s[kCount];
+  constexpr NsSamples() : s() {
+    double v = 1.0;
+    for (int i = 0; i < kCount; ++i, v *= 0.895770256) s[i] = static_cast<float>(v);
+  }
+};
+
+static NsRaised ns_raised(const float* coefs, int steps) {
+  static constexpr NsSamples samples;
+  constexpr int kSamples = NsSamples::kCount;
+  float s[kSamples], first[kSamples], err[kSamples], turn[kSamples];   // floats: four at a time
+  for (int i = 0; i < kSamples; ++i) {
+    s[i] = first[i] = samples.s[i];
+    err[i] = turn[i] = 0.0f;
+  }
+  NsRaised r = {0.0f, 0.0f, 0.0f};
+  for (int t = 0; t < steps; ++t) {
+    const float a = coefs[3 * t], b = coefs[3 * t + 1], c = coefs[3 * t + 2];
+    const float fa = std::fabs(a), fb = 2.0f * std::fabs(b), fc = 3.0f * std::fabs(c);
+    const bool pair = t == 0 && steps > 1;   // its factor is rounded with the next step's
+    const float lead = t == 1 ? fa * std::fabs(coefs[0]) : fa;
+    for (int i = 0; i < kSamples; ++i) {
+      const float x = s[i] * s[i], from = t == 1 ? first[i] : s[i];
+      const float next = std::fabs((a + (b + c * x) * x) * s[i]);
+      err[i] = std::fabs(a + (3.0f * b + 5.0f * c * x) * x) * err[i] + (fa + (fb + fc * x) * x) * s[i];
+      first[i] = s[i];
+      s[i] = next;
+      if (!pair) turn[i] += lead * from / (next > 0.0625f ? next : 0.0625f);
+    }
+    if (t >= 2) r.rest = t == 2 ? 0.0f : (r.rest + 1.0f) * fa;
+  }
+  for (int i = 0; i < kSamples; ++i) {
+    const float rel = err[i] / (s[i] > 0.125f ? s[i] : 0.125f);
+    if (!(rel <= r.value)) r.value = rel;
+    if (!(turn[i] <= r.turn)) r.turn = turn[i];
+  }
+  return r;
+}
+
+int check_ns_coefs(const float* coefs, int steps, Err& e, bool* pairs) {
   if (!coefs) return set_err(e, ZERO_ERR_ARG, "newton_schulz: NULL coefficients");
   if (steps < 1 || steps > ZERO_NS_MAX_STEPS)
     return set_err(e, ZERO_ERR_ARG, "newton_schulz: steps=%d outside [1,%d]", steps, ZERO_NS_MAX_STEPS);
@@ -572,6 +644,11 @@ int check_ns_coefs(const float* coefs, int steps, Err& e) {
                      t, p_max, r_max, ZERO_NS_MAX_SIGMA, ZERO_NS_MAX_GAIN);
     top = p_max;
   }
+  const NsRaised r = ns_raised(coefs, steps);
+  if (pairs) *pairs = r.value > kNsPairsValue || r.turn > kNsPairsTurn || r.rest > kNsPairsRest;
+  if (!(r.value <= kNsMostRaised))
+    return set_err(e, ZERO_ERR_ARG, "newton_schulz: the steps raise a rounding to %g of itself (limit %g): no room "
+                   "between the values they reach and where they grow", r.value, kNsMostRaised);
   return ZERO_OK;
 }
 
@@ -614,8 +691,8 @@ int check_newton_schulz(const void* in, int in_dtype, int64_t in_row_stride, int
                         const uint16_t* out, int64_t out_row_stride, int64_t out_mat_stride,
                         int64_t n_mats, int64_t rows, int64_t cols, const float* coefs, int steps,
                         float scale, const void* workspace, int64_t workspace_bytes,
-                        int64_t workspace_need, Err& e) {
-  int st = check_ns_coefs(coefs, steps, e);
+                        int64_t workspace_need, Err& e, bool* pairs) {
+  int st = check_ns_coefs(coefs, steps, e, pairs);
   if (st) return st;
   if (in_dtype != ZERO_BF16 && in_dtype != ZERO_FP32)
     return set_err(e, ZERO_ERR_ARG, "newton_schulz: in_dtype=%d is neither ZERO_BF16 nor ZERO_FP32", in_dtype);

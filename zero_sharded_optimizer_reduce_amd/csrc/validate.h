@@ -99,12 +99,14 @@ int check_reduce_scatter_muon(const uint16_t* const* rank_grads, const float* ra
 int check_muon_shard(const float* master, const uint16_t* bf16_out, const uint16_t* update,
                      const float* lr_dev, int64_t n, const zero_muon_hparams* hp, Err& e);
 int check_ns_shape(int64_t n_mats, int64_t rows, int64_t cols, Err& e);
-int check_ns_coefs(const float* coefs, int steps, Err& e);
+// pairs: set where the steps raise roundings so far that one FP16 value per operand
+// will not do.
+int check_ns_coefs(const float* coefs, int steps, Err& e, bool* pairs = nullptr);
 int check_newton_schulz(const void* in, int in_dtype, int64_t in_row_stride, int64_t in_mat_stride,
                         const uint16_t* out, int64_t out_row_stride, int64_t out_mat_stride,
                         int64_t n_mats, int64_t rows, int64_t cols, const float* coefs, int steps,
                         float scale, const void* workspace, int64_t workspace_bytes,
-                        int64_t workspace_need, Err& e);
+                        int64_t workspace_need, Err& e, bool* pairs = nullptr);
 
 // Alignment tests for the kernels' vector paths.
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

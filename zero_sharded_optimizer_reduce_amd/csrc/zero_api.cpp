@@ -520,11 +520,12 @@ int zero_newton_schulz(const void* in, int in_dtype, int64_t in_row_stride, int6
                        void* workspace, int64_t workspace_bytes, void* stream) {
   TraceRange tr("zero_newton_schulz");
   Err e;
+  bool pairs = false;
   int st = check_ns_shape(n_mats, rows, cols, e);
   if (st) return fail(st, e.msg);
   st = check_newton_schulz(in, in_dtype, in_row_stride, in_mat_stride, out, out_row_stride, out_mat_stride,
                            n_mats, rows, cols, coefs, steps, scale, workspace, workspace_bytes,
-                           ns_workspace_bytes(n_mats, rows, cols), e);
+                           ns_workspace_bytes(n_mats, rows, cols), e, &pairs);
   if (st) return fail(st, e.msg);
   if (n_mats == 0 || rows == 0 || cols == 0) return ZERO_OK;
   NsParams p;
@@ -542,6 +543,7 @@ int zero_newton_schulz(const void* in, int in_dtype, int64_t in_row_stride, int6
   p.cols = cols;
   p.steps = steps;
   p.in_f32 = in_dtype == ZERO_FP32;
+  p.pairs = pairs;
   p.scale = scale;
   set_path(true);
   return hip_status(launch_newton_schulz(p, static_cast<hipStream_t>(stream)), "zero_newton_schulz");
