@@ -523,9 +523,11 @@ int check_ns_shape(int64_t n_mats, int64_t rows, int64_t cols, Err& e) {
     return set_err(e, ZERO_ERR_SIZE, "newton_schulz: n_mats=%lld above %d", (long long)n_mats, ZERO_NS_MAX_MATS);
   if (rows > ZERO_NS_MAX_SIDE || cols > ZERO_NS_MAX_SIDE)
     return set_err(e, ZERO_ERR_SIZE, "newton_schulz: a side above %d", ZERO_NS_MAX_SIDE);
-  // the workspace: at most 3*(rows + 64)*(cols + 64) + 3*(min side + 64)^2 two-byte values per matrix
-  if (n_mats > 0 && mul_overflows((rows + 64) * (cols + 64) * 16, n_mats))
-    return set_err(e, ZERO_ERR_SIZE, "newton_schulz: size overflow");
+  // The workspace: per matrix three X and four k x k matrices padded to 64 and one X
+  // padded to 256, two-byte values, and 4 KiB at most of sums and alignment; once, 256 rows.
+  static_assert((ZERO_NS_MAX_SIDE + int64_t(256)) * (ZERO_NS_MAX_SIDE + int64_t(256)) * 16 + 4096 <
+                    INT64_MAX / (ZERO_NS_MAX_MATS + int64_t(1)),
+                "its bytes fit 64 bits within the limits");
   return ZERO_OK;
 }
 
