@@ -217,7 +217,8 @@ constexpr int kMuonUpdateBlock = 64;
 // the cap: momentum 115.8 and 113.2 us (6.59, 6.74 TB/s), update 98.5 and 97.6 us
 // (6.64, 6.70 TB/s; at 10 per CU 133 us); fused, TB/s with 1, 2, 4 and 8 ranks 6.62,
 // 6.54, 6.48, 6.32 without and 6.68, 6.67, 6.68, 6.64 with (accumulating 6.63, 6.58,
-// 6.41, 6.23 and 6.70, 6.74, 6.63, 6.63).  Other rank counts (3: 6.59) lose with any.
+// 6.41, 6.23 and 6.70, 6.74, 6.63, 6.63).  Other rank counts lose with any (without: 3
+// ranks 6.65, 5 to 7 6.42 to 6.34, 9 to 16 6.22 to 6.05).
 constexpr unsigned kMomentumResidencyLds = 8 * 1024;     // 20 workgroups
 constexpr unsigned kMuonUpdateResidencyLds = 8 * 1024;
 constexpr unsigned reduce_momentum_residency_lds(int n_ranks) {
