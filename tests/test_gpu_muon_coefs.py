@@ -131,3 +131,21 @@ def test_steps_that_differ(steps, dtype, rows, cols):
 def test_cubic_steps(rows, cols):
     g = torch.randn(rows, cols, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
     assert _off(g, ((1.5, -0.5, 0.0),) * 8, 0.25) <= NS_TOL * 1.3
+
+
+# Sets whose operands stay single FP16 values: a singular vector is turned by up to
+# 55 roundings of half a step, 55 * 2^-11 (five steps whose first slopes' product is 493),
+# six quintics raise X's roundings (2^-10/sqrt(12) rms) 56-fold in half of the
+# directions, 1.6e-2 / sqrt(2); and the result's own rounding.
+@pytest.mark.parametrize("name,coefs", [
+    ("five from 4.1 s", ((4.0848, -6.8946, 2.9270), (3.9505, -6.3029, 2.6377), (3.7418, -5.5913, 2.3037),
+                         (2.8769, -3.1427, 1.2046), (2.8366, -3.0525, 1.2012))),
+    ("quintic x 6", (QUINTIC,) * 6), ("cubic x 10", ((1.5, -0.5, 0.0),) * 10)])
+@pytest.mark.parametrize("kind", ["rank1", "rank6", "half", "decades"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(128, 320), (320, 128), (300, 300), (97, 1000)])
+def test_sets_near_the_default(name, coefs, kind, dtype, rows, cols):
+    print(f"newton_schulz {name} {kind} {rows}x{cols} {dtype}", flush=True)
+    off = _off(_matrix(kind, rows, cols, rows).to(dtype), coefs)
+    print(f"  off by {off:.2e}", flush=True)
+    assert off <= 55 * 2.0 ** -11 + 2.0 ** -8, off
