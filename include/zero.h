@@ -401,7 +401,7 @@ int zero_newton_schulz_workspace(int64_t n_mats, int64_t rows, int64_t cols, int
  * input as pairs of FP16 values (22 bits).  With the five steps (3.4445, -4.7750,
  * 2.0315) the result, for either input type, is 1.7e-3 to 2.1e-3 of its norm away
  * from the exact one on Gaussian matrices (rounding it to BF16 is 1.66e-3 of that),
- * up to 4e-3 on spectra that fall over three decades, up to 7e-3 on matrices of
+ * up to 4e-3 on spectra that fall over three decades, up to 8e-3 on matrices of
  * rank one or with half of the singular values next to nothing, and up to 2e-2 on
  * matrices of a few distinct values, whose roundings agree and add up.  Small
  * matrices, which one compute unit holds, are kept as pairs throughout: there the

@@ -57,6 +57,18 @@ def test_sets_that_raise_roundings(name, kind, dtype, rows, cols):
     assert off <= 2.0 ** -8 + 4e-4, off
 
 
+# matrices that one compute unit holds
+@pytest.mark.parametrize("name", list(SETS))
+@pytest.mark.parametrize("kind", ["rank1", "half", "ones"])
+@pytest.mark.parametrize("rows,cols", [(64, 256), (32, 40), (96, 200), (200, 50)])
+def test_sets_that_raise_roundings_of_small_matrices(name, kind, rows, cols):
+    print(f"newton_schulz {name} {kind} {rows}x{cols} small", flush=True)
+    for dtype in (torch.bfloat16, torch.float32):
+        off = _off(_matrix(kind, rows, cols, rows).to(dtype), SETS[name])
+        print(f"  off by {off:.2e}", flush=True)
+        assert off <= 2.0 ** -8 + 4e-4, off
+
+
 # every tile width: 64 (short and long sums), 128, 192, 256; stacks, odd sides, tall
 @pytest.mark.parametrize("mats,rows,cols", [(2, 515, 530), (7, 517, 650), (1, 300, 2500), (3, 777, 1301), (1, 1290, 4099),
                                             (1, 2900, 2910), (1, 4090, 4097), (1, 4300, 3990)])

@@ -113,3 +113,18 @@ def test_fp32_stack_with_neighbours():
     for i in range(3):
         ref = ns_f64(g[i], scale=0.5)
         assert float((out[i].double() - ref).norm() / ref.norm()) <= TOL["rank1"], i
+
+
+# the wider tiles, and a long sum
+@pytest.mark.parametrize("mats,rows,cols", [(1, 2900, 2910), (1, 4090, 4097), (1, 4300, 3990), (3, 1025, 3001), (1, 100, 9000)])
+@pytest.mark.parametrize("kind", ["rank1", "rank6"])
+def test_fp32_matrices_in_wide_tiles(mats, rows, cols, kind):
+    print(f"newton_schulz {kind} FP32 {mats}x{rows}x{cols}", flush=True)
+    g = torch.stack([_matrix(kind, rows, cols, i) for i in range(mats)])
+    out = torch.full(g.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    z.zero_newton_schulz(g, out, z.zero_newton_schulz_workspace(g))
+    for i in {0, mats - 1}:
+        ref = ns_f64(g[i])
+        off = float((out[i].double() - ref).norm() / ref.norm())
+        print(f"  off by {off:.2e}", flush=True)
+        assert off <= TOL[kind], (i, off)
