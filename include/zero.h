@@ -59,6 +59,16 @@ extern "C" {
 #define ZERO_NS_MAX_SIGMA 2   /* largest singular value a step may give */
 #define ZERO_NS_MAX_GAIN 16   /* largest |p(s)/s| of a step */
 
+/* 8-bit activations and the feed-forward block */
+#define ZERO_ACT8_BLOCK 32   /* neighbours of a row that share a power of two */
+#define ZERO_ACT8_MAX_COLS 2147483648
+#define ZERO_ACT8_MAX_VALUES 1099511627776
+#define ZERO_FFN_MAX_TOKENS 16777216
+#define ZERO_FFN_MAX_SIDE 262144
+#define ZERO_FFN_MAX_STRIDE 8388608
+#define ZERO_FFN_BACKWARD 1    /* flags of zero_ffn_workspace */
+#define ZERO_FFN_UNALIGNED 2
+
 typedef enum zero_status {
   ZERO_OK = 0,
   ZERO_ERR_ARG = -1,    /* null pointer, count out of range, overlapping buffers, bad hyper-parameter */
@@ -440,6 +450,104 @@ int zero_newton_schulz(const void* in, int in_dtype, int64_t in_row_stride, int6
  * Errors: as zero_muon_momentum. */
 int zero_muon_shard_step(float* master, uint16_t* bf16_out, const uint16_t* update, int64_t n,
                          const zero_muon_hparams* hp, const float* lr_dev, void* stream);
+
+/* ---------------------------------------------------------------- a layer's own work
+ * Between the gather of a layer's weights and the reduction of its gradients lies
+ * the layer's work ([essay] ZeRO-3 的一次完整计算: gather -> forward -> release;
+ * gather -> backward -> reduce-scatter -> owner update).  These calls are that of the
+ * gated feed-forward block, which holds most of a layer's parameters: it reads the
+ * gathered BF16 view and writes the BF16 contributions that zero_reduce_scatter
+ * takes.  What the backward pass needs of the forward is kept in 8 bits. */
+
+/* Formats of an 8-bit checkpoint: two's complement whole numbers in [-127, 127], or
+ * e4m3 (sign, 4 exponent bits with bias 7, 3 fraction bits; largest value 448). */
+enum { ZERO_ACT8_INT8 = 0, ZERO_ACT8_E4M3 = 1 };
+
+/* Activations into 8 bits.  The columns of a row are taken in blocks of
+ * ZERO_ACT8_BLOCK (the last one of a row may be shorter).  With a the block's largest magnitude and
+ * M = 127 or 448,
+ *   e = the least whole number >= -126 with a <= M * 2^e,
+ *   code = round_to_nearest_even(x * 2^-e) in the format,  scale = e + 127.
+ * The scaling is exact and no value saturates.  A whole number is off by at most
+ * 2^-1 * 2^e <= a / 127, an e4m3 value by at most 2^-4 of itself (or 2^-10 * 2^e).
+ * A block that holds a NaN, an infinity or a magnitude above 127 * 2^121 (e4m3: 448 *
+ * 2^119), next to which a code could stand for 2^128, has scale 255 and codes 0.
+ *   x             device, BF16 or FP32 (x_dtype), element (i, j) at
+ *                 x[i*x_row_stride + j]; aligned to its element.
+ *   codes         device, written: rows * cols bytes, row by row, any alignment.
+ *   scales        device, written: rows * ceil(cols / ZERO_ACT8_BLOCK) bytes.
+ * Errors: ZERO_ERR_ARG (NULL, negative sizes, x_dtype, format, overlapping buffers),
+ * ZERO_ERR_ALIGN, ZERO_ERR_SIZE (a row stride below cols or above ZERO_ACT8_MAX_COLS, more than
+ * ZERO_ACT8_MAX_COLS columns or ZERO_ACT8_MAX_VALUES values), ZERO_ERR_HIP. */
+int zero_act8_save(const void* x, int x_dtype, int64_t x_row_stride, int64_t rows, int64_t cols, int format,
+                   uint8_t* codes, uint8_t* scales, void* stream);
+
+/* The values of a checkpoint: code * 2^(scale - 127), exact in FP32 and, from 2^-126 on,
+ * in BF16 (below, rounded to nearest even); a block with scale 255 reads as NaN.
+ *   out           device, written, BF16 or FP32 (out_dtype), laid out as
+ *                 zero_act8_save's x.
+ * Errors: as zero_act8_save. */
+int zero_act8_load(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, int format, void* out,
+                   int out_dtype, int64_t out_row_stride, void* stream);
+
+/* Activations of the feed-forward block: x sigma(x); x sigma(2 sqrt(2/pi) (x + 0.044715 x^3)),
+ * which is GELU with tanh; max(x, 0), whose derivative at 0 is taken as 0. */
+enum { ZERO_FFN_SILU = 0, ZERO_FFN_GELU = 1, ZERO_FFN_RELU = 2 };
+
+/* What a forward pass keeps for the backward pass: the block's input x
+ * [tokens, model], and g = x Wg^T and u = x Wu^T [tokens, hidden], each as
+ * zero_act8_save lays it out.  model + 2 hidden bytes per token and 1/32 more, where
+ * BF16 values of x, g, u and h would be 2 model + 6 hidden. */
+typedef struct zero_ffn_checkpoint {
+  uint8_t *x_codes, *x_scales, *gate_codes, *gate_scales, *up_codes, *up_scales;
+  int32_t format;
+} zero_ffn_checkpoint;
+
+/* Bytes of workspace that zero_ffn_forward, or with ZERO_FFN_BACKWARD
+ * zero_ffn_backward, needs.  Weights that are not 16-byte aligned need
+ * ZERO_FFN_UNALIGNED (room for aligned copies; sizes that are no multiples of 64
+ * have that room anyway).
+ * Errors: ZERO_ERR_ARG (NULL, unknown flags, tokens < 0, a side < 1), ZERO_ERR_SIZE
+ * (sizes above ZERO_FFN_MAX_TOKENS, ZERO_FFN_MAX_SIDE). */
+int zero_ffn_workspace(int64_t tokens, int64_t model, int64_t hidden, int flags, int64_t* bytes_out);
+
+/* Gated feed-forward block, forward:
+ *   g = x Wg^T,  u = x Wu^T,  h = act(g) * u,  y = h Wd^T.
+ *   x, y          device BF16, element (t, j) at x[t*x_row_stride + j], 2-byte aligned.
+ *   w_gate, w_up  device BF16 [hidden, model], w_down [model, hidden], contiguous:
+ *                 slices of the gathered view of a layer.
+ *   save          host, or NULL: the checkpoint's buffers, written.
+ *   workspace     device, 256-byte aligned, workspace_bytes >= zero_ffn_workspace's
+ *                 answer; nothing in it carries over between calls.
+ * Arithmetic: products of BF16 values summed in FP32 on the matrix cores; act in
+ * FP32; g and u go into the checkpoint as summed, h is rounded to BF16 (the type the
+ * second product takes), y is rounded to BF16.  Results are the same bits on every
+ * call with the same inputs.
+ * tokens = 0 launches nothing.
+ * Errors: ZERO_ERR_ARG (NULL, negative sizes, activation, format, overlapping
+ * buffers: nothing written may overlap anything else), ZERO_ERR_ALIGN, ZERO_ERR_SIZE
+ * (limits, a row stride below model or above ZERO_FFN_MAX_STRIDE, a small
+ * workspace), ZERO_ERR_HIP. */
+int zero_ffn_forward(const uint16_t* x, int64_t x_row_stride, int64_t tokens, int64_t model, int64_t hidden,
+                     const uint16_t* w_gate, const uint16_t* w_up, const uint16_t* w_down, int activation,
+                     uint16_t* y, int64_t y_row_stride, const zero_ffn_checkpoint* save, void* workspace,
+                     int64_t workspace_bytes, void* stream);
+
+/* Backward, from a checkpoint's values of x, g and u:
+ *   dh = dy Wd,  dg = dh * u * act'(g),  du = dh * act(g),  h = act(g) * u,
+ *   dx = dg Wg + du Wu,  d_gate = dg^T x,  d_up = du^T x,  d_down = dy^T h.
+ *   dy, dx        device BF16 with row strides, as x and y; dx may be NULL (not wanted).
+ *   saved         host: the checkpoint's buffers, read.
+ *   d_gate, d_up  device BF16 [hidden, model], d_down [model, hidden], contiguous,
+ *                 written: slices of a rank's gradient contribution.
+ * Arithmetic as in the forward pass; dg, du and h are rounded to BF16 between the
+ * products.  tokens = 0: the gradients are zeros (a rank without tokens contributes
+ * nothing), and only they are touched.
+ * Errors: as zero_ffn_forward, and ZERO_ERR_ARG for a NULL checkpoint. */
+int zero_ffn_backward(const uint16_t* dy, int64_t dy_row_stride, int64_t tokens, int64_t model, int64_t hidden,
+                      const zero_ffn_checkpoint* saved, const uint16_t* w_gate, const uint16_t* w_up,
+                      const uint16_t* w_down, int activation, uint16_t* dx, int64_t dx_row_stride, uint16_t* d_gate,
+                      uint16_t* d_up, uint16_t* d_down, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------- host-offloaded gradient shard */
 

@@ -18,6 +18,11 @@ ZERO_OFFLOAD_REDUCE, ZERO_OFFLOAD_ADAM, ZERO_OFFLOAD_REDUCE_ADAM = 0, 1, 2
 ZERO_NS_MAX_STEPS, ZERO_NS_MAX_MATS, ZERO_NS_MAX_SIDE = 16, 65535, 262144
 ZERO_NS_MAX_SIGMA, ZERO_NS_MAX_GAIN = 2, 16
 ZERO_BF16, ZERO_FP32 = 0, 1
+ZERO_ACT8_BLOCK, ZERO_ACT8_MAX_COLS, ZERO_ACT8_MAX_VALUES = 32, 2147483648, 1099511627776
+ZERO_ACT8_INT8, ZERO_ACT8_E4M3 = 0, 1
+ZERO_FFN_MAX_TOKENS, ZERO_FFN_MAX_SIDE, ZERO_FFN_MAX_STRIDE = 16777216, 262144, 8388608
+ZERO_FFN_BACKWARD, ZERO_FFN_UNALIGNED = 1, 2
+ZERO_FFN_SILU, ZERO_FFN_GELU, ZERO_FFN_RELU = 0, 1, 2
 
 
 class AdamHparams(C.Structure):
@@ -33,6 +38,11 @@ class AdamScalars(C.Structure):
 
 class MuonHparams(C.Structure):
     _fields_ = [("lr", C.c_float), ("momentum", C.c_float), ("weight_decay", C.c_float), ("nesterov", C.c_int32)]
+
+
+class FfnCheckpointBuffers(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("x_codes", "x_scales", "gate_codes", "gate_scales", "up_codes", "up_scales")
+                ] + [("format", C.c_int32)]
 
 
 P = C.c_void_p
@@ -64,6 +74,13 @@ SIGNATURES = {
     "zero_newton_schulz": (C.c_int, [P, C.c_int, I64, I64, P, I64, I64, I64, I64, I64, FP, C.c_int, C.c_float, P, I64,
                                      P]),
     "zero_muon_shard_step": (C.c_int, [P, P, P, I64, C.POINTER(MuonHparams), P, P]),
+    "zero_act8_save": (C.c_int, [P, C.c_int, I64, I64, I64, C.c_int, P, P, P]),
+    "zero_act8_load": (C.c_int, [P, P, I64, I64, C.c_int, P, C.c_int, I64, P]),
+    "zero_ffn_workspace": (C.c_int, [I64, I64, I64, C.c_int, I64P]),
+    "zero_ffn_forward": (C.c_int, [P, I64, I64, I64, I64, P, P, P, C.c_int, P, I64, C.POINTER(FfnCheckpointBuffers), P,
+                                   I64, P]),
+    "zero_ffn_backward": (C.c_int, [P, I64, I64, I64, I64, C.POINTER(FfnCheckpointBuffers), P, P, P, C.c_int, P, I64, P,
+                                    P, P, P, I64, P]),
     "zero_offload_create": (C.c_int, [C.c_int, I64, I64, P, PP, PP, C.POINTER(C.c_void_p)]),
     "zero_offload_stream": (C.c_int, [P, C.c_int, I64, C.c_int, FP, P, P, P, P,
                                       C.POINTER(AdamHparams), P]),

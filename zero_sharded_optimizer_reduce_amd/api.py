@@ -483,6 +483,148 @@ def zero_muon_shard_step(master: torch.Tensor, bf16_out: torch.Tensor, update: t
           "zero_muon_shard_step")
 
 
+# ------------------------------------------------------------ 8-bit activations, feed-forward block
+ACT8_FORMATS = {"int8": _lib.ZERO_ACT8_INT8, "e4m3": _lib.ZERO_ACT8_E4M3}
+FFN_ACTIVATIONS = {"silu": _lib.ZERO_FFN_SILU, "gelu": _lib.ZERO_FFN_GELU, "relu": _lib.ZERO_FFN_RELU}
+_UINT8 = (torch.uint8,)
+
+
+def _choice(table: Mapping[str, int], name, what: str) -> int:
+    if name not in table:
+        raise ValueError(f"{what}: {name!r} is none of {', '.join(table)}")
+    return table[name]
+
+
+def _rows(t: torch.Tensor, what: str, dtypes):
+    """(pointer, rows, cols, row stride) of a matrix whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise TypeError(f"{what}: expected a 2-D torch.Tensor")
+    _on_device(t, what, dtypes)
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    return t.data_ptr(), rows, cols, t.stride(0) if rows > 1 else cols
+
+
+def _act8(rows: int, cols: int, codes: torch.Tensor, scales: torch.Tensor, what: str = "") -> list:
+    """The pointers of a checkpoint of rows x cols values."""
+    ptrs = []
+    for t, name, width in ((codes, "codes", cols), (scales, "scales", -(-cols // _lib.ZERO_ACT8_BLOCK))):
+        ptr = _dev(t, what + name, _UINT8)
+        if tuple(t.shape) != (rows, width):
+            raise ValueError(f"{what}{name}: shape {tuple(t.shape)}, expected {(rows, width)}")
+        ptrs.append(ptr)
+    return ptrs
+
+
+def zero_act8_buffers(rows: int, cols: int, device="cuda"):
+    """Buffers (codes, scales) of an 8-bit checkpoint of rows x cols values."""
+    return (torch.empty(rows, cols, dtype=torch.uint8, device=device),
+            torch.empty(rows, -(-cols // _lib.ZERO_ACT8_BLOCK), dtype=torch.uint8, device=device))
+
+
+def zero_act8_save(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, format: str = "int8",
+                   stream=None) -> None:
+    """x (BF16 or FP32, [rows, cols], row stride free) as 8 bits a value and a power
+    of two per 32 neighbours of a row; format "int8" or "e4m3"."""
+    xp, rows, cols, row = _rows(x, "x", (torch.bfloat16, torch.float32))
+    cp, sp = _act8(rows, cols, codes, scales)
+    check(load().zero_act8_save(xp, _lib.ZERO_FP32 if x.dtype == torch.float32 else _lib.ZERO_BF16, row, rows, cols,
+                                _choice(ACT8_FORMATS, format, "format"), cp, sp, _stream(stream)), "zero_act8_save")
+
+
+def zero_act8_load(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, format: str = "int8",
+                   stream=None) -> None:
+    """out (BF16 or FP32, [rows, cols], row stride free) = the checkpoint's values."""
+    op, rows, cols, row = _rows(out, "out", (torch.bfloat16, torch.float32))
+    cp, sp = _act8(rows, cols, codes, scales)
+    check(load().zero_act8_load(cp, sp, rows, cols, _choice(ACT8_FORMATS, format, "format"), op,
+                                _lib.ZERO_FP32 if out.dtype == torch.float32 else _lib.ZERO_BF16, row,
+                                _stream(stream)), "zero_act8_load")
+
+
+class FfnCheckpoint:
+    """What a feed-forward block's forward pass keeps for its backward pass: x, x Wg^T
+    and x Wu^T, each as the (codes, scales) of an 8-bit checkpoint."""
+
+    def __init__(self, x, gate, up, format: str = "int8"):
+        self.x, self.gate, self.up = tuple(x), tuple(gate), tuple(up)
+        self.format = format
+        _choice(ACT8_FORMATS, format, "format")
+
+    @classmethod
+    def empty(cls, tokens: int, model: int, hidden: int, format: str = "int8", device="cuda") -> "FfnCheckpoint":
+        return cls(zero_act8_buffers(tokens, model, device), zero_act8_buffers(tokens, hidden, device),
+                   zero_act8_buffers(tokens, hidden, device), format)
+
+    def buffers(self, tokens: int, model: int, hidden: int) -> _lib.FfnCheckpointBuffers:
+        ptrs = [p for held, cols, what in ((self.x, model, "checkpoint.x "), (self.gate, hidden, "checkpoint.gate "),
+                                           (self.up, hidden, "checkpoint.up "))
+                for p in _act8(tokens, cols, *held, what)]
+        return _lib.FfnCheckpointBuffers(*ptrs, ACT8_FORMATS[self.format])
+
+
+def zero_ffn_workspace(tokens: int, model: int, hidden: int, backward: bool = False, unaligned: bool = False,
+                       device="cuda") -> torch.Tensor:
+    """A device workspace for zero_ffn_forward or, with backward, zero_ffn_backward.
+    unaligned: the weights' addresses are no multiples of 16 bytes."""
+    n = C.c_int64()
+    flags = (_lib.ZERO_FFN_BACKWARD if backward else 0) | (_lib.ZERO_FFN_UNALIGNED if unaligned else 0)
+    check(load().zero_ffn_workspace(tokens, model, hidden, flags, C.byref(n)), "zero_ffn_workspace")
+    return torch.empty(n.value, dtype=torch.uint8, device=device)
+
+
+def _ffn_weights(model: int, names, *ts):
+    """(pointers, hidden) of matrices [hidden, model], [hidden, model], [model, hidden]."""
+    ptrs = [_dev(t, name, (torch.bfloat16,)) for t, name in zip(ts, names)]
+    if ts[0].dim() != 2:
+        raise ValueError(f"{names[0]}: expected a 2-D tensor")
+    hidden = ts[0].shape[0]
+    for t, name, shape in zip(ts, names, ((hidden, model), (hidden, model), (model, hidden))):
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    return ptrs, hidden
+
+
+def zero_ffn_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor, y: torch.Tensor,
+                     workspace: torch.Tensor, activation: str = "silu", checkpoint: Optional[FfnCheckpoint] = None,
+                     stream=None) -> None:
+    """y = (act(x Wg^T) * (x Wu^T)) Wd^T, all BF16; x, y [tokens, model] with free row
+    strides, w_gate and w_up [hidden, model], w_down [model, hidden].  activation: "silu", "gelu"
+    (tanh) or "relu".  checkpoint: written, for zero_ffn_backward."""
+    xp, tokens, model, xrow = _rows(x, "x", (torch.bfloat16,))
+    yp, *yshape, yrow = _rows(y, "y", (torch.bfloat16,))
+    if yshape != [tokens, model]:
+        raise ValueError("zero_ffn_forward: y must have x's shape")
+    w, hidden = _ffn_weights(model, ("w_gate", "w_up", "w_down"), w_gate, w_up, w_down)
+    held = None if checkpoint is None else C.byref(checkpoint.buffers(tokens, model, hidden))
+    check(load().zero_ffn_forward(xp, xrow, tokens, model, hidden, *w, _choice(FFN_ACTIVATIONS, activation, "activation"),
+                                  yp, yrow, held, _dev(workspace, "workspace", _UINT8), workspace.numel(),
+                                  _stream(stream)), "zero_ffn_forward")
+
+
+def zero_ffn_backward(dy: torch.Tensor, checkpoint: FfnCheckpoint, w_gate: torch.Tensor, w_up: torch.Tensor,
+                      w_down: torch.Tensor, dx: Optional[torch.Tensor], d_gate: torch.Tensor, d_up: torch.Tensor,
+                      d_down: torch.Tensor, workspace: torch.Tensor, activation: str = "silu", stream=None) -> None:
+    """Gradients of zero_ffn_forward from its checkpoint: dx [tokens, model] (None: not
+    wanted) and d_gate, d_up, d_down of the weights' shapes, all BF16, written."""
+    dyp, tokens, model, dyrow = _rows(dy, "dy", (torch.bfloat16,))
+    dxp, dxrow = None, model
+    if dx is not None:
+        dxp, *shape, dxrow = _rows(dx, "dx", (torch.bfloat16,))
+        if shape != [tokens, model]:
+            raise ValueError("zero_ffn_backward: dx must have dy's shape")
+    w, hidden = _ffn_weights(model, ("w_gate", "w_up", "w_down"), w_gate, w_up, w_down)
+    d, dhidden = _ffn_weights(model, ("d_gate", "d_up", "d_down"), d_gate, d_up, d_down)
+    if dhidden != hidden:
+        raise ValueError("zero_ffn_backward: the gradients must have the weights' shapes")
+    held = checkpoint.buffers(tokens, model, hidden)
+    check(load().zero_ffn_backward(dyp, dyrow, tokens, model, hidden, C.byref(held), *w,
+                                   _choice(FFN_ACTIVATIONS, activation, "activation"), dxp, dxrow, *d,
+                                   _dev(workspace, "workspace", _UINT8), workspace.numel(), _stream(stream)),
+          "zero_ffn_backward")
+
+
 def zero_last_path_vectorized() -> int:
     return int(load().zero_last_path_vectorized())
 

@@ -115,6 +115,33 @@ struct NsParams {
   float scale;
 };
 
+// A matrix of activations and its 8-bit checkpoint; values: read by the save,
+// written by the load.
+struct Act8Params {
+  void* values;
+  int64_t row;          // stride in elements
+  int64_t rows, cols;
+  uint8_t* codes;
+  uint8_t* scales;
+  int format;
+  int f32;
+};
+
+// One feed-forward call, checked; see ffn.hip.
+struct FfnParams {
+  const uint16_t* x;    // backward: dy
+  int64_t x_row;
+  uint16_t* y;          // backward: dx, or NULL
+  int64_t y_row;
+  int64_t tokens, model, hidden;
+  const uint16_t *w_gate, *w_up, *w_down;
+  uint16_t *d_gate, *d_up, *d_down;   // backward
+  zero_ffn_checkpoint ckpt;
+  int save;             // forward: the checkpoint is written
+  int activation;
+  void* workspace;
+};
+
 struct GatherParams {
   const void* src[ZERO_MAX_RANKS];
   void* dst;
@@ -149,6 +176,15 @@ hipError_t launch_muon_update(const MuonUpdateParams& p, bool vec, hipStream_t s
 // Newton-Schulz orthogonalisation: the workspace it needs and its launches.
 int64_t ns_workspace_bytes(int64_t mats, int64_t rows, int64_t cols);
 hipError_t launch_newton_schulz(const NsParams& p, hipStream_t stream);
+
+// Activations to 8 bits and back, and the feed-forward block: the workspace it
+// needs (unaligned: for weights that are not 16-byte aligned) and its launches.
+hipError_t launch_act8_save(const Act8Params& p, hipStream_t stream);
+hipError_t launch_act8_load(const Act8Params& p, hipStream_t stream);
+int64_t ffn_workspace_bytes(int64_t tokens, int64_t model, int64_t hidden, bool backward, bool unaligned);
+bool ffn_weights_aligned(const FfnParams& p);
+hipError_t launch_ffn_forward(const FfnParams& p, hipStream_t stream);
+hipError_t launch_ffn_backward(const FfnParams& p, hipStream_t stream);
 
 // Device address of the current device's partial-sum array for the norm
 // (kNormScratchDoubles doubles, 256-byte aligned).  Looked up once per device

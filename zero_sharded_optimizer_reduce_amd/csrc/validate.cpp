@@ -724,4 +724,144 @@ int check_newton_schulz(const void* in, int in_dtype, int64_t in_row_stride, int
   return ZERO_OK;
 }
 
+// ---------------------------------------------------------------- 8-bit activations, feed-forward block
+// Bytes from the first element of a matrix to behind its last.
+static int64_t matrix_bytes(int64_t rows, int64_t cols, int64_t row_stride, int64_t esz) {
+  return rows && cols ? ((rows - 1) * row_stride + cols) * esz : 0;
+}
+
+int check_act8(const char* what, const void* values, int dtype, int64_t row_stride, int64_t rows, int64_t cols,
+               int format, const uint8_t* codes, const uint8_t* scales, Err& e) {
+  if (dtype != ZERO_BF16 && dtype != ZERO_FP32)
+    return set_err(e, ZERO_ERR_ARG, "%s: dtype=%d is neither ZERO_BF16 nor ZERO_FP32", what, dtype);
+  if (format != ZERO_ACT8_INT8 && format != ZERO_ACT8_E4M3)
+    return set_err(e, ZERO_ERR_ARG, "%s: format=%d is neither ZERO_ACT8_INT8 nor ZERO_ACT8_E4M3", what, format);
+  if (rows < 0 || cols < 0)
+    return set_err(e, ZERO_ERR_ARG, "%s: negative size %lld x %lld", what, (long long)rows, (long long)cols);
+  if (rows == 0 || cols == 0) return ZERO_OK;   // touches no buffer; NULL pointers allowed
+  if (cols > ZERO_ACT8_MAX_COLS || rows > ZERO_ACT8_MAX_VALUES / cols)
+    return set_err(e, ZERO_ERR_SIZE, "%s: %lld x %lld values are too many", what, (long long)rows, (long long)cols);
+  if (rows > 1 && (row_stride < cols || row_stride > ZERO_ACT8_MAX_COLS))
+    return set_err(e, ZERO_ERR_SIZE, "%s: row stride %lld outside [cols=%lld, %lld]", what, (long long)row_stride,
+                   (long long)cols, (long long)ZERO_ACT8_MAX_COLS);
+  if (!values || !codes || !scales) return set_err(e, ZERO_ERR_ARG, "%s: NULL buffer", what);
+  const int64_t esz = dtype == ZERO_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(values) & static_cast<uintptr_t>(esz - 1))
+    return set_err(e, ZERO_ERR_ALIGN, "%s: values not %d-byte aligned", what, (int)esz);
+  const int64_t blocks = (cols + ZERO_ACT8_BLOCK - 1) / ZERO_ACT8_BLOCK;
+  const Range v = range_of(values, matrix_bytes(rows, cols, row_stride, esz));
+  const Range c = range_of(codes, rows * cols), k = range_of(scales, rows * blocks);
+  if (overlaps(v, c) || overlaps(v, k) || overlaps(c, k))
+    return set_err(e, ZERO_ERR_ARG, "%s: values, codes and scales overlap", what);
+  return ZERO_OK;
+}
+
+int check_ffn_shape(int64_t tokens, int64_t model, int64_t hidden, Err& e) {
+  if (tokens < 0 || model < 1 || hidden < 1)
+    return set_err(e, ZERO_ERR_ARG, "ffn: tokens=%lld, model=%lld, hidden=%lld: at least 0, 1 and 1", (long long)tokens,
+                   (long long)model, (long long)hidden);
+  if (tokens > ZERO_FFN_MAX_TOKENS || model > ZERO_FFN_MAX_SIDE || hidden > ZERO_FFN_MAX_SIDE)
+    return set_err(e, ZERO_ERR_SIZE, "ffn: tokens=%lld, model=%lld, hidden=%lld: at most %d, %d and %d", (long long)tokens,
+                   (long long)model, (long long)hidden, ZERO_FFN_MAX_TOKENS, ZERO_FFN_MAX_SIDE, ZERO_FFN_MAX_SIDE);
+  return ZERO_OK;
+}
+
+namespace {
+// Buffers of a call: what it writes may overlap nothing else.
+struct Buffers {
+  static constexpr int kMost = 18;
+  Range range[kMost];
+  const char* name[kMost];
+  bool written[kMost];
+  int n = 0;
+  void add(const char* what, const void* p, int64_t bytes, bool writes) {
+    range[n] = range_of(p, bytes);
+    name[n] = what;
+    written[n++] = writes;
+  }
+  int check(Err& e) const {
+    for (int i = 0; i < n; ++i)
+      for (int j = 0; j < i; ++j)
+        if ((written[i] || written[j]) && overlaps(range[i], range[j]))
+          return set_err(e, ZERO_ERR_ARG, "ffn: %s and %s overlap", name[j], name[i]);
+    return ZERO_OK;
+  }
+};
+
+int check_ffn_matrix(const char* name, const void* p, int64_t tokens, int64_t model, int64_t row_stride, Err& e) {
+  if (tokens == 0) return ZERO_OK;
+  if (!p) return set_err(e, ZERO_ERR_ARG, "ffn: %s is NULL", name);
+  if (reinterpret_cast<uintptr_t>(p) & 1u) return set_err(e, ZERO_ERR_ALIGN, "ffn: %s not 2-byte aligned", name);
+  if (tokens > 1 && (row_stride < model || row_stride > ZERO_FFN_MAX_STRIDE))
+    return set_err(e, ZERO_ERR_SIZE, "ffn: %s's row stride %lld outside [model=%lld, %d]", name, (long long)row_stride,
+                   (long long)model, ZERO_FFN_MAX_STRIDE);
+  return ZERO_OK;
+}
+}  // namespace
+
+int check_ffn(bool backward, const uint16_t* in, int64_t in_row, int64_t tokens, int64_t model, int64_t hidden,
+              const uint16_t* w_gate, const uint16_t* w_up, const uint16_t* w_down, int activation,
+              const uint16_t* out, int64_t out_row, const zero_ffn_checkpoint* ckpt, const uint16_t* d_gate,
+              const uint16_t* d_up, const uint16_t* d_down, const void* workspace, int64_t workspace_bytes,
+              int64_t workspace_need, Err& e) {
+  int st = check_ffn_shape(tokens, model, hidden, e);
+  if (st) return st;
+  if (activation != ZERO_FFN_SILU && activation != ZERO_FFN_GELU && activation != ZERO_FFN_RELU)
+    return set_err(e, ZERO_ERR_ARG, "ffn: activation=%d is none of ZERO_FFN_SILU, _GELU, _RELU", activation);
+  if (backward && !ckpt) return set_err(e, ZERO_ERR_ARG, "ffn: the backward pass needs a checkpoint");
+  if (ckpt && ckpt->format != ZERO_ACT8_INT8 && ckpt->format != ZERO_ACT8_E4M3)
+    return set_err(e, ZERO_ERR_ARG, "ffn: checkpoint format=%d is neither ZERO_ACT8_INT8 nor ZERO_ACT8_E4M3", ckpt->format);
+  if (tokens == 0 && !backward) return ZERO_OK;   // touches no buffer; NULL pointers allowed
+  Buffers b;
+  const int64_t side = model * hidden * 2;
+  if (tokens > 0 || !backward) {
+    const uint16_t* w[3] = {w_gate, w_up, w_down};
+    static const char* const names[3] = {"w_gate", "w_up", "w_down"};
+    for (int k = 0; k < 3; ++k) {
+      if (!w[k]) return set_err(e, ZERO_ERR_ARG, "ffn: %s is NULL", names[k]);
+      if (reinterpret_cast<uintptr_t>(w[k]) & 1u) return set_err(e, ZERO_ERR_ALIGN, "ffn: %s not 2-byte aligned", names[k]);
+      b.add(names[k], w[k], side, false);
+    }
+  }
+  st = check_ffn_matrix(backward ? "dy" : "x", in, tokens, model, in_row, e);
+  if (st) return st;
+  b.add(backward ? "dy" : "x", in, matrix_bytes(tokens, model, in_row, 2), false);
+  if (out || !backward) {
+    st = check_ffn_matrix(backward ? "dx" : "y", out, tokens, model, out_row, e);
+    if (st) return st;
+    b.add(backward ? "dx" : "y", out, matrix_bytes(tokens, model, out_row, 2), true);
+  }
+  if (ckpt && tokens > 0) {
+    const int64_t mb = (model + ZERO_ACT8_BLOCK - 1) / ZERO_ACT8_BLOCK, hb = (hidden + ZERO_ACT8_BLOCK - 1) / ZERO_ACT8_BLOCK;
+    const struct { const char* name; const uint8_t* p; int64_t bytes; } parts[6] = {
+        {"x_codes", ckpt->x_codes, tokens * model},       {"x_scales", ckpt->x_scales, tokens * mb},
+        {"gate_codes", ckpt->gate_codes, tokens * hidden}, {"gate_scales", ckpt->gate_scales, tokens * hb},
+        {"up_codes", ckpt->up_codes, tokens * hidden},     {"up_scales", ckpt->up_scales, tokens * hb}};
+    for (const auto& part : parts) {
+      if (!part.p) return set_err(e, ZERO_ERR_ARG, "ffn: the checkpoint's %s is NULL", part.name);
+      b.add(part.name, part.p, part.bytes, !backward);
+    }
+  }
+  if (backward) {
+    const uint16_t* d[3] = {d_gate, d_up, d_down};
+    static const char* const names[3] = {"d_gate", "d_up", "d_down"};
+    for (int k = 0; k < 3; ++k) {
+      if (!d[k]) return set_err(e, ZERO_ERR_ARG, "ffn: %s is NULL", names[k]);
+      if (reinterpret_cast<uintptr_t>(d[k]) & 1u) return set_err(e, ZERO_ERR_ALIGN, "ffn: %s not 2-byte aligned", names[k]);
+      b.add(names[k], d[k], side, true);
+    }
+  }
+  if (workspace_need > 0) {
+    if (!workspace) return set_err(e, ZERO_ERR_ARG, "ffn: workspace is NULL");
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+      return set_err(e, ZERO_ERR_ALIGN, "ffn: workspace not 256-byte aligned");
+    if (workspace_bytes < workspace_need)
+      return set_err(e, ZERO_ERR_SIZE,
+                     "ffn: workspace of %lld bytes, %lld needed (zero_ffn_workspace; weights that are not 16-byte aligned need ZERO_FFN_UNALIGNED)",
+                     (long long)workspace_bytes, (long long)workspace_need);
+    b.add("workspace", workspace, workspace_need, true);
+  }
+  return b.check(e);
+}
+
 }  // namespace zero

@@ -108,6 +108,18 @@ int check_newton_schulz(const void* in, int in_dtype, int64_t in_row_stride, int
                         float scale, const void* workspace, int64_t workspace_bytes,
                         int64_t workspace_need, Err& e, bool* pairs = nullptr);
 
+// Activations in 8 bits: values is what is read or written.  The feed-forward block:
+// in and out are x and y, or dy and dx (NULL: not wanted); workspace_need: the bytes
+// that the call needs, from ffn_workspace_bytes.
+int check_act8(const char* what, const void* values, int dtype, int64_t row_stride, int64_t rows, int64_t cols,
+               int format, const uint8_t* codes, const uint8_t* scales, Err& e);
+int check_ffn_shape(int64_t tokens, int64_t model, int64_t hidden, Err& e);
+int check_ffn(bool backward, const uint16_t* in, int64_t in_row, int64_t tokens, int64_t model, int64_t hidden,
+              const uint16_t* w_gate, const uint16_t* w_up, const uint16_t* w_down, int activation,
+              const uint16_t* out, int64_t out_row, const zero_ffn_checkpoint* ckpt, const uint16_t* d_gate,
+              const uint16_t* d_up, const uint16_t* d_down, const void* workspace, int64_t workspace_bytes,
+              int64_t workspace_need, Err& e);
+
 // Alignment tests for the kernels' vector paths.
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }

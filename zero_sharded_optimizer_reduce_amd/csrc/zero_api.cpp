@@ -549,4 +549,108 @@ int zero_newton_schulz(const void* in, int in_dtype, int64_t in_row_stride, int6
   return hip_status(launch_newton_schulz(p, static_cast<hipStream_t>(stream)), "zero_newton_schulz");
 }
 
+// ---------------------------------------------------------------- 8-bit activations, feed-forward block
+int zero_act8_save(const void* x, int x_dtype, int64_t x_row_stride, int64_t rows, int64_t cols, int format,
+                   uint8_t* codes, uint8_t* scales, void* stream) {
+  TraceRange tr("zero_act8_save");
+  Err e;
+  int st = check_act8("act8_save", x, x_dtype, x_row_stride, rows, cols, format, codes, scales, e);
+  if (st) return fail(st, e.msg);
+  if (rows == 0 || cols == 0) return ZERO_OK;
+  const Act8Params p = {const_cast<void*>(x), rows > 1 ? x_row_stride : cols, rows, cols, codes, scales, format,
+                        x_dtype == ZERO_FP32};
+  set_path(true);
+  return hip_status(launch_act8_save(p, static_cast<hipStream_t>(stream)), "zero_act8_save");
+}
+
+int zero_act8_load(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, int format, void* out,
+                   int out_dtype, int64_t out_row_stride, void* stream) {
+  TraceRange tr("zero_act8_load");
+  Err e;
+  int st = check_act8("act8_load", out, out_dtype, out_row_stride, rows, cols, format, codes, scales, e);
+  if (st) return fail(st, e.msg);
+  if (rows == 0 || cols == 0) return ZERO_OK;
+  const Act8Params p = {out, rows > 1 ? out_row_stride : cols, rows, cols, const_cast<uint8_t*>(codes),
+                        const_cast<uint8_t*>(scales), format, out_dtype == ZERO_FP32};
+  set_path(true);
+  return hip_status(launch_act8_load(p, static_cast<hipStream_t>(stream)), "zero_act8_load");
+}
+
+int zero_ffn_workspace(int64_t tokens, int64_t model, int64_t hidden, int flags, int64_t* bytes_out) {
+  Err e;
+  if (!bytes_out) return fail(ZERO_ERR_ARG, "ffn: NULL bytes_out");
+  if (flags & ~(ZERO_FFN_BACKWARD | ZERO_FFN_UNALIGNED)) return fail(ZERO_ERR_ARG, "ffn: unknown workspace flags");
+  int st = check_ffn_shape(tokens, model, hidden, e);
+  if (st) return fail(st, e.msg);
+  *bytes_out = ffn_workspace_bytes(tokens, model, hidden, flags & ZERO_FFN_BACKWARD, flags & ZERO_FFN_UNALIGNED);
+  return ZERO_OK;
+}
+
+int zero_ffn_forward(const uint16_t* x, int64_t x_row_stride, int64_t tokens, int64_t model, int64_t hidden,
+                     const uint16_t* w_gate, const uint16_t* w_up, const uint16_t* w_down, int activation,
+                     uint16_t* y, int64_t y_row_stride, const zero_ffn_checkpoint* save, void* workspace,
+                     int64_t workspace_bytes, void* stream) {
+  TraceRange tr("zero_ffn_forward");
+  Err e;
+  int st = check_ffn_shape(tokens, model, hidden, e);
+  if (st) return fail(st, e.msg);
+  FfnParams p;
+  memset(&p, 0, sizeof p);
+  p.x = x;
+  p.x_row = tokens > 1 ? x_row_stride : model;
+  p.y = y;
+  p.y_row = tokens > 1 ? y_row_stride : model;
+  p.tokens = tokens;
+  p.model = model;
+  p.hidden = hidden;
+  p.w_gate = w_gate;
+  p.w_up = w_up;
+  p.w_down = w_down;
+  if (save) p.ckpt = *save;
+  p.save = save != nullptr;
+  p.activation = activation;
+  p.workspace = workspace;
+  st = check_ffn(false, x, x_row_stride, tokens, model, hidden, w_gate, w_up, w_down, activation, y, y_row_stride, save,
+                 nullptr, nullptr, nullptr, workspace, workspace_bytes,
+                 ffn_workspace_bytes(tokens, model, hidden, false, !ffn_weights_aligned(p)), e);
+  if (st) return fail(st, e.msg);
+  if (tokens == 0) return ZERO_OK;
+  set_path(true);
+  return hip_status(launch_ffn_forward(p, static_cast<hipStream_t>(stream)), "zero_ffn_forward");
+}
+
+int zero_ffn_backward(const uint16_t* dy, int64_t dy_row_stride, int64_t tokens, int64_t model, int64_t hidden,
+                      const zero_ffn_checkpoint* saved, const uint16_t* w_gate, const uint16_t* w_up,
+                      const uint16_t* w_down, int activation, uint16_t* dx, int64_t dx_row_stride, uint16_t* d_gate,
+                      uint16_t* d_up, uint16_t* d_down, void* workspace, int64_t workspace_bytes, void* stream) {
+  TraceRange tr("zero_ffn_backward");
+  Err e;
+  int st = check_ffn_shape(tokens, model, hidden, e);
+  if (st) return fail(st, e.msg);
+  FfnParams p;
+  memset(&p, 0, sizeof p);
+  p.x = dy;
+  p.x_row = tokens > 1 ? dy_row_stride : model;
+  p.y = dx;
+  p.y_row = tokens > 1 ? dx_row_stride : model;
+  p.tokens = tokens;
+  p.model = model;
+  p.hidden = hidden;
+  p.w_gate = w_gate;
+  p.w_up = w_up;
+  p.w_down = w_down;
+  p.d_gate = d_gate;
+  p.d_up = d_up;
+  p.d_down = d_down;
+  if (saved) p.ckpt = *saved;
+  p.activation = activation;
+  p.workspace = workspace;
+  st = check_ffn(true, dy, dy_row_stride, tokens, model, hidden, w_gate, w_up, w_down, activation, dx, dx_row_stride,
+                 saved, d_gate, d_up, d_down, workspace, workspace_bytes,
+                 tokens ? ffn_workspace_bytes(tokens, model, hidden, true, !ffn_weights_aligned(p)) : 0, e);
+  if (st) return fail(st, e.msg);
+  set_path(true);
+  return hip_status(launch_ffn_backward(p, static_cast<hipStream_t>(stream)), "zero_ffn_backward");
+}
+
 }  // extern "C"
