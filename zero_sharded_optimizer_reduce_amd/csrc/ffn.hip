@@ -30,7 +30,7 @@ namespace zero {
 namespace {
 
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
-typedef float f16 __attribute__((ext_vector_type(16)));
+typedef float f4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) void lds_void;
@@ -56,18 +56,15 @@ template <int R, int NW>
 struct RowStager {
   static constexpr int kN = R / 8 / NW;   // instructions of a wave
   static_assert(kN * 8 * NW == R, "every wave moves the same number of rows");
-  __amdgpu_buffer_rsrc_t rsrc, none;      // none: no bytes in range, a load through it gives zeros
-  int voff[kN], wave;
-  bool any;
-  // rows: how many of the tile's rows, from the first of this wave's on, the matrix has; lds_row:
-  // the wave's first row in LDS, first: the row of the matrix that goes there.
+  uint16_t* base;
+  int voff[kN], wave, bytes;   // bytes: from base on, 0 where the wave has no rows
+  // first: the matrix's row that is this wave's first; rows: how many it has from there on.
   __device__ __forceinline__ RowStager(const uint16_t* m, int64_t ld, int64_t first, int64_t rows, int kk, int wave_, int lane)
-      : wave(wave_), any(rows > 0) {
+      : wave(wave_) {
     const int64_t most = kN * 8;
     const int64_t n = rows < most ? rows : most;
-    uint16_t* base = const_cast<uint16_t*>(m + (any ? first : 0) * ld);
-    rsrc = __builtin_amdgcn_make_buffer_rsrc(base, 0, any ? static_cast<int>(((n - 1) * ld + kk) * 2) : 0, kRawFlags);
-    none = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(m), 0, 0, kRawFlags);
+    base = const_cast<uint16_t*>(m + (rows > 0 ? first : 0) * ld);
+    bytes = rows > 0 ? static_cast<int>(((n - 1) * ld + kk) * 2) : 0;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const int r = i * 8 + (lane >> 3);   // kN * 8 is a multiple of 16: the wave's first row shifts no piece
@@ -77,60 +74,60 @@ struct RowStager {
   }
   // A stage past the end is loaded too, so that the loads on their way can be
   // counted, but from nowhere.
-  __device__ __forceinline__ void one(uint16_t* lds, int k0, bool live, int i) const {
+  // end: bytes, or 0 for a stage past the end; at: bytes from a row's first column on
+  __device__ __forceinline__ void one(uint16_t* lds, int end, int at, int i) const {
 #ifdef __HIP_DEVICE_COMPILE__   // the builtin is unknown to the host pass
-    const bool l = live && any;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(l ? rsrc : none, (lds_void*)(lds + (wave * kN + i) * 8 * kBk), 16, voff[i],
-                                             l ? k0 * 2 : 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(__builtin_amdgcn_make_buffer_rsrc(base, 0, end, kRawFlags),
+                                             (lds_void*)(lds + (wave * kN + i) * 8 * kBk), 16, voff[i], at, 0, 0);
 #endif
   }
 };
 
 // Rows [k0, k0 + 64) and columns [col0, col0 + C) of an operand whose rows lie along
 // k: 64 rows of 2 C bytes, from which transposing reads take the columns.  Those
-// read 64 bytes of four rows together: the 64-byte piece c of row r lies at piece
-// c ^ (r & 3).  Rows past `end` read as zeros (the descriptor ends there), columns
+// read 32 bytes of rows r, r + 1, r + 2, r + 3 and 8 rows on together (r a multiple of 16, or 4 more):
+// the 32-byte piece c of row r lies at piece c ^ column_turn(r).  Rows past `end` read as zeros (the descriptor ends there), columns
 // past a row's end as the next row's: their results are dropped.
+__device__ __forceinline__ int column_turn(int r) { return (r & 3) * 2 + ((r >> 3) & 1); }
 template <int C, int NW>
 struct ColumnStager {
   static constexpr int kRows = 512 / C, kN = 64 / kRows / NW;   // rows of one instruction, instructions of a wave
   static_assert(kN * kRows * NW == 64 && (kN * kRows) % 4 == 0, "every wave moves the same number of pieces");
-  const uint16_t* m;
-  int64_t ld;
-  int cols, col0, voff[kN], wave;
-  __device__ __forceinline__ ColumnStager(const uint16_t* m_, int64_t ld_, int col0_, int cols_, int wave_, int lane)
-      : m(m_), ld(ld_), cols(cols_), col0(col0_), wave(wave_) {
+  int voff[kN], wave;
+  __device__ __forceinline__ ColumnStager(int64_t ld, int wave_, int lane) : wave(wave_) {
     const int row = lane / (64 / kRows), piece = lane % (64 / kRows);
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const int r = (wave * kN + i) * kRows + row;
-      voff[i] = r * static_cast<int>(ld) * 2 + (((piece >> 2) ^ (r & 3)) << 6) + (piece & 3) * 16;
+      voff[i] = r * static_cast<int>(ld) * 2 + (((piece >> 1) ^ column_turn(r)) << 5) + (piece & 1) * 16;
     }
   }
-  __device__ __forceinline__ void one(uint16_t* lds, const uint16_t* from, int k0, int end, bool live, int i) const {
+  __device__ __forceinline__ void one(uint16_t* lds, __amdgpu_buffer_rsrc_t rsrc, int i) const {
 #ifdef __HIP_DEVICE_COMPILE__
-    const int left = end - k0 < kBk ? end - k0 : kBk;
-    const bool l = live && left > 0;
-    uint16_t* base = const_cast<uint16_t*>(l ? from + k0 * ld + col0 : from);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        __builtin_amdgcn_make_buffer_rsrc(base, 0, l ? static_cast<int>(((left - 1) * ld + cols - col0) * 2) : 0, kRawFlags),
-        (lds_void*)(lds + (wave * kN + i) * 512), 16, voff[i], 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + (wave * kN + i) * 512), 16, voff[i], 0, 0, 0);
 #endif
   }
 };
-
-// Byte offset in a slot of the lane's first fragment piece: row first + (lane & 31),
-// piece lane >> 5, moved as RowStager moves it.  Pieces 2, 4 and 6 further on are at
-// the offset with bits 5 and 6 flipped.
-__device__ __forceinline__ int lane_at_row(int first, int lane) {
-  return (first + (lane & 31)) * kBk * 2 + (((lane >> 5) ^ ((lane >> 1) & 7)) << 4);
+// The rows of a stage: `at` is the first one's first column of the tile, `left` rows are there
+// from it on (none or less: nothing is read), `width` values from that column on.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t column_rows(const uint16_t* at, int left, int64_t ld, int width) {
+  const int rows = left < kBk ? left : kBk;
+  const int bytes = ((rows - 1) * static_cast<int>(ld) + width) * 2;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(at), 0, left > 0 ? bytes : 0, kRawFlags);
 }
-// What the lane points a transposing read at: row 8 * (lane >> 5) + ((lane >> 2) & 3),
-// columns first + 16 * ((lane >> 4) & 1) + 4 * (lane & 3).
+
+// Byte offset in a slot of the lane's fragment piece in the first half of a stage: row first +
+// (lane & 15), piece lane >> 4, moved as RowStager moves it.  The second half's is at
+// the offset with bit 6 flipped.
+__device__ __forceinline__ int lane_at_row(int first, int lane) {
+  return (first + (lane & 15)) * kBk * 2 + (((lane >> 4) ^ ((lane >> 1) & 7)) << 4);
+}
+// What the lane points a transposing read at: row 8 * (lane >> 4) + ((lane >> 2) & 3),
+// columns first + 4 * (lane & 3).  4 rows on, column_turn is the same.
 template <int C>
 __device__ __forceinline__ int lane_at_column(int first, int lane) {
-  return ((lane >> 5) * 8 + ((lane >> 2) & 3)) * C * 2 + (((first >> 5) ^ ((lane >> 2) & 3)) << 6) +
-         ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+  const int row = (lane >> 4) * 8 + ((lane >> 2) & 3);
+  return row * C * 2 + (((first >> 4) ^ column_turn(row)) << 5) + (lane & 3) * 8;
 }
 
 // 4 values down a column, twice: the transposing LDS read hands lane j of 16 the
@@ -198,7 +195,7 @@ __device__ __forceinline__ void activate_slope(float g, int act, float& a, float
   if (act == ZERO_FFN_SILU) {
     const float s = sigmoid(g);
     a = g * s;
-    slope = s * (1.0f + g * (1.0f - s));
+    slope = s + a * (1.0f - s);
     return;
   }
   const float s = sigmoid(gelu_inner(g));
@@ -247,7 +244,7 @@ struct Products {
   int format, act, save;
 };
 
-constexpr int kGroup = 8;  // tiles of q that one XCD's neighbours share
+constexpr int kGroup = 4;  // tiles of q that one XCD's neighbours share (2, 4 and 8 within 1%, 16 2% slower)
 
 // 8 values to memory, which is 16-byte aligned if vec; the first n of them.
 __device__ __forceinline__ void store8(uint16_t* dst, const float (&v)[8], int vec, int n) {
@@ -282,39 +279,37 @@ __device__ __forceinline__ u32x2 load_codes8(const uint8_t* src, int n) {
   return w;
 }
 
-// A block's sums, as the matrix cores leave them: lane l has column q = l & 31 and rows p = 8 u +
-// 4 * (l >> 5) + 0..3, u = 0..3.  After the exchange of halves between u and u + 1
-// it has 8 neighbours along p, 16 h + 8 * (l >> 5) + 0..7, h = 0, 1.
-__device__ __forceinline__ void octets(const f16& acc, float (&v)[2][8]) {
+// Two blocks' sums one after the other along p, as the matrix cores leave them: lane l has
+// column q = l & 15 and rows p = 4 * (l >> 4) + 0..3 of each.  After the exchange of
+// lanes 16 to 31 and 48 to 63 of the first for 0 to 15 and 32 to 47 of the second it has
+// 8 neighbours along p, octet_at(lane) + 0..7 of the 32.
+__device__ __forceinline__ int octet_at(int lane) { return ((lane >> 4) & 1) * 16 + (lane >> 5) * 8; }
+__device__ __forceinline__ void octet(const f4& lo, const f4& hi, float (&v)[8]) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t a = __float_as_uint(acc[8 * h + q]), b = __float_as_uint(acc[8 * h + 4 + q]);
+  for (int q = 0; q < 4; ++q) {
+    uint32_t a = __float_as_uint(lo[q]), b = __float_as_uint(hi[q]);
 #ifdef __HIP_DEVICE_COMPILE__
-      const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-      a = r[0];
-      b = r[1];
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
 #endif
-      v[h][q] = __uint_as_float(a);
-      v[h][4 + q] = __uint_as_float(b);
-    }
+    v[q] = __uint_as_float(a);
+    v[4 + q] = __uint_as_float(b);
+  }
 }
 
 // A tile of BP x BQ results by WP x WQ waves.
 template <int BP, int BQ, int WP, int WQ, bool PCOL, bool QCOL, Epilogue EPI>
 __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args) {
   constexpr int NW = WP * WQ;
-  constexpr int TP = BP / WP / 32, TQ = BQ / WQ / 32;   // 32 x 32 blocks of a wave
-  constexpr int kSlot = (BP > BQ ? BP : BQ) * kBk;
-  static_assert(EPI != kGated || (!PCOL && TP % 2 == 0), "gate's and up's blocks of a wave are side by side");
-  // Five places for an operand's part of one stage.  Separate arrays, so that the
+  constexpr int TP = BP / WP / 16, TQ = BQ / WQ / 16;   // 16 x 16 blocks of a wave
+  static_assert(TP % 2 == 0 && (EPI != kGated || (!PCOL && TP % 4 == 0)), "gate's and up's blocks of a wave are side by side");
+  // Two places for each operand's part of one stage.  Separate arrays, so that the
   // compiler can tell a load on its way into one from a read of another.
-  __shared__ __align__(16) uint16_t slot0[kSlot];
-  __shared__ __align__(16) uint16_t slot1[kSlot];
-  __shared__ __align__(16) uint16_t slot2[kSlot];
-  __shared__ __align__(16) uint16_t slot3[kSlot];
-  __shared__ __align__(16) uint16_t slot4[kSlot];
+  __shared__ __align__(16) uint16_t pslot0[BP * kBk];
+  __shared__ __align__(16) uint16_t pslot1[BP * kBk];
+  __shared__ __align__(16) uint16_t qslot0[BQ * kBk];
+  __shared__ __align__(16) uint16_t qslot1[BQ * kBk];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int id = xcd_order(blockIdx.x, gridDim.x);
   const int which = id >= args.first[2] ? 2 : id >= args.first[1] ? 1 : 0;
@@ -332,7 +327,7 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
   using QStager = std::conditional_t<QCOL, ColumnStager<BQ, NW>, RowStager<BQ, NW>>;
   auto p_stager = [&] {
     if constexpr (PCOL) {
-      return PStager(g.p, g.p_ld, p0, g.p_cols, wave, lane);
+      return PStager(g.p_ld, wave, lane);
     } else {
       constexpr int kMine = PStager::kN * 8;   // rows of a wave
       const int row = wave * kMine;
@@ -349,7 +344,7 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
   };
   auto q_stager = [&] {
     if constexpr (QCOL) {
-      return QStager(g.q, g.q_ld, q0, g.q_cols, wave, lane);
+      return QStager(g.q_ld, wave, lane);
     } else {
       const int row = wave * QStager::kN * 8;
       return QStager(g.q, g.q_ld, q0 + row, g.nq - q0 - row, g.kk, wave, lane);
@@ -358,205 +353,282 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
   const PStager sp = p_stager();
   const QStager sq = q_stager();
   constexpr int kP = PStager::kN, kQ = QStager::kN;
-  auto load_p = [&](uint16_t* lds, int k0, int i) {
-    const bool live = k0 < g.kk;
+  // Where the stage to load next comes from; next_p and next_q go on to it.
+  const int kk = g.kk;
+  const uint16_t* p_at = g.p + p0;
+  const uint16_t* q_at = g.q + q0;
+  const uint16_t* const p2_at = g.p2 + p0;
+  const int p_rows = g.p_end, p_ld = static_cast<int>(g.p_ld), q_ld = static_cast<int>(g.q_ld);
+  const int p_width = g.p_cols - p0, q_width = g.q_cols - q0;
+  int p_left = p_rows, q_left = g.q_end, p_turn = g.turn, p_k = -kBk, q_k = -kBk, p_byte = 0, q_byte = 0, p_end = 0, q_end = 0;
+  __amdgpu_buffer_rsrc_t p_from, q_from;
+  auto next_p = [&] {
     if constexpr (PCOL) {
-      const bool second = k0 >= g.turn;
-      sp.one(lds, second ? g.p2 : g.p, second ? k0 - g.turn : k0, g.p_end, live, i);
+      const bool turn = p_turn == 0;
+      p_at = turn ? p2_at : p_at;
+      p_left = turn ? p_rows : p_left;
+      p_from = column_rows(p_at, p_left, p_ld, p_width);
+      p_at += kBk * static_cast<int64_t>(p_ld);
+      p_left -= kBk;
+      p_turn -= kBk;
     } else {
-      sp.one(lds, k0, live, i);
+      p_k += kBk;
+      p_end = p_k < kk ? sp.bytes : 0;
+      p_byte = p_end ? p_k * 2 : 0;
     }
   };
-  auto load_q = [&](uint16_t* lds, int k0, int i) {
-    const bool live = k0 < g.kk;
-    if constexpr (QCOL)
-      sq.one(lds, g.q, k0, g.q_end, live, i);
+  auto next_q = [&] {
+    if constexpr (QCOL) {
+      q_from = column_rows(q_at, q_left, q_ld, q_width);
+      q_at += kBk * static_cast<int64_t>(q_ld);
+      q_left -= kBk;
+    } else {
+      q_k += kBk;
+      q_end = q_k < kk ? sq.bytes : 0;
+      q_byte = q_end ? q_k * 2 : 0;
+    }
+  };
+  auto load_p = [&](uint16_t* lds, int i) {
+    if constexpr (PCOL)
+      sp.one(lds, p_from, i);
     else
-      sq.one(lds, k0, live, i);
+      sp.one(lds, p_end, p_byte, i);
+  };
+  auto load_q = [&](uint16_t* lds, int i) {
+    if constexpr (QCOL)
+      sq.one(lds, q_from, i);
+    else
+      sq.one(lds, q_end, q_byte, i);
   };
 
   int at_p = PCOL ? lane_at_column<BP>(wp * (BP / WP), lane) : lane_at_row(wp * (BP / WP), lane);
   int at_q = QCOL ? lane_at_column<BQ>(wq * (BQ / WQ), lane) : lane_at_row(wq * (BQ / WQ), lane);
-  // A wave's operands for half a stage: two 16-wide pieces of the summed index.
-  struct Frags {
-    b8 p[2][TP], q[2][TQ];
-  };
-  constexpr int kReads = 2 * (TP + TQ);
-  auto read = [&](Frags& f, const uint16_t* ps, const uint16_t* qs, int half, int n) {
-    const int u = n / (TP + TQ), i = n - u * (TP + TQ);
-    if (i < TP) {
-      if constexpr (PCOL) {
-        const char* at = reinterpret_cast<const char*>(ps) + (at_p ^ (i << 6)) + (half * 32 + u * 16) * BP * 2;
-        f.p[u][i] = transpose8(at, at + 4 * BP * 2);
-      } else {
-        f.p[u][i] = *reinterpret_cast<const b8*>(reinterpret_cast<const char*>(ps) + (at_p ^ (half * 64 + u * 32)) + i * 32 * kBk * 2);
-      }
+  auto read_p = [&](const uint16_t* ps, int half, int i) {
+    if constexpr (PCOL) {
+      const char* at = reinterpret_cast<const char*>(ps) + (at_p ^ (i << 5)) + half * 32 * BP * 2;
+      return transpose8(at, at + 4 * BP * 2);
     } else {
-      const int j = i - TP;
-      if constexpr (QCOL) {
-        const char* at = reinterpret_cast<const char*>(qs) + (at_q ^ (j << 6)) + (half * 32 + u * 16) * BQ * 2;
-        f.q[u][j] = transpose8(at, at + 4 * BQ * 2);
-      } else {
-        f.q[u][j] = *reinterpret_cast<const b8*>(reinterpret_cast<const char*>(qs) + (at_q ^ (half * 64 + u * 32)) + j * 32 * kBk * 2);
-      }
+      return *reinterpret_cast<const b8*>(reinterpret_cast<const char*>(ps) + (at_p ^ (half * 64)) + i * 16 * kBk * 2);
+    }
+  };
+  auto read_q = [&](const uint16_t* qs, int half, int j) {
+    if constexpr (QCOL) {
+      const char* at = reinterpret_cast<const char*>(qs) + (at_q ^ (j << 5)) + half * 32 * BQ * 2;
+      return transpose8(at, at + 4 * BQ * 2);
+    } else {
+      return *reinterpret_cast<const b8*>(reinterpret_cast<const char*>(qs) + (at_q ^ (half * 64)) + j * 16 * kBk * 2);
     }
   };
 
-  f16 acc[TP][TQ] = {};
-  Frags f0, f1;
-  constexpr int kProducts = 2 * TP * TQ;
-  // Half a stage: the products of `now`, and between them, evenly, the reads of
-  // `then` and the loads of one operand (a wave issues in order: loads in a row hold
-  // its products up).  The compiler keeps the groups apart.
-  auto half = [&](const auto& load, auto n_loads, const Frags& now, Frags& then, const uint16_t* ps, const uint16_t* qs,
-                  int which_half) {
-    constexpr int kLoads = decltype(n_loads)::value;
+  // A stage is 2 TP steps: step s multiplies P's block s % TP by the TQ blocks of Q, both
+  // in half s / TP of the stage.  P's blocks are read two steps ahead (four places), Q's
+  // during the half before.  So Q's slot is free, and its next one needed, half-way; P's two
+  // steps before the end: a barrier at each, and from there on the loads of the stage
+  // after the next, a few per step (a wave issues in order: loads in a row hold its
+  // products up).  Each load has between half a stage and a whole one to arrive.
+  constexpr int kSteps = 2 * TP, kQSpan = TP - 2, kPSpan = TP;   // steps with loads
+  static_assert(kSteps % 4 == 0, "a stage starts with the first place");
+  f4 acc[TP][TQ] = {};
+  b8 fp[4], fq[2][TQ];
+  auto stage = [&](uint16_t* ps0, uint16_t* qs0, uint16_t* ps1, uint16_t* qs1) {
     // Addresses are formed anew: kept over the loop for every slot they would
     // not fit the registers.
     asm volatile("" : "+v"(at_p), "+v"(at_q));
 #pragma unroll
-    for (int s = 0; s < kLoads; ++s) {
-#pragma unroll
-      for (int k = s * kProducts / kLoads; k < (s + 1) * kProducts / kLoads; ++k) {
-        const int u = k / (TP * TQ), i = (k - u * TP * TQ) / TQ, j = k % TQ;
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(now.p[u][i], now.q[u][j], acc[i][j], 0, 0, 0);
+    for (int s = 0; s < kSteps; ++s) {
+      if (s == TP) {   // Q's next stage has arrived (all but P's loads), and this one's is read
+        __builtin_amdgcn_s_waitcnt(wait_vm_lds(kP));
+        wave_barrier();
+        next_q();
       }
-      load(s);
+      if (s == kSteps - 2) {   // the same of P
+        __builtin_amdgcn_s_waitcnt(wait_vm_lds(kQ));
+        wave_barrier();
+        next_p();
+      }
 #pragma unroll
-      for (int k = s * kReads / kLoads; k < (s + 1) * kReads / kLoads; ++k) read(then, ps, qs, which_half, k);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int j = s % TP * TQ / TP; j < (s % TP + 1) * TQ / TP; ++j)
+        fq[s < TP ? 1 : 0][j] = s < TP ? read_q(qs0, 1, j) : read_q(qs1, 0, j);
+      fp[(s + 2) % 4] = s + 2 < kSteps ? read_p(ps0, (s + 2) / TP, (s + 2) % TP) : read_p(ps1, 0, s + 2 - kSteps);
+      if (s >= TP && s < TP + kQSpan) {
+#pragma unroll
+        for (int i = (s - TP) * kQ / kQSpan; i < (s - TP + 1) * kQ / kQSpan; ++i) load_q(qs0, i);
+      }
+      const int r = s >= kSteps - 2 ? s - (kSteps - 2) : s + 2;   // steps since P's barrier
+      if (r < kPSpan) {
+#pragma unroll
+        for (int i = r * kP / kPSpan; i < (r + 1) * kP / kPSpan; ++i) load_p(s >= kSteps - 2 ? ps0 : ps1, i);
+      }
+#pragma unroll
+      for (int j = 0; j < TQ; ++j)
+        acc[s % TP][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp[s % 4], fq[s / TP][j], acc[s % TP][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);   // the steps stay apart
     }
   };
-  int k0 = 0;
-  // One stage: P and Q in ps0 and qs0, the next stage's in ps1 and qs1; the stage
-  // after that goes to ps2 and, once every wave has read this one, ps0.
-  auto stage = [&](uint16_t* ps0, uint16_t* qs0, uint16_t* ps1, uint16_t* qs1, uint16_t* ps2) {
-    half([&](int s) { load_p(ps2, k0 + 2 * kBk, s); }, std::integral_constant<int, kP>(), f0, f1, ps0, qs0, 1);
-    // the next stage has arrived (all but ps2's loads), and this one is read
-    __builtin_amdgcn_s_waitcnt(wait_vm_lds(kP));
-    wave_barrier();
-    half([&](int s) { load_q(ps0, k0 + 2 * kBk, s); }, std::integral_constant<int, kQ>(), f1, f0, ps1, qs1, 0);
-    return (k0 += kBk) < g.kk;
-  };
+  next_p();
 #pragma unroll
-  for (int i = 0; i < kP; ++i) load_p(slot0, 0, i);
+  for (int i = 0; i < kP; ++i) load_p(pslot0, i);
+  next_q();
 #pragma unroll
-  for (int i = 0; i < kQ; ++i) load_q(slot1, 0, i);
+  for (int i = 0; i < kQ; ++i) load_q(qslot0, i);
+  next_q();
 #pragma unroll
-  for (int i = 0; i < kP; ++i) load_p(slot2, kBk, i);
+  for (int i = 0; i < kQ; ++i) load_q(qslot1, i);
+  next_p();   // of P's second stage what the two steps before the first one would have loaded
+  constexpr int kAhead = 2 * kP / kPSpan;
 #pragma unroll
-  for (int i = 0; i < kQ; ++i) load_q(slot3, kBk, i);
-  __builtin_amdgcn_s_waitcnt(wait_vm(kP + kQ));
+  for (int i = 0; i < kAhead; ++i) load_p(pslot1, i);
+  __builtin_amdgcn_s_waitcnt(wait_vm(kQ + kAhead));
   wave_barrier();
 #pragma unroll
-  for (int k = 0; k < kReads; ++k) read(f0, slot0, slot1, 0, k);
-  while (stage(slot0, slot1, slot2, slot3, slot4) && stage(slot2, slot3, slot4, slot0, slot1) &&
-         stage(slot4, slot0, slot1, slot2, slot3) && stage(slot1, slot2, slot3, slot4, slot0) &&
-         stage(slot3, slot4, slot0, slot1, slot2)) {
-  }
+  for (int j = 0; j < TQ; ++j) fq[0][j] = read_q(qslot0, 0, j);
+  fp[0] = read_p(pslot0, 0, 0);
+  fp[1] = read_p(pslot0, 0, 1);
+  // Two stages each time, the second of zeros where their number is odd: with an exit
+  // between them the sums' registers were saved and restored at every turn.
+  int k0 = 0;
+  do {
+    stage(pslot0, qslot0, pslot1, qslot1);
+    stage(pslot1, qslot1, pslot0, qslot0);
+    k0 += 2 * kBk;
+  } while (k0 < kk);
   __builtin_amdgcn_s_waitcnt(wait_vm_lds(0));   // nothing is on its way into LDS any more
 
-  // Results.  The lane's token (or row) and its neighbours along p.
-  const int lq = lane & 31, lp = (lane >> 5) * 8;
-#pragma unroll
-  for (int j = 0; j < TQ; ++j) {
-    const int q = q0 + wq * (BQ / WQ) + j * 32 + lq;
+  // Results.  The lane's token (or row) and its neighbours along p.  FULL: the whole
+  // tile lies inside the matrix, and nothing is asked for each value.
+  const int np = g.np, nq = g.nq, out_cols = g.out_cols, out_vec = g.out_vec, act = args.act, format = args.format;
+  const int64_t out_ld = g.out_ld;
+  uint16_t* const out = g.out;
+  const int lp = octet_at(lane);
+  const int first_q = q0 + wq * (BQ / WQ) + (lane & 15);
+  const int first_p = p0 + wp * (kOwn / WP);   // the wave's: a multiple of 32
+  auto results = [&](auto full) {
+    constexpr bool FULL = decltype(full)::value;
     if constexpr (EPI == kStore) {
 #pragma unroll
-      for (int i = 0; i < TP; ++i) {
-        float v[2][8];
-        octets(acc[i][j], v);
+      for (int j = 0; j < TQ; ++j) {
+        const int q = first_q + j * 16;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int p = p0 + wp * (BP / WP) + i * 32 + h * 16 + lp;
-          if (q < g.nq && p < g.out_cols) store8(g.out + q * g.out_ld + p, v[h], g.out_vec, g.out_cols - p);
+        for (int i = 0; i < TP; i += 2) {
+          float v[8];
+          octet(acc[i][j], acc[i + 1][j], v);
+          const int p = first_p + i * 16 + lp;
+          if (FULL)
+            store8(out + q * out_ld + p, v, 1, 8);
+          else if (q < nq && p < out_cols)
+            store8(out + q * out_ld + p, v, out_vec, out_cols - p);
         }
       }
     } else if constexpr (EPI == kGated) {
+      const int save = args.save, blocks = args.blocks;
 #pragma unroll
-      for (int i = 0; i < TP / 2; ++i) {
-        float a[2][8], b[2][8], v[2][8];
-        octets(acc[i][j], a);
-        octets(acc[i + TP / 2][j], b);
-        const int pb = p0 + wp * (BP / WP / 2) + i * 32;   // the block's first: a multiple of 32
+      for (int j = 0; j < TQ; ++j) {
+        const int q = first_q + j * 16;
+        const int64_t row = static_cast<int64_t>(q) * np;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int i = 0; i < TP / 2; i += 2) {
+          float a[8], b[8], v[8];
+          octet(acc[i][j], acc[i + 1][j], a);
+          octet(acc[i + TP / 2][j], acc[i + TP / 2 + 1][j], b);
+          const int pb = first_p + i * 16, p = pb + lp;
 #pragma unroll
-          for (int n = 0; n < 8; ++n) v[h][n] = activate(a[h][n], args.act) * b[h][n];
-          const int p = pb + h * 16 + lp;
-          if (q < g.nq && p < g.out_cols) store8(g.out + q * g.out_ld + p, v[h], 1, 8);   // the workspace's: whole octets
-        }
-        if (args.save) {
-          // 32 neighbours are one block: the lane's 16 and those of lane ^ 32
-          auto keep = [&](const float (&x)[2][8], const Act8Rows& to) {
+          for (int n = 0; n < 8; ++n) v[n] = activate(a[n], act) * b[n];
+          if (FULL || (q < nq && p < out_cols)) store8(out + q * out_ld + p, v, 1, 8);   // the workspace's: whole octets
+          if (!save) continue;
+          // 32 neighbours are one block: the lane's 8 and those of lanes ^ 16, ^ 32, ^ 48
+          auto keep = [&](const float (&x)[8], const Act8Rows& to) {
             uint32_t top = 0;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int n = 0; n < 8; ++n) {
-                const uint32_t m = __float_as_uint(x[h][n]) & 0x7FFFFFFFu;
-                top = m > top ? m : top;
-              }
-            const uint32_t other = __shfl_xor(top, 32, 64);
-            top = other > top ? other : top;
-            const uint32_t byte = act8_scale_byte(top, args.format);
-            const float inverse = act8_inverse(byte);
-            if (q >= g.nq) return;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int p = pb + h * 16 + lp;
-              const u32x2 w = {act8_codes(x[h][0], x[h][1], x[h][2], x[h][3], inverse, args.format),
-                               act8_codes(x[h][4], x[h][5], x[h][6], x[h][7], inverse, args.format)};
-              if (p < g.np) store_codes8(to.codes + static_cast<int64_t>(q) * g.np + p, w, g.np - p);
+            for (int n = 0; n < 8; ++n) {
+              const uint32_t m = __float_as_uint(x[n]) & 0x7FFFFFFFu;
+              top = m > top ? m : top;
             }
-            if (lane < 32 && pb < g.np) to.scales[static_cast<int64_t>(q) * args.blocks + (pb >> 5)] = static_cast<uint8_t>(byte);
+#pragma unroll
+            for (int off = 16; off <= 32; off <<= 1) {
+              const uint32_t other = __shfl_xor(top, off, 64);
+              top = other > top ? other : top;
+            }
+            const uint32_t byte = act8_scale_byte(top, format);
+            const float inverse = act8_inverse(byte);
+            const u32x2 w = {act8_codes(x[0], x[1], x[2], x[3], inverse, format),
+                             act8_codes(x[4], x[5], x[6], x[7], inverse, format)};
+            if (!FULL && (q >= nq || p >= np)) return;
+            store_codes8(to.codes + row + p, w, FULL ? 8 : np - p);
+            if (lane < 16) to.scales[static_cast<int64_t>(q) * blocks + (pb >> 5)] = static_cast<uint8_t>(byte);
           };
           keep(a, args.gate);
           keep(b, args.up);
         }
       }
     } else {
+      // The checkpoints' codes of 16 rows, fetched while the rows before are computed.
+      struct Held {
+        u32x2 g[TP / 2], u[TP / 2];
+        uint32_t sg[TP / 2], su[TP / 2];
+      };
+      const Act8Rows gate = args.gate, up = args.up;
+      const int blocks = args.blocks;
+      auto fetch = [&](int j) {
+        Held x;
+        const int q = first_q + j * 16;
+        const int64_t row = static_cast<int64_t>(q) * np + first_p + lp, at = static_cast<int64_t>(q) * blocks + (first_p >> 5);
 #pragma unroll
-      for (int i = 0; i < TP; ++i) {
-        float dh[2][8];
-        octets(acc[i][j], dh);
-        const int pb = p0 + wp * (BP / WP) + i * 32;
-        if (q >= g.nq || pb >= g.out_cols) continue;
-        const bool some = pb < g.np;   // else: the pitch's zeros
-        const int64_t at = static_cast<int64_t>(q) * args.blocks + (pb >> 5);
-        const float sg = some ? act8_scale(args.gate.scales[at]) : 0.0f, su = some ? act8_scale(args.up.scales[at]) : 0.0f;
+        for (int i = 0; i < TP / 2; ++i) {
+          const int left = np - first_p - i * 32 - lp;   // of this lane's octet on
+          const bool some = FULL || (q < nq && left > 0);
+          x.sg[i] = some ? gate.scales[at + i] : 0u;
+          x.su[i] = some ? up.scales[at + i] : 0u;
+          x.g[i] = some ? load_codes8(gate.codes + row + i * 32, FULL ? 8 : left) : u32x2{};
+          x.u[i] = some ? load_codes8(up.codes + row + i * 32, FULL ? 8 : left) : u32x2{};
+        }
+        return x;
+      };
+      uint16_t* const du_out = args.du;
+      uint16_t* const h_out = args.h;
+      const int64_t h_ld = args.h_ld;
+      Held next = fetch(0);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int p = pb + h * 16 + lp;
-          const u32x2 wg = load_codes8(args.gate.codes + static_cast<int64_t>(q) * g.np + p, g.np - p);
-          const u32x2 wu = load_codes8(args.up.codes + static_cast<int64_t>(q) * g.np + p, g.np - p);
+      for (int j = 0; j < TQ; ++j) {
+        const Held x = next;
+        if (j + 1 < TQ) next = fetch(j + 1);
+        const int q = first_q + j * 16;
+#pragma unroll
+        for (int i = 0; i < TP; i += 2) {
+          float dh[8];
+          octet(acc[i][j], acc[i + 1][j], dh);
+          const int p = first_p + i * 16 + lp;
+          const float sg = act8_scale(x.sg[i / 2]), su = act8_scale(x.su[i / 2]);
           float dg[8], du[8], hv[8];
 #pragma unroll
           for (int n4 = 0; n4 < 2; ++n4) {
             float gv[4], uv[4];
-            act8_values(wg[n4], sg, args.format, gv);
-            act8_values(wu[n4], su, args.format, uv);
+            act8_values(x.g[i / 2][n4], sg, format, gv);
+            act8_values(x.u[i / 2][n4], su, format, uv);
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
               const int k = n4 * 4 + n;
               float a, slope;
-              activate_slope(gv[n], args.act, a, slope);
+              activate_slope(gv[n], act, a, slope);
               // past the matrix's columns the sums are of something else
-              const bool in_row = p + k < g.np;
-              dg[k] = in_row ? dh[h][k] * uv[n] * slope : 0.0f;
-              du[k] = in_row ? dh[h][k] * a : 0.0f;
+              const bool in_row = FULL || p + k < np;
+              dg[k] = in_row ? dh[k] * uv[n] * slope : 0.0f;
+              du[k] = in_row ? dh[k] * a : 0.0f;
               hv[k] = in_row ? a * uv[n] : 0.0f;
             }
           }
-          if (p < g.out_cols) {   // the workspace's: whole octets
-            store8(g.out + q * g.out_ld + p, dg, 1, 8);
-            store8(args.du + q * g.out_ld + p, du, 1, 8);
-            store8(args.h + q * args.h_ld + p, hv, 1, 8);
+          if (FULL || (q < nq && p < out_cols)) {   // the workspace's: whole octets
+            store8(out + q * out_ld + p, dg, 1, 8);
+            store8(du_out + q * out_ld + p, du, 1, 8);
+            store8(h_out + q * h_ld + p, hv, 1, 8);
           }
         }
       }
     }
-  }
+  };
+  if (q0 + BQ <= nq && p0 + kOwn <= np && (EPI != kStore || out_vec))
+    results(std::true_type());
+  else
+    results(std::false_type());
 }
 
 // ------------------------------------------------------------------ operands that the products cannot take
