@@ -207,6 +207,7 @@ __device__ __forceinline__ void activate_slope(float g, int act, float& a, float
 // ------------------------------------------------------------------ products
 enum Epilogue {
   kStore,      // out = the sums
+  kPartial,    // the FP32 sums of a part of the summed index, for ffn_join_kernel
   kGated,      // P is gate's and up's rows in turn: out = act(g) * u, and both into checkpoints
   kSlopes,     // sums are dh: dg, du and h from the checkpoints of g and u
 };
@@ -242,6 +243,10 @@ struct Products {
   int64_t h_ld;
   int blocks;              // scales of a row
   int format, act, save;
+  int rows;                // of a workgroup, with a few tokens
+  int splits, chunk;       // kPartial: parts of the summed index and their length, a multiple of 2 kBk
+  float* partial;          // kPartial: [splits][nq][pitch]
+  int64_t pitch;
 };
 
 constexpr int kGroup = 4;  // tiles of q that one XCD's neighbours share (2, 4 and 8 within 1%, 16 2% slower)
@@ -311,7 +316,9 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
   __shared__ __align__(16) uint16_t qslot0[BQ * kBk];
   __shared__ __align__(16) uint16_t qslot1[BQ * kBk];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int id = xcd_order(blockIdx.x, gridDim.x);
+  int id = xcd_order(blockIdx.x, gridDim.x);
+  const int split = EPI == kPartial ? id % args.splits : 0;
+  if constexpr (EPI == kPartial) id /= args.splits;
   const int which = id >= args.first[2] ? 2 : id >= args.first[1] ? 1 : 0;
   const Product& g = args.of[which];
   const int t = id - args.first[which];
@@ -321,6 +328,8 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
   const int tp = in / height, tq = group * kGroup + in - tp * height;
   const int wp = wave / WQ, wq = wave - wp * WQ;
 
+  const int k_first = EPI == kPartial ? split * args.chunk : 0;
+  const int kk = EPI == kPartial && g.kk - k_first > args.chunk ? args.chunk : g.kk - k_first;
   constexpr int kOwn = EPI == kGated ? BP / 2 : BP;   // values along p of a tile
   const int p0 = tp * kOwn, q0 = tq * BQ;
   using PStager = std::conditional_t<PCOL, ColumnStager<BP, NW>, RowStager<BP, NW>>;
@@ -336,9 +345,9 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
         constexpr int kHalf = BP / WP / 2;
         static_assert(kHalf % kMine == 0, "a wave stages rows of one of them");
         const int first = p0 + row / (2 * kHalf) * kHalf + row % kHalf;
-        return PStager(row / kHalf % 2 ? g.p2 : g.p, g.p_ld, first, g.np - first, g.kk, wave, lane);
+        return PStager(row / kHalf % 2 ? g.p2 : g.p, g.p_ld, first, g.np - first, kk, wave, lane);
       } else {
-        return PStager(g.p, g.p_ld, p0 + row, g.np - p0 - row, g.kk, wave, lane);
+        return PStager(g.p + k_first, g.p_ld, p0 + row, g.np - p0 - row, kk, wave, lane);
       }
     }
   };
@@ -347,20 +356,21 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
       return QStager(g.q_ld, wave, lane);
     } else {
       const int row = wave * QStager::kN * 8;
-      return QStager(g.q, g.q_ld, q0 + row, g.nq - q0 - row, g.kk, wave, lane);
+      return QStager(g.q + k_first, g.q_ld, q0 + row, g.nq - q0 - row, kk, wave, lane);
     }
   };
   const PStager sp = p_stager();
   const QStager sq = q_stager();
   constexpr int kP = PStager::kN, kQ = QStager::kN;
   // Where the stage to load next comes from; next_p and next_q go on to it.
-  const int kk = g.kk;
-  const uint16_t* p_at = g.p + p0;
-  const uint16_t* q_at = g.q + q0;
+  const bool past_turn = PCOL && k_first >= g.turn;   // a part that starts in p2
+  const int p_first = past_turn ? k_first - g.turn : k_first;
   const uint16_t* const p2_at = g.p2 + p0;
+  const uint16_t* p_at = (past_turn ? p2_at : g.p + p0) + (PCOL ? p_first * g.p_ld : 0);
+  const uint16_t* q_at = g.q + q0;
   const int p_rows = g.p_end, p_ld = static_cast<int>(g.p_ld), q_ld = static_cast<int>(g.q_ld);
   const int p_width = g.p_cols - p0, q_width = g.q_cols - q0;
-  int p_left = p_rows, q_left = g.q_end, p_turn = g.turn, p_k = -kBk, q_k = -kBk, p_byte = 0, q_byte = 0, p_end = 0, q_end = 0;
+  int p_left = p_rows - p_first, q_left = g.q_end, p_turn = past_turn ? -kBk : g.turn - k_first, p_k = -kBk, q_k = -kBk, p_byte = 0, q_byte = 0, p_end = 0, q_end = 0;
   __amdgpu_buffer_rsrc_t p_from, q_from;
   auto next_p = [&] {
     if constexpr (PCOL) {
@@ -519,6 +529,23 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
             store8(out + q * out_ld + p, v, out_vec, out_cols - p);
         }
       }
+    } else if constexpr (EPI == kPartial) {
+      float* const partial = args.partial + static_cast<int64_t>(split) * nq * args.pitch;
+#pragma unroll
+      for (int j = 0; j < TQ; ++j) {
+        const int q = first_q + j * 16;
+#pragma unroll
+        for (int i = 0; i < TP; i += 2) {
+          float v[8];
+          octet(acc[i][j], acc[i + 1][j], v);
+          const int p = first_p + i * 16 + lp;
+          if (FULL || (q < nq && p < args.pitch)) {
+            f4* to = reinterpret_cast<f4*>(partial + q * args.pitch + p);
+            to[0] = f4{v[0], v[1], v[2], v[3]};
+            to[1] = f4{v[4], v[5], v[6], v[7]};
+          }
+        }
+      }
     } else if constexpr (EPI == kGated) {
       const int save = args.save, blocks = args.blocks;
 #pragma unroll
@@ -631,6 +658,219 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
     results(std::false_type());
 }
 
+// ------------------------------------------------------------------ parts of a long sum
+// Where a product has fewer tiles than the card has room for, several workgroups share a
+// tile's sum and this adds their parts up, in order.
+struct JoinArgs {
+  const float* partial;
+  int64_t pitch;
+  int splits, nq, np;
+  uint16_t* out;
+  int64_t out_ld;
+  int out_vec;
+};
+__global__ __launch_bounds__(256) void ffn_join_kernel(JoinArgs a) {
+  const int64_t pieces = a.pitch / 8, n = a.nq * pieces;
+  const int64_t k = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (k >= n) return;
+  const int64_t q = k / pieces;
+  const int p = static_cast<int>(k - q * pieces) * 8;
+  f4 lo = {}, hi = {};
+  for (int s = 0; s < a.splits; ++s) {
+    const f4* from = reinterpret_cast<const f4*>(a.partial + (s * static_cast<int64_t>(a.nq) + q) * a.pitch + p);
+    lo += from[0];
+    hi += from[1];
+  }
+  const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  store8(a.out + q * a.out_ld + p, v, a.out_vec, a.np - p);
+}
+
+// ------------------------------------------------------------------ a few tokens
+// Up to kFewTokens tokens: the weights' way from memory is all that counts, and every
+// weight is used once.  No LDS on the way in: a wave takes RB blocks of 16 rows of P (of gate and
+// of up) as the matrix cores want them, a row's 64 bytes by 4 lanes, and the
+// tokens' the same way (from L2).  Fewer rows than the blocks have are the last one
+// several times, which costs no memory: so the workgroups get equal shares.  The waves of a workgroup
+// take turns along the summed index and add up at the end, in order, in LDS.
+// Rows and columns of any alignment are read where they lie.
+constexpr int kFewTokens = 32;
+constexpr int kFewStep = 64;   // summed index of a wave's turn: a cache line of each row
+
+// 8 values from `at` on, of which n are there; any alignment.
+__device__ __forceinline__ b8 load_piece(const uint16_t* at, int n) {
+  u32x4 w = {};
+  if (n >= 8) {
+    __builtin_memcpy(&w, at, 16);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < n) w[q >> 1] |= static_cast<uint32_t>(at[q]) << ((q & 1) * 16);
+  }
+  return __builtin_bit_cast(b8, w);
+}
+
+template <int TB, int NW, int RB, bool GATED>
+__global__ __launch_bounds__(NW * 64) void ffn_few_kernel(Products args) {
+  constexpr int M = GATED ? 2 : 1, kParts = M * RB * TB;
+  __shared__ f4 part[NW][kParts][64];
+  const Product& g = args.of[0];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int row0 = blockIdx.x * args.rows, kk = g.kk, nq = g.nq;
+  const int np = g.np - row0 < args.rows ? g.np : row0 + args.rows;   // where this workgroup's end
+  const uint16_t* w[M][RB];
+  const uint16_t* x[TB];
+#pragma unroll
+  for (int r = 0; r < RB; ++r) {
+    // rows past the end: the last one once more, their results are dropped
+    const int row = row0 + r * 16 + (lane & 15);
+    const int64_t at = (row < np ? row : np - 1) * g.p_ld + (lane >> 4) * 8;
+    w[0][r] = g.p + at;
+    if constexpr (GATED) w[1][r] = g.p2 + at;
+  }
+#pragma unroll
+  for (int b = 0; b < TB; ++b) {
+    const int q = b * 16 + (lane & 15);
+    x[b] = g.q + (q < nq ? q : nq - 1) * g.q_ld + (lane >> 4) * 8;
+  }
+  f4 acc[M][RB][TB] = {};
+  constexpr int kU = kFewStep / 32;
+  struct Frags {
+    b8 w[M][RB][kU], x[TB][kU];
+  };
+  auto load = [&](Frags& f, int k, auto whole) {
+    constexpr bool WHOLE = decltype(whole)::value;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int at = k + u * 32, n = WHOLE ? 8 : kk - at - (lane >> 4) * 8;
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int r = 0; r < RB; ++r) f.w[m][r][u] = load_piece(w[m][r] + at, n);
+#pragma unroll
+      for (int b = 0; b < TB; ++b) f.x[b][u] = load_piece(x[b] + at, n);
+    }
+    __builtin_amdgcn_sched_barrier(0);   // all on their way before the first is waited for
+  };
+  auto multiply = [&](const Frags& f) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+#pragma unroll
+          for (int b = 0; b < TB; ++b)
+            acc[m][r][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.w[m][r][u], f.x[b][u], acc[m][r][b], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // The wave's turns, one loaded ahead; each workgroup starts at another one, so that
+  // they do not all read the same columns of their rows, which lie in the same few channels.
+  const int whole = kk / kFewStep, turns = whole > wave ? (whole - wave - 1) / NW + 1 : 0;
+  int next = turns ? blockIdx.x % turns : 0;
+  auto place = [&] {
+    const int k = (next * NW + wave) * kFewStep;
+    next = next + 1 < turns ? next + 1 : 0;
+    return k;
+  };
+  Frags f0, f1;
+  if (turns) load(f0, place(), std::true_type());
+  int t = 0;
+  for (; t + 2 < turns; t += 2) {
+    load(f1, place(), std::true_type());
+    multiply(f0);
+    load(f0, place(), std::true_type());
+    multiply(f1);
+  }
+  if (t + 1 < turns) {
+    load(f1, place(), std::true_type());
+    multiply(f0);
+    multiply(f1);
+  } else if (turns) {
+    multiply(f0);
+  }
+  if (whole * kFewStep < kk && wave == whole % NW) {
+    load(f0, whole * kFewStep, std::false_type());
+    multiply(f0);
+  }
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+#pragma unroll
+      for (int b = 0; b < TB; ++b) part[wave][(m * RB + r) * TB + b][lane] = acc[m][r][b];
+  __syncthreads();
+  if (wave >= TB) return;
+  // Wave b: tokens 16 b to 16 b + 15, one per lane & 15; 4 neighbours along p of each block.
+  const int q = wave * 16 + (lane & 15), lp = (lane >> 4) * 4;
+  f4 sum[M][RB];
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      f4 v = part[0][(m * RB + r) * TB + wave][lane];
+#pragma unroll
+      for (int n = 1; n < NW; ++n) v += part[n][(m * RB + r) * TB + wave][lane];
+      sum[m][r] = v;
+    }
+#pragma unroll
+  for (int r = 0; r < RB; ++r) {
+    const int p = row0 + r * 16 + lp;
+    f4 v = sum[0][r];
+    if constexpr (GATED) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) v[n] = activate(v[n], args.act) * sum[1][r][n];
+    }
+    if (q >= nq || p >= np) continue;
+    const u32x2 two = {bf16x2(v[0], v[1]), bf16x2(v[2], v[3])};
+    uint16_t* dst = g.out + q * g.out_ld + p;
+    if (p + 4 <= np) {
+      __builtin_memcpy(dst, &two, 8);
+    } else {
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        if (p + n < np) dst[n] = static_cast<uint16_t>(two[n >> 1] >> ((n & 1) * 16));
+    }
+  }
+  if constexpr (GATED) {
+    static_assert(RB * 16 == ZERO_ACT8_BLOCK, "a workgroup has whole blocks of a checkpoint");
+    if (!args.save) return;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const Act8Rows& to = m ? args.up : args.gate;
+      uint32_t top = 0;   // rows past the end are copies of the last one, which is in this block
+#pragma unroll
+      for (int r = 0; r < RB; ++r)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const uint32_t v = __float_as_uint(sum[m][r][n]) & 0x7FFFFFFFu;
+          top = v > top ? v : top;
+        }
+#pragma unroll
+      for (int off = 16; off <= 32; off <<= 1) {
+        const uint32_t other = __shfl_xor(top, off, 64);
+        top = other > top ? other : top;
+      }
+      const uint32_t byte = act8_scale_byte(top, args.format);
+      const float inverse = act8_inverse(byte);
+      if (q >= nq) continue;
+#pragma unroll
+      for (int r = 0; r < RB; ++r) {
+        const int p = row0 + r * 16 + lp;
+        const uint32_t c = act8_codes(sum[m][r][0], sum[m][r][1], sum[m][r][2], sum[m][r][3], inverse, args.format);
+        uint8_t* dst = to.codes + static_cast<int64_t>(q) * g.np + p;
+        if (p + 4 <= np) {
+          __builtin_memcpy(dst, &c, 4);
+        } else {
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+            if (p + n < np) dst[n] = static_cast<uint8_t>(c >> (8 * n));
+        }
+      }
+      if (lane < 16) to.scales[static_cast<int64_t>(q) * args.blocks + blockIdx.x] = static_cast<uint8_t>(byte);
+    }
+  }
+}
+
 // ------------------------------------------------------------------ operands that the products cannot take
 // A matrix whose rows are not 16-byte aligned, or end inside a stage: copied to the
 // workspace with a pitch of whole stages, zeros behind each row.
@@ -700,8 +940,67 @@ hipError_t tiles(Products a, int n, hipStream_t s) {
     g.tiles_q = (g.nq + BQ - 1) / BQ;
     total += static_cast<int64_t>(g.tiles_p) * g.tiles_q;
   }
+  if (EPI == kPartial) total *= a.splits;
   hipLaunchKernelGGL((ffn_product_kernel<BP, BQ, WP, WQ, PCOL, QCOL, EPI>), dim3(static_cast<unsigned>(total)), dim3(WP * WQ * 64),
                      0, s, a);
+  return hipGetLastError();
+}
+
+// Gate and up: up to 32 rows of each by 8 waves (over 16 tokens by 4: more registers each);
+// down: up to 16 rows by 8.  A CU takes in some 25
+// bytes/ns from memory, so the CUs' shares decide: 1 token through gate and up of 4096 x 11008
+// takes as long as through 4096 x 14336 where every workgroup has 32 rows (2 on some CUs,
+// 1 on the others).
+template <bool GATED>
+hipError_t few(Products a, hipStream_t s) {
+  constexpr int kBlocks = GATED ? 2 : 1, kMost = kBlocks * 16, kCus = 256;
+  const int np = a.of[0].np, each = (np + kCus * kMost - 1) / (kCus * kMost);   // workgroups of a CU
+  const int rows = (np + kCus * each - 1) / (kCus * each);
+  a.rows = a.save ? kMost : rows < 8 ? 8 : rows;
+  const dim3 grid(static_cast<unsigned>((np + a.rows - 1) / a.rows));
+  constexpr int kWaves = GATED ? 4 : 8;
+  if (a.of[0].nq <= 16)
+    hipLaunchKernelGGL((ffn_few_kernel<1, 8, kBlocks, GATED>), grid, dim3(8 * 64), 0, s, a);
+  else
+    hipLaunchKernelGGL((ffn_few_kernel<2, kWaves, kBlocks, GATED>), grid, dim3(kWaves * 64), 0, s, a);
+  return hipGetLastError();
+}
+
+// How y's and dx's sums (nq rows of np values) are shared out: two workgroups for every CU, as
+// long as each has 512 of the summed index.  256 tokens through 4096 x 14336 have 64 tiles
+// of 128 x 128 for y.
+struct Parts {
+  int splits, chunk;
+  int64_t pitch, bytes;
+};
+Parts parts_of(int64_t np, int64_t nq, int64_t kk) {
+  constexpr int64_t kRoom = 512, kLeast = 512, kMost = 16;
+  Parts x = {1, 0, (np + 7) / 8 * 8, 0};
+  const int64_t n = (np + 127) / 128 * ((nq + 127) / 128);
+  if (n > kRoom / 2) return x;
+  int64_t splits = kRoom / n;
+  if (splits > kk / kLeast) splits = kk / kLeast;
+  if (splits > kMost) splits = kMost;
+  if (splits < 2) return x;
+  const int64_t chunk = ((kk + splits - 1) / splits + 2 * kBk - 1) / (2 * kBk) * (2 * kBk);
+  x.splits = static_cast<int>((kk + chunk - 1) / chunk);
+  x.chunk = static_cast<int>(chunk);
+  x.bytes = x.splits * nq * x.pitch * 4;
+  return x;
+}
+
+template <bool PCOL>
+hipError_t product_in_parts(Products a, const Parts& parts, void* room, hipStream_t s) {
+  a.splits = parts.splits;
+  a.chunk = parts.chunk;
+  a.pitch = parts.pitch;
+  a.partial = static_cast<float*>(room);
+  const Product& g = a.of[0];
+  const hipError_t e = tiles<128, 128, 2, 2, PCOL, false, kPartial>(a, 1, s);
+  if (e != hipSuccess) return e;
+  const JoinArgs j = {a.partial, a.pitch, a.splits, g.nq, g.np, g.out, g.out_ld, g.out_vec};
+  const int64_t n = g.nq * (a.pitch / 8);
+  hipLaunchKernelGGL(ffn_join_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, j);
   return hipGetLastError();
 }
 
@@ -729,11 +1028,13 @@ hipError_t product(const Products& a, int n, hipStream_t s) {
 int64_t ffn_workspace_bytes(int64_t tokens, int64_t model, int64_t hidden, bool backward, bool unaligned) {
   const int64_t dp = pad_up(model), fp = pad_up(hidden);
   auto bytes = [](int64_t elements) { return (elements * 2 + 255) / 256 * 256; };
+  if (!backward && tokens <= kFewTokens) return bytes(tokens * fp);
   int64_t n = bytes(tokens * dp);                                   // x or dy
   if (backward)
     n += bytes(tokens * 2 * fp) + bytes(tokens * fp) + bytes(tokens * dp);
   else
     n += bytes(tokens * fp);
+  n += bytes(parts_of(model, tokens, backward ? 2 * fp : fp).bytes / 2);
   if (unaligned || model % kPad || hidden % kPad) n += 2 * bytes(hidden * dp) + bytes(model * fp);
   return n;
 }
@@ -746,13 +1047,16 @@ hipError_t launch_ffn_forward(const FfnParams& p, hipStream_t s) {
   const int64_t t = p.tokens, d = p.model, f = p.hidden, dp = pad_up(d), fp = pad_up(f);
   Carver ws = {static_cast<char*>(p.workspace)};
   uint16_t* h = ws.take(t * fp);
-  uint16_t* x_room = ws.take(t * dp);
+  const bool is_few = t <= kFewTokens;
+  const Parts parts = is_few ? Parts{1, 0, 0, 0} : parts_of(d, t, fp);
+  uint16_t* parts_room = ws.take(parts.bytes / 2);
+  uint16_t* x_room = is_few ? nullptr : ws.take(t * dp);
   Matrix x = {p.x, p.x_row}, gate = {p.w_gate, d}, up = {p.w_up, d}, down = {p.w_down, f};
-  if (!aligned(x.at, x.ld) || d % kPad) {
+  if (!is_few && (!aligned(x.at, x.ld) || d % kPad)) {
     ZERO_TRY(pack(x.at, x.ld, x_room, dp, t, d, s));
     x = {x_room, dp};
   }
-  if (!ffn_weights_aligned(p) || d % kPad || f % kPad) {
+  if (!is_few && (!ffn_weights_aligned(p) || d % kPad || f % kPad)) {
     uint16_t* room[3] = {ws.take(f * dp), ws.take(f * dp), ws.take(d * fp)};
     ZERO_TRY(pack(gate.at, d, room[0], dp, f, d, s));
     ZERO_TRY(pack(up.at, d, room[1], dp, f, d, s));
@@ -780,12 +1084,12 @@ hipError_t launch_ffn_forward(const FfnParams& p, hipStream_t s) {
   g.q_ld = x.ld;
   g.np = static_cast<int>(f);
   g.nq = static_cast<int>(t);
-  g.kk = static_cast<int>(dp);
+  g.kk = static_cast<int>(is_few ? d : dp);
   g.out = h;
   g.out_ld = fp;
   g.out_cols = static_cast<int>(fp);
   g.out_vec = 1;
-  ZERO_TRY((product<false, false, kGated>(a, 1, s)));
+  ZERO_TRY((is_few ? few<true>(a, s) : product<false, false, kGated>(a, 1, s)));
   Products b = {};
   Product& y = b.of[0];
   y.p = down.at;
@@ -794,11 +1098,13 @@ hipError_t launch_ffn_forward(const FfnParams& p, hipStream_t s) {
   y.q_ld = fp;
   y.np = static_cast<int>(d);
   y.nq = static_cast<int>(t);
-  y.kk = static_cast<int>(fp);
+  y.kk = static_cast<int>(is_few ? f : fp);
   y.out = p.y;
   y.out_ld = p.y_row;
   y.out_cols = static_cast<int>(d);
   y.out_vec = aligned(p.y, p.y_row);
+  if (is_few) return few<false>(b, s);
+  if (parts.splits > 1) return product_in_parts<false>(b, parts, parts_room, s);
   return product<false, false, kStore>(b, 1, s);
 }
 
@@ -809,6 +1115,8 @@ hipError_t launch_ffn_backward(const FfnParams& p, hipStream_t s) {
   uint16_t* h = ws.take(t * fp);
   uint16_t* x = ws.take(t * dp);
   uint16_t* dy_room = ws.take(t * dp);
+  const Parts parts = parts_of(d, t, 2 * fp);
+  uint16_t* parts_room = ws.take(parts.bytes / 2);
   Matrix dy = {p.x, p.x_row}, gate = {p.w_gate, d}, up = {p.w_up, d}, down = {p.w_down, f};
   int dy_cols = static_cast<int>(d), w_cols = static_cast<int>(d), down_cols = static_cast<int>(f);
   if (!aligned(dy.at, dy.ld) || d % kPad) {
@@ -873,7 +1181,7 @@ hipError_t launch_ffn_backward(const FfnParams& p, hipStream_t s) {
     y.out_ld = p.y_row;
     y.out_cols = static_cast<int>(d);
     y.out_vec = aligned(p.y, p.y_row);
-    ZERO_TRY((product<true, false, kStore>(b, 1, s)));
+    ZERO_TRY((parts.splits > 1 ? product_in_parts<true>(b, parts, parts_room, s) : product<true, false, kStore>(b, 1, s)));
   }
   Products c = {};
   for (int k = 0; k < 3; ++k) {
