@@ -36,42 +36,59 @@ __device__ __forceinline__ float act8_scale(uint32_t byte) {
 }
 
 // Four codes, lowest byte first.  Whole numbers: adding 1.5 * 2^23 rounds to the
-// nearest even and leaves the two's complement in the low byte.  A block without a
-// scale (inverse 0) has codes of 0 and reads back as NaN.
-__device__ __forceinline__ uint32_t act8_codes(float a, float b, float c, float d, float inverse, int format) {
-  a *= inverse;
-  b *= inverse;
-  c *= inverse;
-  d *= inverse;
-  if (format == ZERO_ACT8_INT8) {
-    constexpr float kRound = 12582912.0f;
-    const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(b + kRound), __float_as_uint(a + kRound), 0x0C0C0400u);
-    const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(d + kRound), __float_as_uint(c + kRound), 0x04000C0Cu);
-    return inverse == 0.0f ? 0u : lo | hi;
-  }
+// nearest even and leaves the two's complement in the low byte.
+__device__ __forceinline__ uint32_t act8_int8(float a, float b, float c, float d) {
+  constexpr float kRound = 12582912.0f;
+  const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(b + kRound), __float_as_uint(a + kRound), 0x0C0C0400u);
+  const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(d + kRound), __float_as_uint(c + kRound), 0x04000C0Cu);
+  return lo | hi;
+}
+__device__ __forceinline__ uint32_t act8_e4m3(float a, float b, float c, float d) {
   uint32_t w = 0;
 #ifdef __HIP_DEVICE_COMPILE__
   w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, w, false);
   w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
 #endif
-  return inverse == 0.0f ? 0u : w;
+  return w;
 }
 
-// The values of four codes: exact products.
-__device__ __forceinline__ void act8_values(uint32_t w, float scale, int format, float (&v)[4]) {
+// N codes of N values (N a multiple of 4).  A block without a scale (inverse 0) has
+// codes of 0 and reads back as NaN.
+template <int N>
+__device__ __forceinline__ void act8_codes(const float (&x)[N], float inverse, int format, uint32_t (&w)[N / 4]) {
+  float v[N];
+#pragma unroll
+  for (int q = 0; q < N; ++q) v[q] = x[q] * inverse;
   if (format == ZERO_ACT8_INT8) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = static_cast<float>(static_cast<int32_t>(w << (24 - 8 * q)) >> 24) * scale;
-    return;
+    for (int q = 0; q < N / 4; ++q) w[q] = act8_int8(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+  } else {
+#pragma unroll
+    for (int q = 0; q < N / 4; ++q) w[q] = act8_e4m3(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
   }
+#pragma unroll
+  for (int q = 0; q < N / 4; ++q) w[q] = inverse == 0.0f ? 0u : w[q];
+}
+
+// What codes stand for before the scale: exact.
+template <int N>
+__device__ __forceinline__ void act8_numbers_int8(const uint32_t (&w)[N / 4], float (&v)[N]) {
+#pragma unroll
+  for (int q = 0; q < N; ++q) v[q] = static_cast<float>(static_cast<int8_t>(w[q / 4] >> (8 * (q & 3))));
+}
+template <int N>
+__device__ __forceinline__ void act8_numbers_e4m3(const uint32_t (&w)[N / 4], float (&v)[N]) {
 #ifdef __HIP_DEVICE_COMPILE__
   typedef float f2 __attribute__((ext_vector_type(2)));
-  const f2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), false);
-  const f2 hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), true);
-  v[0] = lo.x * scale;
-  v[1] = lo.y * scale;
-  v[2] = hi.x * scale;
-  v[3] = hi.y * scale;
+#pragma unroll
+  for (int q = 0; q < N / 4; ++q) {
+    const f2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w[q]), false);
+    const f2 hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w[q]), true);
+    v[4 * q] = lo.x;
+    v[4 * q + 1] = lo.y;
+    v[4 * q + 2] = hi.x;
+    v[4 * q + 3] = hi.y;
+  }
 #endif
 }
 

@@ -137,9 +137,9 @@ __global__ __launch_bounds__(kThreads) void act8_save_kernel(SaveArgs a) {
     if (first + t >= a.u.total) continue;
     const uint32_t byte = act8_scale_byte(top, a.format);
     const float inverse = act8_inverse(byte);
-    u32x2 w;
-    w.x = act8_codes(v[n][0], v[n][1], v[n][2], v[n][3], inverse, a.format);
-    w.y = act8_codes(v[n][4], v[n][5], v[n][6], v[n][7], inverse, a.format);
+    uint32_t words[2];
+    act8_codes(v[n], inverse, a.format, words);
+    const u32x2 w = {words[0], words[1]};
     const int64_t c = static_cast<int64_t>(at[n].unit) * kUnit;
     uint8_t* out = a.codes + at[n].row * a.u.cols + c;
     if (c + kUnit <= a.u.cols) {
@@ -196,26 +196,30 @@ __global__ __launch_bounds__(kThreads) void act8_load_kernel(LoadArgs a) {
     const int64_t c = static_cast<int64_t>(at[n].unit) * kUnit;
     if (first + t >= a.u.total || c >= a.u.cols) continue;
     const float scale = act8_scale(byte[n]);
-    float lo[4], hi[4];
-    act8_values(w[n].x, scale, a.format, lo);
-    act8_values(w[n].y, scale, a.format, hi);
+    const uint32_t words[2] = {w[n].x, w[n].y};
+    float v[kUnit];
+    if (a.format == ZERO_ACT8_INT8)
+      act8_numbers_int8(words, v);
+    else
+      act8_numbers_e4m3(words, v);
+#pragma unroll
+    for (int q = 0; q < kUnit; ++q) v[q] *= scale;   // exact
     if constexpr (F32) {
       float* out = static_cast<float*>(a.out) + at[n].row * a.out_row + c;
       if (c + kUnit <= a.u.cols) {
-        store_any(out, f32x4{lo[0], lo[1], lo[2], lo[3]});
-        store_any(out + 4, f32x4{hi[0], hi[1], hi[2], hi[3]});
+        store_any(out, f32x4{v[0], v[1], v[2], v[3]});
+        store_any(out + 4, f32x4{v[4], v[5], v[6], v[7]});
       } else {
 #pragma unroll
         for (int q = 0; q < kUnit; ++q)
-          if (c + q < a.u.cols) out[q] = q < 4 ? lo[q & 3] : hi[q & 3];
+          if (c + q < a.u.cols) out[q] = v[q];
       }
     } else {
       // whole numbers and e4m3 have less than BF16's 8 bits: rounded only below its normal values
       uint16_t* out = static_cast<uint16_t*>(a.out) + at[n].row * a.out_row + c;
       typedef __bf16 b8 __attribute__((ext_vector_type(8)));
-      b8 o;
-#pragma unroll
-      for (int q = 0; q < kUnit; ++q) o[q] = static_cast<__bf16>(q < 4 ? lo[q & 3] : hi[q & 3]);
+      typedef float f8 __attribute__((ext_vector_type(8)));
+      const b8 o = __builtin_convertvector((f8{v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]}), b8);
       if (c + kUnit <= a.u.cols) {
         store_any(out, o);
       } else {

@@ -42,8 +42,9 @@ constexpr int kRawFlags = 0x00020000;
 __host__ __device__ inline int64_t pad_up(int64_t n) { return (n + kPad - 1) / kPad * kPad; }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  return static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(lo))) |
-         (static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(hi))) << 16);
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{lo, hi}), b2));
 }
 
 // ------------------------------------------------------------------ staging
@@ -179,29 +180,29 @@ __device__ __forceinline__ float gelu_inner(float x) {
   return 2.0f * kGeluIn * z * (1.0f + kGeluCube * z * z);
 }
 
-__device__ __forceinline__ float activate(float g, int act) {
-  if (act == ZERO_FFN_SILU) return g * sigmoid(g);
-  if (act == ZERO_FFN_GELU) return g * sigmoid(gelu_inner(g));
+template <int ACT>
+__device__ __forceinline__ float activate(float g) {
+  if (ACT == ZERO_FFN_SILU) return g * sigmoid(g);
+  if (ACT == ZERO_FFN_GELU) return g * sigmoid(gelu_inner(g));
   return g < 0.0f ? 0.0f : g;   // NaN stays
 }
 
 // act(g) and its derivative (0 at ReLU's corner).
-__device__ __forceinline__ void activate_slope(float g, int act, float& a, float& slope) {
-  if (act == ZERO_FFN_RELU) {
+template <int ACT>
+__device__ __forceinline__ void activate_slope(float g, float& a, float& slope) {
+  if (ACT == ZERO_FFN_RELU) {
     a = g < 0.0f ? 0.0f : g;
     slope = g > 0.0f ? 1.0f : g <= 0.0f ? 0.0f : g;
     return;
   }
-  if (act == ZERO_FFN_SILU) {
-    const float s = sigmoid(g);
-    a = g * s;
-    slope = s + a * (1.0f - s);
-    return;
-  }
-  const float s = sigmoid(gelu_inner(g));
-  const float z = g < -16.0f ? -16.0f : g > 16.0f ? 16.0f : g;   // sigma' is 0 there
+  const float s = sigmoid(ACT == ZERO_FFN_SILU ? g : gelu_inner(g));
   a = g * s;
-  slope = s + z * s * (1.0f - s) * (2.0f * kGeluIn) * (1.0f + 3.0f * kGeluCube * z * z);
+  if (ACT == ZERO_FFN_SILU) {
+    slope = s + a * (1.0f - s);
+  } else {
+    const float z = g < -16.0f ? -16.0f : g > 16.0f ? 16.0f : g;   // sigma' is 0 there
+    slope = s + z * s * (1.0f - s) * (2.0f * kGeluIn) * (1.0f + 3.0f * kGeluCube * z * z);
+  }
 }
 
 // ------------------------------------------------------------------ products
@@ -303,8 +304,29 @@ __device__ __forceinline__ void octet(const f4& lo, const f4& hi, float (&v)[8])
   }
 }
 
-// A tile of BP x BQ results by WP x WQ waves.
-template <int BP, int BQ, int WP, int WQ, bool PCOL, bool QCOL, Epilogue EPI>
+// The largest magnitude of 8 values, as a whole number (NaN is above infinity), and the largest of
+// lanes l, l ^ 16, l ^ 32 and l ^ 48.
+__device__ __forceinline__ uint32_t top_of(const float (&x)[8]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int n = 0; n < 8; ++n) {
+    const uint32_t m = __float_as_uint(x[n]) & 0x7FFFFFFFu;
+    top = m > top ? m : top;
+  }
+  return top;
+}
+__device__ __forceinline__ uint32_t across_groups(uint32_t top) {
+#ifdef __HIP_DEVICE_COMPILE__
+  const auto a = __builtin_amdgcn_permlane16_swap(top, top, false, false);
+  top = a[0] > a[1] ? a[0] : a[1];
+  const auto b = __builtin_amdgcn_permlane32_swap(top, top, false, false);
+  top = b[0] > b[1] ? b[0] : b[1];
+#endif
+  return top;
+}
+
+// A tile of BP x BQ results by WP x WQ waves.  ACT: of kGated and kSlopes.
+template <int BP, int BQ, int WP, int WQ, bool PCOL, bool QCOL, Epilogue EPI, int ACT>
 __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args) {
   constexpr int NW = WP * WQ;
   constexpr int TP = BP / WP / 16, TQ = BQ / WQ / 16;   // 16 x 16 blocks of a wave
@@ -504,158 +526,139 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
   } while (k0 < kk);
   __builtin_amdgcn_s_waitcnt(wait_vm_lds(0));   // nothing is on its way into LDS any more
 
-  // Results.  The lane's token (or row) and its neighbours along p.  FULL: the whole
-  // tile lies inside the matrix, and nothing is asked for each value.
-  const int np = g.np, nq = g.nq, out_cols = g.out_cols, out_vec = g.out_vec, act = args.act, format = args.format;
+  // Results.  The lane's token (or row) and its neighbours along p; rows 16 apart follow.
+  const int np = g.np, nq = g.nq, out_cols = g.out_cols;
   const int64_t out_ld = g.out_ld;
-  uint16_t* const out = g.out;
   const int lp = octet_at(lane);
   const int first_q = q0 + wq * (BQ / WQ) + (lane & 15);
   const int first_p = p0 + wp * (kOwn / WP);   // the wave's: a multiple of 32
-  auto results = [&](auto full) {
-    constexpr bool FULL = decltype(full)::value;
-    if constexpr (EPI == kStore) {
+  uint16_t* out = g.out + first_q * out_ld + first_p + lp;
+  if constexpr (EPI == kStore) {
+    const int out_vec = g.out_vec;
 #pragma unroll
-      for (int j = 0; j < TQ; ++j) {
-        const int q = first_q + j * 16;
+    for (int j = 0; j < TQ; ++j, out += 16 * out_ld)
 #pragma unroll
-        for (int i = 0; i < TP; i += 2) {
-          float v[8];
-          octet(acc[i][j], acc[i + 1][j], v);
-          const int p = first_p + i * 16 + lp;
-          if (FULL)
-            store8(out + q * out_ld + p, v, 1, 8);
-          else if (q < nq && p < out_cols)
-            store8(out + q * out_ld + p, v, out_vec, out_cols - p);
+      for (int i = 0; i < TP; i += 2) {
+        float v[8];
+        octet(acc[i][j], acc[i + 1][j], v);
+        const int p = first_p + i * 16 + lp;
+        if (first_q + j * 16 < nq && p < out_cols) store8(out + i * 16, v, out_vec, out_cols - p);
+      }
+  } else if constexpr (EPI == kPartial) {
+    const int64_t pitch = args.pitch;
+    float* partial = args.partial + (static_cast<int64_t>(split) * nq + first_q) * pitch + first_p + lp;
+#pragma unroll
+    for (int j = 0; j < TQ; ++j, partial += 16 * pitch)
+#pragma unroll
+      for (int i = 0; i < TP; i += 2) {
+        float v[8];
+        octet(acc[i][j], acc[i + 1][j], v);
+        if (first_q + j * 16 < nq && first_p + i * 16 + lp < pitch) {
+          f4* to = reinterpret_cast<f4*>(partial + i * 16);
+          to[0] = f4{v[0], v[1], v[2], v[3]};
+          to[1] = f4{v[4], v[5], v[6], v[7]};
         }
       }
-    } else if constexpr (EPI == kPartial) {
-      float* const partial = args.partial + static_cast<int64_t>(split) * nq * args.pitch;
+  } else if constexpr (EPI == kGated) {
+    const int save = args.save, blocks = args.blocks, format = args.format;
+    const Act8Rows gate = args.gate, up = args.up;
+    int64_t row = static_cast<int64_t>(first_q) * np + first_p + lp, block = static_cast<int64_t>(first_q) * blocks + (first_p >> 5);
 #pragma unroll
-      for (int j = 0; j < TQ; ++j) {
-        const int q = first_q + j * 16;
+    for (int j = 0; j < TQ; ++j, out += 16 * out_ld, row += 16 * static_cast<int64_t>(np), block += 16 * static_cast<int64_t>(blocks)) {
+      const bool in_q = first_q + j * 16 < nq;
 #pragma unroll
-        for (int i = 0; i < TP; i += 2) {
-          float v[8];
-          octet(acc[i][j], acc[i + 1][j], v);
-          const int p = first_p + i * 16 + lp;
-          if (FULL || (q < nq && p < args.pitch)) {
-            f4* to = reinterpret_cast<f4*>(partial + q * args.pitch + p);
-            to[0] = f4{v[0], v[1], v[2], v[3]};
-            to[1] = f4{v[4], v[5], v[6], v[7]};
-          }
+      for (int i = 0; i < TP / 2; i += 2) {
+        float a[8], b[8], v[8];
+        octet(acc[i][j], acc[i + 1][j], a);
+        octet(acc[i + TP / 2][j], acc[i + TP / 2 + 1][j], b);
+        const int p = first_p + i * 16 + lp;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) v[n] = activate<ACT>(a[n]) * b[n];
+        if (in_q && p < out_cols) store8(out + i * 16, v, 1, 8);   // the workspace's: whole octets
+        if (!save) continue;
+        // 32 neighbours are one block: the lane's 8 and those of lanes ^ 16, ^ 32, ^ 48
+        auto keep = [&](const float (&x)[8], const Act8Rows& to) {
+          const uint32_t byte = act8_scale_byte(across_groups(top_of(x)), format);
+          uint32_t w[2];
+          act8_codes(x, act8_inverse(byte), format, w);
+          if (!in_q || p >= np) return;
+          store_codes8(to.codes + row + i * 16, u32x2{w[0], w[1]}, np - p);
+          if (lane < 16) to.scales[block + (i >> 1)] = static_cast<uint8_t>(byte);
+        };
+        keep(a, gate);
+        keep(b, up);
+      }
+    }
+  } else {
+    // The checkpoints' codes of 16 rows, fetched while the rows before are computed.
+    struct Held {
+      u32x2 g[TP / 2], u[TP / 2];
+      uint32_t sg[TP / 2], su[TP / 2];
+    };
+    const Act8Rows gate = args.gate, up = args.up;
+    const int blocks = args.blocks, format = args.format;
+    auto fetch = [&](int j) {
+      Held x;
+      const int q = first_q + j * 16;
+      const int64_t row = static_cast<int64_t>(q) * np + first_p + lp, block = static_cast<int64_t>(q) * blocks + (first_p >> 5);
+#pragma unroll
+      for (int i = 0; i < TP / 2; ++i) {
+        const int left = np - first_p - i * 32 - lp;   // of this lane's octet on
+        x.sg[i] = x.su[i] = 0;
+        x.g[i] = x.u[i] = u32x2{};
+        if (q < nq && left > 0) {
+          x.sg[i] = gate.scales[block + i];
+          x.su[i] = up.scales[block + i];
+          x.g[i] = load_codes8(gate.codes + row + i * 32, left);
+          x.u[i] = load_codes8(up.codes + row + i * 32, left);
         }
       }
-    } else if constexpr (EPI == kGated) {
-      const int save = args.save, blocks = args.blocks;
+      return x;
+    };
+    uint16_t* du_out = args.du + first_q * out_ld + first_p + lp;
+    uint16_t* h_out = args.h + first_q * args.h_ld + first_p + lp;
+    Held next = fetch(0);
 #pragma unroll
-      for (int j = 0; j < TQ; ++j) {
-        const int q = first_q + j * 16;
-        const int64_t row = static_cast<int64_t>(q) * np;
+    for (int j = 0; j < TQ; ++j, out += 16 * out_ld, du_out += 16 * out_ld, h_out += 16 * args.h_ld) {
+      const Held x = next;
+      if (j + 1 < TQ) next = fetch(j + 1);
 #pragma unroll
-        for (int i = 0; i < TP / 2; i += 2) {
-          float a[8], b[8], v[8];
-          octet(acc[i][j], acc[i + 1][j], a);
-          octet(acc[i + TP / 2][j], acc[i + TP / 2 + 1][j], b);
-          const int pb = first_p + i * 16, p = pb + lp;
+      for (int i = 0; i < TP; i += 2) {
+        float dh[8];
+        octet(acc[i][j], acc[i + 1][j], dh);
+        const int p = first_p + i * 16 + lp;
+        if (p + 8 > np) {   // past the matrix's columns the sums are of something else
 #pragma unroll
-          for (int n = 0; n < 8; ++n) v[n] = activate(a[n], act) * b[n];
-          if (FULL || (q < nq && p < out_cols)) store8(out + q * out_ld + p, v, 1, 8);   // the workspace's: whole octets
-          if (!save) continue;
-          // 32 neighbours are one block: the lane's 8 and those of lanes ^ 16, ^ 32, ^ 48
-          auto keep = [&](const float (&x)[8], const Act8Rows& to) {
-            uint32_t top = 0;
-#pragma unroll
-            for (int n = 0; n < 8; ++n) {
-              const uint32_t m = __float_as_uint(x[n]) & 0x7FFFFFFFu;
-              top = m > top ? m : top;
-            }
-#pragma unroll
-            for (int off = 16; off <= 32; off <<= 1) {
-              const uint32_t other = __shfl_xor(top, off, 64);
-              top = other > top ? other : top;
-            }
-            const uint32_t byte = act8_scale_byte(top, format);
-            const float inverse = act8_inverse(byte);
-            const u32x2 w = {act8_codes(x[0], x[1], x[2], x[3], inverse, format),
-                             act8_codes(x[4], x[5], x[6], x[7], inverse, format)};
-            if (!FULL && (q >= nq || p >= np)) return;
-            store_codes8(to.codes + row + p, w, FULL ? 8 : np - p);
-            if (lane < 16) to.scales[static_cast<int64_t>(q) * blocks + (pb >> 5)] = static_cast<uint8_t>(byte);
-          };
-          keep(a, args.gate);
-          keep(b, args.up);
+          for (int n = 0; n < 8; ++n) dh[n] = p + n < np ? dh[n] : 0.0f;
         }
-      }
-    } else {
-      // The checkpoints' codes of 16 rows, fetched while the rows before are computed.
-      struct Held {
-        u32x2 g[TP / 2], u[TP / 2];
-        uint32_t sg[TP / 2], su[TP / 2];
-      };
-      const Act8Rows gate = args.gate, up = args.up;
-      const int blocks = args.blocks;
-      auto fetch = [&](int j) {
-        Held x;
-        const int q = first_q + j * 16;
-        const int64_t row = static_cast<int64_t>(q) * np + first_p + lp, at = static_cast<int64_t>(q) * blocks + (first_p >> 5);
-#pragma unroll
-        for (int i = 0; i < TP / 2; ++i) {
-          const int left = np - first_p - i * 32 - lp;   // of this lane's octet on
-          const bool some = FULL || (q < nq && left > 0);
-          x.sg[i] = some ? gate.scales[at + i] : 0u;
-          x.su[i] = some ? up.scales[at + i] : 0u;
-          x.g[i] = some ? load_codes8(gate.codes + row + i * 32, FULL ? 8 : left) : u32x2{};
-          x.u[i] = some ? load_codes8(up.codes + row + i * 32, FULL ? 8 : left) : u32x2{};
+        const uint32_t wg[2] = {x.g[i / 2].x, x.g[i / 2].y}, wu[2] = {x.u[i / 2].x, x.u[i / 2].y};
+        float gv[8], uv[8];
+        if (format == ZERO_ACT8_INT8) {
+          act8_numbers_int8(wg, gv);
+          act8_numbers_int8(wu, uv);
+        } else {
+          act8_numbers_e4m3(wg, gv);
+          act8_numbers_e4m3(wu, uv);
         }
-        return x;
-      };
-      uint16_t* const du_out = args.du;
-      uint16_t* const h_out = args.h;
-      const int64_t h_ld = args.h_ld;
-      Held next = fetch(0);
+        const float sg = act8_scale(x.sg[i / 2]), su = act8_scale(x.su[i / 2]);
+        float dg[8], du[8], hv[8];
 #pragma unroll
-      for (int j = 0; j < TQ; ++j) {
-        const Held x = next;
-        if (j + 1 < TQ) next = fetch(j + 1);
-        const int q = first_q + j * 16;
-#pragma unroll
-        for (int i = 0; i < TP; i += 2) {
-          float dh[8];
-          octet(acc[i][j], acc[i + 1][j], dh);
-          const int p = first_p + i * 16 + lp;
-          const float sg = act8_scale(x.sg[i / 2]), su = act8_scale(x.su[i / 2]);
-          float dg[8], du[8], hv[8];
-#pragma unroll
-          for (int n4 = 0; n4 < 2; ++n4) {
-            float gv[4], uv[4];
-            act8_values(x.g[i / 2][n4], sg, format, gv);
-            act8_values(x.u[i / 2][n4], su, format, uv);
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              const int k = n4 * 4 + n;
-              float a, slope;
-              activate_slope(gv[n], act, a, slope);
-              // past the matrix's columns the sums are of something else
-              const bool in_row = FULL || p + k < np;
-              dg[k] = in_row ? dh[k] * uv[n] * slope : 0.0f;
-              du[k] = in_row ? dh[k] * a : 0.0f;
-              hv[k] = in_row ? a * uv[n] : 0.0f;
-            }
-          }
-          if (FULL || (q < nq && p < out_cols)) {   // the workspace's: whole octets
-            store8(out + q * out_ld + p, dg, 1, 8);
-            store8(du_out + q * out_ld + p, du, 1, 8);
-            store8(h_out + q * h_ld + p, hv, 1, 8);
-          }
+        for (int n = 0; n < 8; ++n) {
+          float a, slope;
+          const float u = uv[n] * su;
+          activate_slope<ACT>(gv[n] * sg, a, slope);
+          dg[n] = dh[n] * u * slope;
+          du[n] = dh[n] * a;
+          hv[n] = a * u;
+        }
+        if (first_q + j * 16 < nq && p < out_cols) {   // the workspace's: whole octets
+          store8(out + i * 16, dg, 1, 8);
+          store8(du_out + i * 16, du, 1, 8);
+          store8(h_out + i * 16, hv, 1, 8);
         }
       }
     }
-  };
-  if (q0 + BQ <= nq && p0 + kOwn <= np && (EPI != kStore || out_vec))
-    results(std::true_type());
-  else
-    results(std::false_type());
+  }
 }
 
 // ------------------------------------------------------------------ parts of a long sum
@@ -818,7 +821,12 @@ __global__ __launch_bounds__(NW * 64) void ffn_few_kernel(Products args) {
     f4 v = sum[0][r];
     if constexpr (GATED) {
 #pragma unroll
-      for (int n = 0; n < 4; ++n) v[n] = activate(v[n], args.act) * sum[1][r][n];
+      for (int n = 0; n < 4; ++n) {
+        const float a = args.act == ZERO_FFN_SILU   ? activate<ZERO_FFN_SILU>(v[n])
+                        : args.act == ZERO_FFN_GELU ? activate<ZERO_FFN_GELU>(v[n])
+                                                    : activate<ZERO_FFN_RELU>(v[n]);
+        v[n] = a * sum[1][r][n];
+      }
     }
     if (q >= nq || p >= np) continue;
     const u32x2 two = {bf16x2(v[0], v[1]), bf16x2(v[2], v[3])};
@@ -837,26 +845,20 @@ __global__ __launch_bounds__(NW * 64) void ffn_few_kernel(Products args) {
 #pragma unroll
     for (int m = 0; m < M; ++m) {
       const Act8Rows& to = m ? args.up : args.gate;
-      uint32_t top = 0;   // rows past the end are copies of the last one, which is in this block
+      // rows past the end are copies of the last one, which is in this block
+      float all[RB * 4];
 #pragma unroll
       for (int r = 0; r < RB; ++r)
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const uint32_t v = __float_as_uint(sum[m][r][n]) & 0x7FFFFFFFu;
-          top = v > top ? v : top;
-        }
-#pragma unroll
-      for (int off = 16; off <= 32; off <<= 1) {
-        const uint32_t other = __shfl_xor(top, off, 64);
-        top = other > top ? other : top;
-      }
-      const uint32_t byte = act8_scale_byte(top, args.format);
-      const float inverse = act8_inverse(byte);
+        for (int n = 0; n < 4; ++n) all[r * 4 + n] = sum[m][r][n];
+      const uint32_t byte = act8_scale_byte(across_groups(top_of(all)), args.format);
+      uint32_t codes[RB];
+      act8_codes(all, act8_inverse(byte), args.format, codes);
       if (q >= nq) continue;
 #pragma unroll
       for (int r = 0; r < RB; ++r) {
         const int p = row0 + r * 16 + lp;
-        const uint32_t c = act8_codes(sum[m][r][0], sum[m][r][1], sum[m][r][2], sum[m][r][3], inverse, args.format);
+        const uint32_t c = codes[r];
         uint8_t* dst = to.codes + static_cast<int64_t>(q) * g.np + p;
         if (p + 4 <= np) {
           __builtin_memcpy(dst, &c, 4);
@@ -927,7 +929,7 @@ hipError_t pack(const uint16_t* from, int64_t ld, uint16_t* to, int64_t pitch, i
   return hipGetLastError();
 }
 
-template <int BP, int BQ, int WP, int WQ, bool PCOL, bool QCOL, Epilogue EPI>
+template <int BP, int BQ, int WP, int WQ, bool PCOL, bool QCOL, Epilogue EPI, int ACT = 0>
 hipError_t tiles(Products a, int n, hipStream_t s) {
   int64_t total = 0;
   for (int k = 0; k < 3; ++k) {
@@ -941,7 +943,7 @@ hipError_t tiles(Products a, int n, hipStream_t s) {
     total += static_cast<int64_t>(g.tiles_p) * g.tiles_q;
   }
   if (EPI == kPartial) total *= a.splits;
-  hipLaunchKernelGGL((ffn_product_kernel<BP, BQ, WP, WQ, PCOL, QCOL, EPI>), dim3(static_cast<unsigned>(total)), dim3(WP * WQ * 64),
+  hipLaunchKernelGGL((ffn_product_kernel<BP, BQ, WP, WQ, PCOL, QCOL, EPI, ACT>), dim3(static_cast<unsigned>(total)), dim3(WP * WQ * 64),
                      0, s, a);
   return hipGetLastError();
 }
@@ -1004,15 +1006,24 @@ hipError_t product_in_parts(Products a, const Parts& parts, void* room, hipStrea
   return hipGetLastError();
 }
 
-template <bool PCOL, bool QCOL, Epilogue EPI>
+template <bool PCOL, bool QCOL, Epilogue EPI, int ACT = 0>
 hipError_t product(const Products& a, int n, hipStream_t s) {
   int64_t large = 0;
   for (int k = 0; k < n; ++k) {
     const int64_t own = EPI == kGated ? 128 : 256;
     large += (a.of[k].np + own - 1) / own * ((a.of[k].nq + 255) / 256);
   }
-  if (large >= 256) return tiles<256, 256, 2, 4, PCOL, QCOL, EPI>(a, n, s);
-  return tiles<128, 128, 2, 2, PCOL, QCOL, EPI>(a, n, s);
+  if (large >= 256) return tiles<256, 256, 2, 4, PCOL, QCOL, EPI, ACT>(a, n, s);
+  return tiles<128, 128, 2, 2, PCOL, QCOL, EPI, ACT>(a, n, s);
+}
+
+// The activation is a constant of the kernel: asked for each value, its code was 250 KB and did not
+// fit the instruction cache (dh's product of 8192 x 4096 x 14336: 967 us).
+template <bool PCOL, Epilogue EPI>
+hipError_t activated(const Products& a, hipStream_t s) {
+  if (a.act == ZERO_FFN_SILU) return product<PCOL, false, EPI, ZERO_FFN_SILU>(a, 1, s);
+  if (a.act == ZERO_FFN_GELU) return product<PCOL, false, EPI, ZERO_FFN_GELU>(a, 1, s);
+  return product<PCOL, false, EPI, ZERO_FFN_RELU>(a, 1, s);
 }
 
 }  // namespace
@@ -1089,7 +1100,7 @@ hipError_t launch_ffn_forward(const FfnParams& p, hipStream_t s) {
   g.out_ld = fp;
   g.out_cols = static_cast<int>(fp);
   g.out_vec = 1;
-  ZERO_TRY((is_few ? few<true>(a, s) : product<false, false, kGated>(a, 1, s)));
+  ZERO_TRY((is_few ? few<true>(a, s) : activated<false, kGated>(a, s)));
   Products b = {};
   Product& y = b.of[0];
   y.p = down.at;
@@ -1162,7 +1173,7 @@ hipError_t launch_ffn_backward(const FfnParams& p, hipStream_t s) {
   g.out_ld = 2 * fp;
   g.out_cols = static_cast<int>(fp);
   g.out_vec = 1;
-  ZERO_TRY((product<true, false, kSlopes>(a, 1, s)));
+  ZERO_TRY((activated<true, kSlopes>(a, s)));
   if (p.y) {   // dx
     Products b = {};
     Product& y = b.of[0];
