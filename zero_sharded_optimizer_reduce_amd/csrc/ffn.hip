@@ -231,7 +231,6 @@ struct Product {
   uint16_t* out;
   int64_t out_ld;
   int out_cols;            // columns that are written: np, or the pitch, with zeros
-  int out_vec;             // 16-byte stores are aligned
 };
 
 struct Products {
@@ -252,11 +251,12 @@ struct Products {
 
 constexpr int kGroup = 4;  // tiles of q that one XCD's neighbours share (2, 4 and 8 within 1%, 16 2% slower)
 
-// 8 values to memory, which is 16-byte aligned if vec; the first n of them.
-__device__ __forceinline__ void store8(uint16_t* dst, const float (&v)[8], int vec, int n) {
+// The first n of 8 values to memory, at any alignment: the memory takes whole pieces as they lie
+// (one by one they cost the gradients of 777 x 1301 from 1001 tokens 20 us instead of 13).
+__device__ __forceinline__ void store8(uint16_t* dst, const float (&v)[8], int n) {
   const u32x4 w = {bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7])};
-  if (vec && n >= 8) {
-    *reinterpret_cast<u32x4*>(dst) = w;
+  if (n >= 8) {
+    __builtin_memcpy(dst, &w, 16);
   } else {
 #pragma unroll
     for (int q = 0; q < 8; ++q)
@@ -340,17 +340,23 @@ __device__ __forceinline__ uint32_t across_groups(uint32_t top) {
 }
 
 // A tile of BP x BQ results by WP x WQ waves.  ACT: of kGated and kSlopes.
-template <int BP, int BQ, int WP, int WQ, bool PCOL, bool QCOL, Epilogue EPI, int ACT>
+template <int BP, int BQ, int WP, int WQ, int SLOTS, bool PCOL, bool QCOL, Epilogue EPI, int ACT>
 __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args) {
   constexpr int NW = WP * WQ;
   constexpr int TP = BP / WP / 16, TQ = BQ / WQ / 16;   // 16 x 16 blocks of a wave
   static_assert(TP % 2 == 0 && (EPI != kGated || (!PCOL && TP % 4 == 0)), "gate's and up's blocks of a wave are side by side");
-  // Two places for each operand's part of one stage.  Separate arrays, so that the
+  // SLOTS places for each operand's part of one stage.  Separate arrays, so that the
   // compiler can tell a load on its way into one from a read of another.
+  static_assert(SLOTS == 2 || SLOTS == 4, "see the loop");
+  constexpr bool MORE = SLOTS == 4;
   __shared__ __align__(16) uint16_t pslot0[BP * kBk];
   __shared__ __align__(16) uint16_t pslot1[BP * kBk];
+  __shared__ __align__(16) uint16_t pslot2[MORE ? BP * kBk : 1];
+  __shared__ __align__(16) uint16_t pslot3[MORE ? BP * kBk : 1];
   __shared__ __align__(16) uint16_t qslot0[BQ * kBk];
   __shared__ __align__(16) uint16_t qslot1[BQ * kBk];
+  __shared__ __align__(16) uint16_t qslot2[MORE ? BQ * kBk : 1];
+  __shared__ __align__(16) uint16_t qslot3[MORE ? BQ * kBk : 1];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   int id = xcd_order(blockIdx.x, gridDim.x);
   const int split = EPI == kPartial ? id % args.splits : 0;
@@ -470,25 +476,29 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
   // in half s / TP of the stage.  P's blocks are read two steps ahead (four places), Q's
   // during the half before.  So Q's slot is free, and its next one needed, half-way; P's two
   // steps before the end: a barrier at each, and from there on the loads of the stage
-  // after the next, a few per step (a wave issues in order: loads in a row hold its
-  // products up).  Each load has between half a stage and a whole one to arrive.
+  // SLOTS on into the free slot, a few per step (a wave issues in order: loads in a row
+  // hold its products up).  With two slots each load has between half a stage and a whole one to
+  // arrive.  Tiles of 128 x 128 gain nothing from four: a CU takes in 55 to 95 bytes/ns, and a
+  // stage of 32 KiB takes the 0.46 us that says.  Few tiles of 128 x 64, alone on their CU, do:
+  // dh's product of 1001 x 1301 x 777 takes 12.7 us with four, 16.5 with two.
   constexpr int kSteps = 2 * TP, kQSpan = TP - 2, kPSpan = TP;   // steps with loads
   static_assert(kSteps % 4 == 0, "a stage starts with the first place");
   f4 acc[TP][TQ] = {};
   b8 fp[4], fq[2][TQ];
-  auto stage = [&](uint16_t* ps0, uint16_t* qs0, uint16_t* ps1, uint16_t* qs1) {
+  // The stage in ps0 and qs0; the next in ps1 and qs1; the one before was in psp.
+  auto stage = [&](uint16_t* ps0, uint16_t* qs0, uint16_t* ps1, uint16_t* qs1, uint16_t* psp) {
     // Addresses are formed anew: kept over the loop for every slot they would
     // not fit the registers.
     asm volatile("" : "+v"(at_p), "+v"(at_q));
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      if (s == TP) {   // Q's next stage has arrived (all but P's loads), and this one's is read
-        __builtin_amdgcn_s_waitcnt(wait_vm_lds(kP));
+      if (s == TP) {   // Q's next stage has arrived (all but the loads after its own), and this one's is read
+        __builtin_amdgcn_s_waitcnt(wait_vm_lds((SLOTS - 1) * kP + (SLOTS - 2) * kQ));
         wave_barrier();
         next_q();
       }
       if (s == kSteps - 2) {   // the same of P
-        __builtin_amdgcn_s_waitcnt(wait_vm_lds(kQ));
+        __builtin_amdgcn_s_waitcnt(wait_vm_lds((SLOTS - 1) * kQ + (SLOTS - 2) * kP));
         wave_barrier();
         next_p();
       }
@@ -503,7 +513,7 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
       const int r = s >= kSteps - 2 ? s - (kSteps - 2) : s + 2;   // steps since P's barrier
       if (r < kPSpan) {
 #pragma unroll
-        for (int i = r * kP / kPSpan; i < (r + 1) * kP / kPSpan; ++i) load_p(s >= kSteps - 2 ? ps0 : ps1, i);
+        for (int i = r * kP / kPSpan; i < (r + 1) * kP / kPSpan; ++i) load_p(s >= kSteps - 2 ? ps0 : psp, i);
       }
 #pragma unroll
       for (int j = 0; j < TQ; ++j)
@@ -511,20 +521,25 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
       __builtin_amdgcn_sched_barrier(0);   // the steps stay apart
     }
   };
-  next_p();
-#pragma unroll
-  for (int i = 0; i < kP; ++i) load_p(pslot0, i);
-  next_q();
-#pragma unroll
-  for (int i = 0; i < kQ; ++i) load_q(qslot0, i);
-  next_q();
-#pragma unroll
-  for (int i = 0; i < kQ; ++i) load_q(qslot1, i);
-  next_p();   // of P's second stage what the two steps before the first one would have loaded
+  // The first SLOTS stages, of P's last one what the two steps before the first would have loaded.
   constexpr int kAhead = 2 * kP / kPSpan;
+  auto load_stage = [&](uint16_t* ps, uint16_t* qs, auto n_p) {
+    next_q();
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) load_p(pslot1, i);
-  __builtin_amdgcn_s_waitcnt(wait_vm(kQ + kAhead));
+    for (int i = 0; i < kQ; ++i) load_q(qs, i);
+    next_p();
+#pragma unroll
+    for (int i = 0; i < decltype(n_p)::value; ++i) load_p(ps, i);
+  };
+  load_stage(pslot0, qslot0, std::integral_constant<int, kP>());
+  if constexpr (MORE) {
+    load_stage(pslot1, qslot1, std::integral_constant<int, kP>());
+    load_stage(pslot2, qslot2, std::integral_constant<int, kP>());
+    load_stage(pslot3, qslot3, std::integral_constant<int, kAhead>());
+  } else {
+    load_stage(pslot1, qslot1, std::integral_constant<int, kAhead>());
+  }
+  __builtin_amdgcn_s_waitcnt(wait_vm((SLOTS - 1) * kQ + (SLOTS - 2) * kP + kAhead));
   wave_barrier();
 #pragma unroll
   for (int j = 0; j < TQ; ++j) fq[0][j] = read_q(qslot0, 0, j);
@@ -533,11 +548,21 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
   // Two stages each time, the second of zeros where their number is odd: with an exit
   // between them the sums' registers were saved and restored at every turn.
   int k0 = 0;
-  do {
-    stage(pslot0, qslot0, pslot1, qslot1);
-    stage(pslot1, qslot1, pslot0, qslot0);
-    k0 += 2 * kBk;
-  } while (k0 < kk);
+  if constexpr (MORE) {
+    while (true) {
+      stage(pslot0, qslot0, pslot1, qslot1, pslot3);
+      stage(pslot1, qslot1, pslot2, qslot2, pslot0);
+      if ((k0 += 2 * kBk) >= kk) break;
+      stage(pslot2, qslot2, pslot3, qslot3, pslot1);
+      stage(pslot3, qslot3, pslot0, qslot0, pslot2);
+      if ((k0 += 2 * kBk) >= kk) break;
+    }
+  } else {
+    do {
+      stage(pslot0, qslot0, pslot1, qslot1, pslot1);
+      stage(pslot1, qslot1, pslot0, qslot0, pslot0);
+    } while ((k0 += 2 * kBk) < kk);
+  }
   __builtin_amdgcn_s_waitcnt(wait_vm_lds(0));   // nothing is on its way into LDS any more
 
   // Results.  The lane's token (or row) and its neighbours along p; rows 16 apart follow.
@@ -548,7 +573,6 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
   const int first_p = p0 + wp * (kOwn / WP);   // the wave's: a multiple of 32
   uint16_t* out = g.out + first_q * out_ld + first_p + lp;
   if constexpr (EPI == kStore) {
-    const int out_vec = g.out_vec;
 #pragma unroll
     for (int j = 0; j < TQ; ++j, out += 16 * out_ld)
 #pragma unroll
@@ -556,7 +580,7 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
         float v[8];
         octet(acc[i][j], acc[i + 1][j], v);
         const int p = first_p + i * 16 + lp;
-        if (first_q + j * 16 < nq && p < out_cols) store8(out + i * 16, v, out_vec, out_cols - p);
+        if (first_q + j * 16 < nq && p < out_cols) store8(out + i * 16, v, out_cols - p);
       }
   } else if constexpr (EPI == kPartial) {
     const int64_t pitch = args.pitch;
@@ -588,7 +612,7 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
         const int p = first_p + i * 16 + lp;
 #pragma unroll
         for (int n = 0; n < 8; ++n) v[n] = activate<ACT>(a[n]) * b[n];
-        if (in_q && p < out_cols) store8(out + i * 16, v, 1, 8);   // the workspace's: whole octets
+        if (in_q && p < out_cols) store8(out + i * 16, v, 8);   // the workspace's: whole octets
         if (!save) continue;
         // 32 neighbours are one block: the lane's 8 and those of lanes ^ 16, ^ 32, ^ 48
         auto keep = [&](const float (&x)[8], const Act8Rows& to) {
@@ -669,9 +693,9 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
           hv[n] = a * u;
         }
         if (first_q + j * 16 < nq && p < out_cols) {   // the workspace's: whole octets
-          store8(out + i * 16, dg, 1, 8);
-          store8(du_out + i * 16, du, 1, 8);
-          store8(h_out + i * 16, hv, 1, 8);
+          store8(out + i * 16, dg, 8);
+          store8(du_out + i * 16, du, 8);
+          store8(h_out + i * 16, hv, 8);
         }
       }
     }
@@ -687,7 +711,6 @@ struct JoinArgs {
   int splits, nq, np;
   uint16_t* out;
   int64_t out_ld;
-  int out_vec;
 };
 __global__ __launch_bounds__(256) void ffn_join_kernel(JoinArgs a) {
   const int64_t pieces = a.pitch / 8, n = a.nq * pieces;
@@ -702,7 +725,7 @@ __global__ __launch_bounds__(256) void ffn_join_kernel(JoinArgs a) {
     hi += from[1];
   }
   const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-  store8(a.out + q * a.out_ld + p, v, a.out_vec, a.np - p);
+  store8(a.out + q * a.out_ld + p, v, a.np - p);
 }
 
 // ------------------------------------------------------------------ a few tokens
@@ -908,7 +931,7 @@ __global__ __launch_bounds__(256) void ffn_pack_kernel(PackArgs args) {
   for (int64_t k = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; k < n; k += static_cast<int64_t>(gridDim.x) * 256) {
     const int64_t r = k / pieces;
     const int c = static_cast<int>(k - r * pieces) * 8;
-    *reinterpret_cast<b8*>(a.to + r * a.pitch + c) = load_piece(a.from + r * a.ld + c, a.cols - c);
+    *reinterpret_cast<b8*>(a.to + k * 8) = load_piece(a.from + r * a.ld + c, a.cols - c);   // rows follow one another
   }
 }
 
@@ -948,7 +971,7 @@ struct Packing {
   }
 };
 
-template <int BP, int BQ, int WP, int WQ, bool PCOL, bool QCOL, Epilogue EPI, int ACT = 0>
+template <int BP, int BQ, int WP, int WQ, int SLOTS, bool PCOL, bool QCOL, Epilogue EPI, int ACT = 0>
 hipError_t tiles(Products a, int n, hipStream_t s) {
   int64_t total = 0;
   for (int k = 0; k < 3; ++k) {
@@ -962,7 +985,7 @@ hipError_t tiles(Products a, int n, hipStream_t s) {
     total += static_cast<int64_t>(g.tiles_p) * g.tiles_q;
   }
   if (EPI == kPartial) total *= a.splits;
-  hipLaunchKernelGGL((ffn_product_kernel<BP, BQ, WP, WQ, PCOL, QCOL, EPI, ACT>), dim3(static_cast<unsigned>(total)), dim3(WP * WQ * 64),
+  hipLaunchKernelGGL((ffn_product_kernel<BP, BQ, WP, WQ, SLOTS, PCOL, QCOL, EPI, ACT>), dim3(static_cast<unsigned>(total)), dim3(WP * WQ * 64),
                      0, s, a);
   return hipGetLastError();
 }
@@ -1017,9 +1040,9 @@ hipError_t product_in_parts(Products a, const Parts& parts, void* room, hipStrea
   a.pitch = parts.pitch;
   a.partial = static_cast<float*>(room);
   const Product& g = a.of[0];
-  const hipError_t e = tiles<128, 128, 2, 2, PCOL, false, kPartial>(a, 1, s);
+  const hipError_t e = tiles<128, 128, 2, 2, 2, PCOL, false, kPartial>(a, 1, s);
   if (e != hipSuccess) return e;
-  const JoinArgs j = {a.partial, a.pitch, a.splits, g.nq, g.np, g.out, g.out_ld, g.out_vec};
+  const JoinArgs j = {a.partial, a.pitch, a.splits, g.nq, g.np, g.out, g.out_ld};
   const int64_t n = g.nq * (a.pitch / 8);
   hipLaunchKernelGGL(ffn_join_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, j);
   return hipGetLastError();
@@ -1027,18 +1050,17 @@ hipError_t product_in_parts(Products a, const Parts& parts, void* room, hipStrea
 
 template <bool PCOL, bool QCOL, Epilogue EPI, int ACT = 0>
 hipError_t product(const Products& a, int n, hipStream_t s) {
-  int64_t large = 0;
-  for (int k = 0; k < n; ++k) {
-    const int64_t own = EPI == kGated ? 128 : 256;
-    large += (a.of[k].np + own - 1) / own * ((a.of[k].nq + 255) / 256);
-  }
-  if (large >= 256) return tiles<256, 256, 2, 4, PCOL, QCOL, EPI, ACT>(a, n, s);
+  auto count = [&](int bp, int bq) {
+    const int64_t own = EPI == kGated ? bp / 2 : bp;
+    int64_t t = 0;
+    for (int k = 0; k < n; ++k) t += (a.of[k].np + own - 1) / own * ((a.of[k].nq + bq - 1) / bq);
+    return t;
+  };
+  if (count(256, 256) >= 256) return tiles<256, 256, 2, 4, 2, PCOL, QCOL, EPI, ACT>(a, n, s);
   if constexpr (EPI == kGated || EPI == kSlopes) {
-    const int64_t own = EPI == kGated ? 64 : 128;
-    if ((a.of[0].np + own - 1) / own * ((a.of[0].nq + 127) / 128) <= 128 || a.of[0].nq <= 64)
-      return tiles<128, 64, 2, 2, PCOL, QCOL, EPI, ACT>(a, n, s);
+    if (count(128, 64) <= 256 || a.of[0].nq <= 64) return tiles<128, 64, 2, 2, 4, PCOL, QCOL, EPI, ACT>(a, n, s);
   }
-  return tiles<128, 128, 2, 2, PCOL, QCOL, EPI, ACT>(a, n, s);
+  return tiles<128, 128, 2, 2, 2, PCOL, QCOL, EPI, ACT>(a, n, s);
 }
 
 // The activation is a constant of the kernel: asked for each value, its code was 250 KB and did not
@@ -1118,7 +1140,6 @@ hipError_t launch_ffn_forward(const FfnParams& p, hipStream_t s) {
   g.out = h;
   g.out_ld = fp;
   g.out_cols = static_cast<int>(fp);
-  g.out_vec = 1;
   ZERO_TRY((is_few ? few<true>(a, s) : activated<false, kGated>(a, s)));
   Products b = {};
   Product& y = b.of[0];
@@ -1132,7 +1153,6 @@ hipError_t launch_ffn_forward(const FfnParams& p, hipStream_t s) {
   y.out = p.y;
   y.out_ld = p.y_row;
   y.out_cols = static_cast<int>(d);
-  y.out_vec = aligned(p.y, p.y_row);
   if (is_few) return few<false>(b, s);
   if (parts.splits > 1) return product_in_parts<false>(b, parts, parts_room, s);
   return product<false, false, kStore>(b, 1, s);
@@ -1188,7 +1208,6 @@ hipError_t launch_ffn_backward(const FfnParams& p, hipStream_t s) {
   g.out = dgu;
   g.out_ld = 2 * fp;
   g.out_cols = static_cast<int>(fp);
-  g.out_vec = 1;
   ZERO_TRY((activated<true, kSlopes>(a, s)));
   if (p.y) {   // dx
     Products b = {};
@@ -1207,7 +1226,6 @@ hipError_t launch_ffn_backward(const FfnParams& p, hipStream_t s) {
     y.out = p.y;
     y.out_ld = p.y_row;
     y.out_cols = static_cast<int>(d);
-    y.out_vec = aligned(p.y, p.y_row);
     ZERO_TRY((parts.splits > 1 ? product_in_parts<true>(b, parts, parts_room, s) : product<true, false, kStore>(b, 1, s)));
   }
   Products c = {};
@@ -1228,7 +1246,6 @@ hipError_t launch_ffn_backward(const FfnParams& p, hipStream_t s) {
     w.out = k == 0 ? p.d_gate : k == 1 ? p.d_up : p.d_down;
     w.out_ld = w.np;
     w.out_cols = w.np;
-    w.out_vec = aligned(w.out, w.out_ld);
   }
   return product<true, true, kStore>(c, 3, s);
 }
