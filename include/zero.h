@@ -62,7 +62,7 @@ extern "C" {
 /* 8-bit activations and the feed-forward block */
 #define ZERO_ACT8_BLOCK 32   /* neighbours of a row that share a power of two */
 #define ZERO_ACT8_MAX_COLS 2147483648
-#define ZERO_ACT8_MAX_VALUES 1099511627776
+#define ZERO_ACT8_MAX_VALUES 34359738368   /* rows filled up to whole blocks */
 #define ZERO_FFN_MAX_TOKENS 16777216
 #define ZERO_FFN_MAX_SIDE 262144
 #define ZERO_FFN_MAX_STRIDE 8388608
@@ -478,7 +478,8 @@ enum { ZERO_ACT8_INT8 = 0, ZERO_ACT8_E4M3 = 1 };
  *   scales        device, written: rows * ceil(cols / ZERO_ACT8_BLOCK) bytes.
  * Errors: ZERO_ERR_ARG (NULL, negative sizes, x_dtype, format, overlapping buffers),
  * ZERO_ERR_ALIGN, ZERO_ERR_SIZE (a row stride below cols or above ZERO_ACT8_MAX_COLS, more than
- * ZERO_ACT8_MAX_COLS columns or ZERO_ACT8_MAX_VALUES values), ZERO_ERR_HIP. */
+ * ZERO_ACT8_MAX_COLS columns, or than ZERO_ACT8_MAX_VALUES values with every row's last
+ * block filled up), ZERO_ERR_HIP. */
 int zero_act8_save(const void* x, int x_dtype, int64_t x_row_stride, int64_t rows, int64_t cols, int format,
                    uint8_t* codes, uint8_t* scales, void* stream);
 
@@ -508,7 +509,8 @@ typedef struct zero_ffn_checkpoint {
  * ZERO_FFN_UNALIGNED (room for aligned copies; sizes that are no multiples of 64
  * have that room anyway).
  * Errors: ZERO_ERR_ARG (NULL, unknown flags, tokens < 0, a side < 1), ZERO_ERR_SIZE
- * (sizes above ZERO_FFN_MAX_TOKENS, ZERO_FFN_MAX_SIDE). */
+ * (sizes above ZERO_FFN_MAX_TOKENS, ZERO_FFN_MAX_SIDE, or activations that
+ * zero_act8_save would refuse). */
 int zero_ffn_workspace(int64_t tokens, int64_t model, int64_t hidden, int flags, int64_t* bytes_out);
 
 /* Gated feed-forward block, forward:

@@ -18,7 +18,7 @@ ZERO_OFFLOAD_REDUCE, ZERO_OFFLOAD_ADAM, ZERO_OFFLOAD_REDUCE_ADAM = 0, 1, 2
 ZERO_NS_MAX_STEPS, ZERO_NS_MAX_MATS, ZERO_NS_MAX_SIDE = 16, 65535, 262144
 ZERO_NS_MAX_SIGMA, ZERO_NS_MAX_GAIN = 2, 16
 ZERO_BF16, ZERO_FP32 = 0, 1
-ZERO_ACT8_BLOCK, ZERO_ACT8_MAX_COLS, ZERO_ACT8_MAX_VALUES = 32, 2147483648, 1099511627776
+ZERO_ACT8_BLOCK, ZERO_ACT8_MAX_COLS, ZERO_ACT8_MAX_VALUES = 32, 2147483648, 34359738368
 ZERO_ACT8_INT8, ZERO_ACT8_E4M3 = 0, 1
 ZERO_FFN_MAX_TOKENS, ZERO_FFN_MAX_SIDE, ZERO_FFN_MAX_STRIDE = 16777216, 262144, 8388608
 ZERO_FFN_BACKWARD, ZERO_FFN_UNALIGNED = 1, 2

@@ -557,6 +557,10 @@ class FfnCheckpoint:
         return cls(zero_act8_buffers(tokens, model, device), zero_act8_buffers(tokens, hidden, device),
                    zero_act8_buffers(tokens, hidden, device), format)
 
+    def first(self, tokens: int) -> "FfnCheckpoint":
+        """The first rows of these buffers, as a checkpoint of so many tokens."""
+        return FfnCheckpoint(*([t[:tokens] for t in held] for held in (self.x, self.gate, self.up)), self.format)
+
     def buffers(self, tokens: int, model: int, hidden: int) -> _lib.FfnCheckpointBuffers:
         ptrs = [p for held, cols, what in ((self.x, model, "checkpoint.x "), (self.gate, hidden, "checkpoint.gate "),
                                            (self.up, hidden, "checkpoint.up "))

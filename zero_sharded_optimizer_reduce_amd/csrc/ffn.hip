@@ -1021,7 +1021,7 @@ Parts parts_of(int64_t np, int64_t nq, int64_t kk) {
   constexpr int64_t kRoom = 512, kLeast = 512, kMost = 16;
   Parts x = {1, 0, (np + 7) / 8 * 8, 0};
   const int64_t n = (np + 127) / 128 * ((nq + 127) / 128);
-  if (n > kRoom / 2) return x;
+  if (n == 0 || n > kRoom / 2) return x;
   int64_t splits = kRoom / n;
   if (splits > kk / kLeast) splits = kk / kLeast;
   if (splits > kMost) splits = kMost;
@@ -1170,11 +1170,11 @@ hipError_t launch_ffn_backward(const FfnParams& p, hipStream_t s) {
   Matrix dy = {p.x, p.x_row}, gate = {p.w_gate, d}, up = {p.w_up, d}, down = {p.w_down, f};
   int dy_cols = static_cast<int>(d), w_cols = static_cast<int>(d), down_cols = static_cast<int>(f);
   Packing packing;
-  if (!aligned(dy.at, dy.ld) || d % kPad) {
+  if (t > 0 && (!aligned(dy.at, dy.ld) || d % kPad)) {
     dy = packing.add(dy.at, dy.ld, dy_room, dp, t, d);
     dy_cols = static_cast<int>(dp);
   }
-  if (!ffn_weights_aligned(p) || d % kPad || f % kPad) {
+  if (t > 0 && (!ffn_weights_aligned(p) || d % kPad || f % kPad)) {
     gate = packing.add(gate.at, d, ws.take(f * dp), dp, f, d);
     up = packing.add(up.at, d, ws.take(f * dp), dp, f, d);
     down = packing.add(down.at, f, ws.take(d * fp), fp, d, f);
@@ -1182,8 +1182,10 @@ hipError_t launch_ffn_backward(const FfnParams& p, hipStream_t s) {
     down_cols = static_cast<int>(fp);
   }
   ZERO_TRY(packing.go(s));
-  Act8Params held = {x, dp, t, d, p.ckpt.x_codes, p.ckpt.x_scales, p.ckpt.format, 0};
-  ZERO_TRY(launch_act8_load(held, s));
+  if (t > 0) {
+    Act8Params held = {x, dp, t, d, p.ckpt.x_codes, p.ckpt.x_scales, p.ckpt.format, 0};
+    ZERO_TRY(launch_act8_load(held, s));
+  }
   // dh, and from it dg, du and h
   Products a = {};
   a.gate = {p.ckpt.gate_codes, p.ckpt.gate_scales};
@@ -1208,8 +1210,8 @@ hipError_t launch_ffn_backward(const FfnParams& p, hipStream_t s) {
   g.out = dgu;
   g.out_ld = 2 * fp;
   g.out_cols = static_cast<int>(fp);
-  ZERO_TRY((activated<true, kSlopes>(a, s)));
-  if (p.y) {   // dx
+  if (t > 0) ZERO_TRY((activated<true, kSlopes>(a, s)));
+  if (p.y && t > 0) {   // dx
     Products b = {};
     Product& y = b.of[0];
     y.p = gate.at;
@@ -1228,7 +1230,7 @@ hipError_t launch_ffn_backward(const FfnParams& p, hipStream_t s) {
     y.out_cols = static_cast<int>(d);
     ZERO_TRY((parts.splits > 1 ? product_in_parts<true>(b, parts, parts_room, s) : product<true, false, kStore>(b, 1, s)));
   }
-  Products c = {};
+  Products c = {};   // without tokens: sums of nothing, zeros
   for (int k = 0; k < 3; ++k) {
     Product& w = c.of[k];
     const bool last = k == 2;

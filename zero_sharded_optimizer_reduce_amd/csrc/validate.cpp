@@ -730,6 +730,11 @@ static int64_t matrix_bytes(int64_t rows, int64_t cols, int64_t row_stride, int6
   return rows && cols ? ((rows - 1) * row_stride + cols) * esz : 0;
 }
 
+// Rows of so many columns that a launch can take, each filled up to whole blocks.
+static int64_t act8_most_rows(int64_t cols) {
+  return ZERO_ACT8_MAX_VALUES / ((cols + ZERO_ACT8_BLOCK - 1) / ZERO_ACT8_BLOCK * ZERO_ACT8_BLOCK);
+}
+
 int check_act8(const char* what, const void* values, int dtype, int64_t row_stride, int64_t rows, int64_t cols,
                int format, const uint8_t* codes, const uint8_t* scales, Err& e) {
   if (dtype != ZERO_BF16 && dtype != ZERO_FP32)
@@ -739,7 +744,7 @@ int check_act8(const char* what, const void* values, int dtype, int64_t row_stri
   if (rows < 0 || cols < 0)
     return set_err(e, ZERO_ERR_ARG, "%s: negative size %lld x %lld", what, (long long)rows, (long long)cols);
   if (rows == 0 || cols == 0) return ZERO_OK;   // touches no buffer; NULL pointers allowed
-  if (cols > ZERO_ACT8_MAX_COLS || rows > ZERO_ACT8_MAX_VALUES / cols)
+  if (cols > ZERO_ACT8_MAX_COLS || rows > act8_most_rows(cols))
     return set_err(e, ZERO_ERR_SIZE, "%s: %lld x %lld values are too many", what, (long long)rows, (long long)cols);
   if (rows > 1 && (row_stride < cols || row_stride > ZERO_ACT8_MAX_COLS))
     return set_err(e, ZERO_ERR_SIZE, "%s: row stride %lld outside [cols=%lld, %lld]", what, (long long)row_stride,
@@ -763,6 +768,9 @@ int check_ffn_shape(int64_t tokens, int64_t model, int64_t hidden, Err& e) {
   if (tokens > ZERO_FFN_MAX_TOKENS || model > ZERO_FFN_MAX_SIDE || hidden > ZERO_FFN_MAX_SIDE)
     return set_err(e, ZERO_ERR_SIZE, "ffn: tokens=%lld, model=%lld, hidden=%lld: at most %d, %d and %d", (long long)tokens,
                    (long long)model, (long long)hidden, ZERO_FFN_MAX_TOKENS, ZERO_FFN_MAX_SIDE, ZERO_FFN_MAX_SIDE);
+  if (tokens > act8_most_rows(model > hidden ? model : hidden))
+    return set_err(e, ZERO_ERR_SIZE, "ffn: %lld tokens of %lld values are too many", (long long)tokens,
+                   (long long)(model > hidden ? model : hidden));
   return ZERO_OK;
 }
 

@@ -12,6 +12,10 @@ arithmetic step runs in the HIP kernels of libzero.
 * Zero3Chain        per-layer gather/release forward, reverse-order reduce and
                     update backward (essay, section ZeRO-3 的一次完整计算;
                     slide, note 原 N47)
+* Zero3FeedForward  a Zero3Chain of gated feed-forward blocks with the layers' own
+                    work: gather -> forward (activations kept in 8 bits) -> release;
+                    gather -> backward -> reduce-scatter -> owner update (essay,
+                    section ZeRO-3 的一次完整计算)
 * OffloadStep       host-resident gradient shard through two device slots (blog,
                     section 分片放到 CPU：两个缓冲就够)
 * MuonStep          matrices updated along an orthogonalised momentum instead of
@@ -31,8 +35,9 @@ from typing import Callable, Optional, Sequence, Tuple
 import torch
 
 from ._lib import ZERO_NORM_BLOCKS
-from .api import (ADAM_SCALARS_FLOATS, NS_COEFS, ZeroOffload, adam_scalars_tensor, zero_adam_scalars_fetch,
-                  zero_adam_shard_step, zero_adam_shard_step_dev, zero_all_gather_layer, zero_grad_norm_sq,
+from .api import (ADAM_SCALARS_FLOATS, FFN_ACTIVATIONS, NS_COEFS, FfnCheckpoint, ZeroOffload, adam_scalars_tensor,
+                  zero_adam_scalars_fetch, zero_adam_shard_step, zero_adam_shard_step_dev, zero_all_gather_layer,
+                  zero_ffn_backward, zero_ffn_forward, zero_ffn_workspace, zero_grad_norm_sq,
                   zero_muon_momentum, zero_muon_shard_step, zero_newton_schulz, zero_newton_schulz_workspace,
                   zero_reduce_scatter, zero_reduce_scatter_adam, zero_reduce_scatter_adam_dev,
                   zero_reduce_scatter_muon, zero_shard_layout)
@@ -357,6 +362,88 @@ class Zero3Chain:
         for k, (p, m, v, b) in enumerate(zip(*(self.owner_slices(u, x) for x in
                                               (self.master, self.exp_avg, self.exp_avg_sq, self.bf16)))):
             zero_adam_shard_step(p, m, v, b, self.grad_shards[k][:s], hp, stream=stream)
+
+
+class Zero3FeedForward(Zero3Chain):
+    """A Zero3Chain whose units are gated feed-forward blocks, (model, hidden) each,
+    with the layers' own work between the gathers and the reductions: w_gate, w_up
+    [hidden, model] and w_down [model, hidden] one after the other in a unit.
+
+    forward_layer runs every rank's tokens (at most max_tokens each) through the
+    gathered view and keeps what the backward pass needs in 8 bits (FfnCheckpoint,
+    one per layer and rank); backward_layer gathers the view again, writes every
+    rank's contributions and reduces and updates them as Zero3Chain does.  The ranks
+    may have different numbers of tokens (weights: their shares); one without tokens
+    contributes zeros.  Nothing is allocated after the construction, so a step can
+    be captured into a graph; the view, the workspace and the contributions are
+    shared by all layers and ranks, so the calls of one object belong on one stream."""
+
+    def __init__(self, layers: Sequence[Tuple[int, int]], n_ranks: int, max_tokens: int, activation: str = "silu",
+                 format: str = "int8", device="cuda"):
+        if activation not in FFN_ACTIVATIONS:
+            raise ValueError(f"activation: {activation!r} is none of {', '.join(FFN_ACTIVATIONS)}")
+        self.layers = [(int(m), int(h)) for m, h in layers]
+        super().__init__([(f"layer {k}", [("gate", m * h), ("up", m * h), ("down", m * h)])
+                          for k, (m, h) in enumerate(self.layers)], n_ranks, device)
+        self.activation, self.max_tokens = activation, int(max_tokens)
+        self.view = _empty(self.max_pad, torch.bfloat16, device)
+        self.checkpoints = [[FfnCheckpoint.empty(self.max_tokens, m, h, format, device) for _ in range(n_ranks)]
+                            for m, h in self.layers]
+        self.tokens = [[None] * n_ranks for _ in self.layers]   # of the kept forward passes
+        self.workspace = _empty(max(self._workspace_bytes(m, h) for m, h in self.layers), torch.uint8, device)
+
+    def _workspace_bytes(self, m: int, h: int) -> int:
+        """Of any call with at most max_tokens tokens: the room for sums in parts grows within 128
+        tokens and falls from one 128 to the next."""
+        unaligned = m * h % 8 != 0   # the view and the contributions start at allocations, the matrices follow
+        most = self.max_tokens
+        counts = {most, *range(128, min(most, 128 * 256) + 1, 128)}
+        return max(zero_ffn_workspace(t, m, h, backward=back, unaligned=unaligned, device="meta").numel()
+                   for t in counts for back in (False, True))
+
+    def _matrices(self, u: int, flat: torch.Tensor):
+        m, h = self.layers[u]
+        return [flat[k * m * h:(k + 1) * m * h].view(shape) for k, shape in enumerate(((h, m), (h, m), (m, h)))]
+
+    def _per_rank(self, *lists):
+        if any(len(x) != self.n for x in lists):
+            raise ValueError(f"one tensor for each of the {self.n} ranks")
+        return enumerate(zip(*lists))
+
+    def forward_layer(self, u: int, xs: Sequence[torch.Tensor], ys: Sequence[torch.Tensor], stream=None, keep: bool = True):
+        """ys[r] = layer u of rank r's tokens xs[r] ([tokens, model], BF16).  keep=False: nothing
+        is kept, for an evaluation."""
+        ranks = self._per_rank(xs, ys)
+        if any(x.shape[0] > self.max_tokens for x in xs):
+            raise ValueError(f"more than max_tokens={self.max_tokens} tokens")
+        w = self._matrices(u, self.forward_unit(u, stream=stream))
+        for r, (x, y) in ranks:
+            if keep:
+                self.tokens[u][r] = x.shape[0]
+            zero_ffn_forward(x, *w, y, self.workspace, activation=self.activation,
+                             checkpoint=self.checkpoints[u][r].first(x.shape[0]) if keep else None, stream=stream)
+        return ys
+
+    def contribute(self, u: int, dys: Sequence[torch.Tensor], dxs: Sequence[Optional[torch.Tensor]], stream=None):
+        """Every rank's gradients of layer u into `grads`, the unit's padding zero, and dxs[r]
+        (None: not wanted)."""
+        ranks = self._per_rank(dys, dxs)
+        if any(dy.shape[0] != t for dy, t in zip(dys, self.tokens[u])):
+            raise ValueError(f"layer {u}: the gradients are of other tokens than the kept forward pass")
+        psi, pad = self.units[u][1:3]
+        w = self._matrices(u, self.forward_unit(u, stream=stream))
+        for r, (dy, dx) in ranks:
+            if pad > psi:
+                with _allocating_on(stream):   # on that stream
+                    self.grads[r][psi:pad].zero_()
+            zero_ffn_backward(dy, self.checkpoints[u][r].first(dy.shape[0]), *w, dx, *self._matrices(u, self.grads[r]),
+                              self.workspace, activation=self.activation, stream=stream)
+
+    def backward_layer(self, u: int, dys, dxs, weights, hp, stream=None):
+        """Layer u's backward pass on every rank, the reduction of its contributions and the
+        owners' updates."""
+        self.contribute(u, dys, dxs, stream=stream)
+        self.backward_unit(u, weights, hp, stream=stream)
 
 
 class OffloadStep:
