@@ -487,6 +487,8 @@ def zero_muon_shard_step(master: torch.Tensor, bf16_out: torch.Tensor, update: t
 ACT8_FORMATS = {"int8": _lib.ZERO_ACT8_INT8, "e4m3": _lib.ZERO_ACT8_E4M3}
 FFN_ACTIVATIONS = {"silu": _lib.ZERO_FFN_SILU, "gelu": _lib.ZERO_FFN_GELU, "relu": _lib.ZERO_FFN_RELU}
 _UINT8 = (torch.uint8,)
+_BF16 = (torch.bfloat16,)
+_ACT8_DTYPES = {torch.bfloat16: _lib.ZERO_BF16, torch.float32: _lib.ZERO_FP32}
 
 
 def _choice(table: Mapping[str, int], name, what: str) -> int:
@@ -499,21 +501,26 @@ def _rows(t: torch.Tensor, what: str, dtypes):
     """(pointer, rows, cols, row stride) of a matrix whose rows are contiguous."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise TypeError(f"{what}: expected a 2-D torch.Tensor")
-    _on_device(t, what, dtypes)
+    if not (t.is_cuda and t.get_device() == _current_device() and t.dtype in dtypes):
+        _on_device(t, what, dtypes)
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    row, col = t.stride()
+    if cols > 1 and col != 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
-    return t.data_ptr(), rows, cols, t.stride(0) if rows > 1 else cols
+    return t.data_ptr(), rows, cols, row if rows > 1 else cols
 
 
-def _act8(rows: int, cols: int, codes: torch.Tensor, scales: torch.Tensor, what: str = "") -> list:
-    """The pointers of a checkpoint of rows x cols values."""
+def _whole(device: int, dtypes, *matrices) -> list:
+    """The pointers of contiguous (tensor, name, rows, cols), without a call for each
+    that passes: a pass of the feed-forward block has up to sixteen."""
     ptrs = []
-    for t, name, width in ((codes, "codes", cols), (scales, "scales", -(-cols // _lib.ZERO_ACT8_BLOCK))):
-        ptr = _dev(t, what + name, _UINT8)
-        if tuple(t.shape) != (rows, width):
-            raise ValueError(f"{what}{name}: shape {tuple(t.shape)}, expected {(rows, width)}")
-        ptrs.append(ptr)
+    for t, what, rows, cols in matrices:
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == device and t.dtype in dtypes
+                and t.is_contiguous()):
+            _dev(t, what, dtypes)
+        if t.shape != (rows, cols):
+            raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {(rows, cols)}")
+        ptrs.append(t.data_ptr())
     return ptrs
 
 
@@ -527,20 +534,19 @@ def zero_act8_save(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, f
                    stream=None) -> None:
     """x (BF16 or FP32, [rows, cols], row stride free) as 8 bits a value and a power
     of two per 32 neighbours of a row; format "int8" or "e4m3"."""
-    xp, rows, cols, row = _rows(x, "x", (torch.bfloat16, torch.float32))
-    cp, sp = _act8(rows, cols, codes, scales)
-    check(load().zero_act8_save(xp, _lib.ZERO_FP32 if x.dtype == torch.float32 else _lib.ZERO_BF16, row, rows, cols,
-                                _choice(ACT8_FORMATS, format, "format"), cp, sp, _stream(stream)), "zero_act8_save")
+    xp, rows, cols, row = _rows(x, "x", _ACT8_DTYPES)
+    cp, sp = _whole(_current_device(), _UINT8, (codes, "codes", rows, cols), (scales, "scales", rows, (cols + 31) // 32))
+    check(load().zero_act8_save(xp, _ACT8_DTYPES[x.dtype], row, rows, cols, _choice(ACT8_FORMATS, format, "format"), cp,
+                                sp, _stream(stream)), "zero_act8_save")
 
 
 def zero_act8_load(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, format: str = "int8",
                    stream=None) -> None:
     """out (BF16 or FP32, [rows, cols], row stride free) = the checkpoint's values."""
-    op, rows, cols, row = _rows(out, "out", (torch.bfloat16, torch.float32))
-    cp, sp = _act8(rows, cols, codes, scales)
+    op, rows, cols, row = _rows(out, "out", _ACT8_DTYPES)
+    cp, sp = _whole(_current_device(), _UINT8, (codes, "codes", rows, cols), (scales, "scales", rows, (cols + 31) // 32))
     check(load().zero_act8_load(cp, sp, rows, cols, _choice(ACT8_FORMATS, format, "format"), op,
-                                _lib.ZERO_FP32 if out.dtype == torch.float32 else _lib.ZERO_BF16, row,
-                                _stream(stream)), "zero_act8_load")
+                                _ACT8_DTYPES[out.dtype], row, _stream(stream)), "zero_act8_load")
 
 
 class FfnCheckpoint:
@@ -562,10 +568,13 @@ class FfnCheckpoint:
         return FfnCheckpoint(*([t[:tokens] for t in held] for held in (self.x, self.gate, self.up)), self.format)
 
     def buffers(self, tokens: int, model: int, hidden: int) -> _lib.FfnCheckpointBuffers:
-        ptrs = [p for held, cols, what in ((self.x, model, "checkpoint.x "), (self.gate, hidden, "checkpoint.gate "),
-                                           (self.up, hidden, "checkpoint.up "))
-                for p in _act8(tokens, cols, *held, what)]
-        return _lib.FfnCheckpointBuffers(*ptrs, ACT8_FORMATS[self.format])
+        (xc, xs), (gc, gs), (uc, us) = self.x, self.gate, self.up
+        mb, hb = (model + 31) // 32, (hidden + 31) // 32
+        return _lib.FfnCheckpointBuffers(*_whole(
+            _current_device(), _UINT8, (xc, "checkpoint.x codes", tokens, model), (xs, "checkpoint.x scales", tokens, mb),
+            (gc, "checkpoint.gate codes", tokens, hidden), (gs, "checkpoint.gate scales", tokens, hb),
+            (uc, "checkpoint.up codes", tokens, hidden), (us, "checkpoint.up scales", tokens, hb)),
+            ACT8_FORMATS[self.format])
 
 
 def zero_ffn_workspace(tokens: int, model: int, hidden: int, backward: bool = False, unaligned: bool = False,
@@ -578,16 +587,10 @@ def zero_ffn_workspace(tokens: int, model: int, hidden: int, backward: bool = Fa
     return torch.empty(n.value, dtype=torch.uint8, device=device)
 
 
-def _ffn_weights(model: int, names, *ts):
-    """(pointers, hidden) of matrices [hidden, model], [hidden, model], [model, hidden]."""
-    ptrs = [_dev(t, name, (torch.bfloat16,)) for t, name in zip(ts, names)]
-    if ts[0].dim() != 2:
-        raise ValueError(f"{names[0]}: expected a 2-D tensor")
-    hidden = ts[0].shape[0]
-    for t, name, shape in zip(ts, names, ((hidden, model), (hidden, model), (model, hidden))):
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    return ptrs, hidden
+def _hidden(w_gate: torch.Tensor) -> int:
+    if not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 2:
+        raise TypeError("w_gate: expected a 2-D torch.Tensor")
+    return w_gate.shape[0]
 
 
 def zero_ffn_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor, y: torch.Tensor,
@@ -596,11 +599,13 @@ def zero_ffn_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, 
     """y = (act(x Wg^T) * (x Wu^T)) Wd^T, all BF16; x, y [tokens, model] with free row
     strides, w_gate and w_up [hidden, model], w_down [model, hidden].  activation: "silu", "gelu"
     (tanh) or "relu".  checkpoint: written, for zero_ffn_backward."""
-    xp, tokens, model, xrow = _rows(x, "x", (torch.bfloat16,))
-    yp, *yshape, yrow = _rows(y, "y", (torch.bfloat16,))
-    if yshape != [tokens, model]:
+    xp, tokens, model, xrow = _rows(x, "x", _BF16)
+    yp, yrows, ycols, yrow = _rows(y, "y", _BF16)
+    if yrows != tokens or ycols != model:
         raise ValueError("zero_ffn_forward: y must have x's shape")
-    w, hidden = _ffn_weights(model, ("w_gate", "w_up", "w_down"), w_gate, w_up, w_down)
+    hidden = _hidden(w_gate)
+    w = _whole(_current_device(), _BF16, (w_gate, "w_gate", hidden, model), (w_up, "w_up", hidden, model),
+               (w_down, "w_down", model, hidden))
     held = None if checkpoint is None else C.byref(checkpoint.buffers(tokens, model, hidden))
     check(load().zero_ffn_forward(xp, xrow, tokens, model, hidden, *w, _choice(FFN_ACTIVATIONS, activation, "activation"),
                                   yp, yrow, held, _dev(workspace, "workspace", _UINT8), workspace.numel(),
@@ -612,18 +617,19 @@ def zero_ffn_backward(dy: torch.Tensor, checkpoint: FfnCheckpoint, w_gate: torch
                       d_down: torch.Tensor, workspace: torch.Tensor, activation: str = "silu", stream=None) -> None:
     """Gradients of zero_ffn_forward from its checkpoint: dx [tokens, model] (None: not
     wanted) and d_gate, d_up, d_down of the weights' shapes, all BF16, written."""
-    dyp, tokens, model, dyrow = _rows(dy, "dy", (torch.bfloat16,))
+    dyp, tokens, model, dyrow = _rows(dy, "dy", _BF16)
     dxp, dxrow = None, model
     if dx is not None:
-        dxp, *shape, dxrow = _rows(dx, "dx", (torch.bfloat16,))
-        if shape != [tokens, model]:
+        dxp, dxrows, dxcols, dxrow = _rows(dx, "dx", _BF16)
+        if dxrows != tokens or dxcols != model:
             raise ValueError("zero_ffn_backward: dx must have dy's shape")
-    w, hidden = _ffn_weights(model, ("w_gate", "w_up", "w_down"), w_gate, w_up, w_down)
-    d, dhidden = _ffn_weights(model, ("d_gate", "d_up", "d_down"), d_gate, d_up, d_down)
-    if dhidden != hidden:
-        raise ValueError("zero_ffn_backward: the gradients must have the weights' shapes")
+    hidden = _hidden(w_gate)
+    wg, wu, wd, *d = _whole(
+        _current_device(), _BF16, (w_gate, "w_gate", hidden, model), (w_up, "w_up", hidden, model),
+        (w_down, "w_down", model, hidden), (d_gate, "d_gate", hidden, model), (d_up, "d_up", hidden, model),
+        (d_down, "d_down", model, hidden))
     held = checkpoint.buffers(tokens, model, hidden)
-    check(load().zero_ffn_backward(dyp, dyrow, tokens, model, hidden, C.byref(held), *w,
+    check(load().zero_ffn_backward(dyp, dyrow, tokens, model, hidden, C.byref(held), wg, wu, wd,
                                    _choice(FFN_ACTIVATIONS, activation, "activation"), dxp, dxrow, *d,
                                    _dev(workspace, "workspace", _UINT8), workspace.numel(), _stream(stream)),
           "zero_ffn_backward")
