@@ -236,6 +236,7 @@ struct Product {
 struct Products {
   Product of[3];
   int first[3];            // tile number of each; those past the last have 0x7FFFFFFF
+  int begin, quarters;     // the first tile of the launch; whether its workgroups take quarters of tiles
   // kGated and kSlopes
   Act8Rows gate, up;
   uint16_t* du;            // kSlopes: out is dg, both with out_ld
@@ -361,19 +362,27 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
   int id = xcd_order(blockIdx.x, gridDim.x);
   const int split = EPI == kPartial ? id % args.splits : 0;
   if constexpr (EPI == kPartial) id /= args.splits;
+  // One of the four quarters of a larger tile, or a tile.
+  const int quarter = args.quarters ? id & 3 : 0;
+  id = args.begin + (args.quarters ? id >> 2 : id);
   const int which = id >= args.first[2] ? 2 : id >= args.first[1] ? 1 : 0;
   const Product& g = args.of[which];
   const int t = id - args.first[which];
   // Groups of kGroup tiles of q: an XCD's 32 workgroups share their operands' rows.
   const int group = t / (kGroup * g.tiles_p), in = t - group * kGroup * g.tiles_p;
   const int left = g.tiles_q - group * kGroup, height = left < kGroup ? left : kGroup;
-  const int tp = in / height, tq = group * kGroup + in - tp * height;
+  int tp = in / height, tq = group * kGroup + in - tp * height;
+  if (args.quarters) {
+    tp = 2 * tp + (quarter & 1);
+    tq = 2 * tq + (quarter >> 1);
+  }
   const int wp = wave / WQ, wq = wave - wp * WQ;
 
   const int k_first = EPI == kPartial ? split * args.chunk : 0;
   const int kk = EPI == kPartial && g.kk - k_first > args.chunk ? args.chunk : g.kk - k_first;
   constexpr int kOwn = EPI == kGated ? BP / 2 : BP;   // values along p of a tile
   const int p0 = tp * kOwn, q0 = tq * BQ;
+  if (p0 >= g.out_cols || q0 >= g.nq) return;   // a quarter past the edge
   using PStager = std::conditional_t<PCOL, ColumnStager<BP, NW>, RowStager<BP, NW>>;
   using QStager = std::conditional_t<QCOL, ColumnStager<BQ, NW>, RowStager<BQ, NW>>;
   auto p_stager = [&] {
@@ -971,23 +980,49 @@ struct Packing {
   }
 };
 
-template <int BP, int BQ, int WP, int WQ, int SLOTS, bool PCOL, bool QCOL, Epilogue EPI, int ACT = 0>
-hipError_t tiles(Products a, int n, hipStream_t s) {
+// Tiles of bp x bq: numbers a's products' and says how many there are.
+template <Epilogue EPI>
+int64_t number_tiles(Products& a, int n, int bp, int bq) {
   int64_t total = 0;
   for (int k = 0; k < 3; ++k) {
     a.first[k] = k < n ? static_cast<int>(total) : 0x7FFFFFFF;
     if (k >= n) continue;
     Product& g = a.of[k];
-    const int own = EPI == kGated ? BP / 2 : BP;
+    const int own = EPI == kGated ? bp / 2 : bp;
     const int columns = g.out_cols > g.np ? g.out_cols : g.np;
     g.tiles_p = (columns + own - 1) / own;
-    g.tiles_q = (g.nq + BQ - 1) / BQ;
+    g.tiles_q = (g.nq + bq - 1) / bq;
     total += static_cast<int64_t>(g.tiles_p) * g.tiles_q;
   }
-  if (EPI == kPartial) total *= a.splits;
-  hipLaunchKernelGGL((ffn_product_kernel<BP, BQ, WP, WQ, SLOTS, PCOL, QCOL, EPI, ACT>), dim3(static_cast<unsigned>(total)), dim3(WP * WQ * 64),
-                     0, s, a);
+  return total;
+}
+
+// `count` workgroups, from a.begin on.
+template <int BP, int BQ, int WP, int WQ, int SLOTS, bool PCOL, bool QCOL, Epilogue EPI, int ACT = 0>
+hipError_t launch_tiles(const Products& a, int64_t count, hipStream_t s) {
+  hipLaunchKernelGGL((ffn_product_kernel<BP, BQ, WP, WQ, SLOTS, PCOL, QCOL, EPI, ACT>), dim3(static_cast<unsigned>(count)),
+                     dim3(WP * WQ * 64), 0, s, a);
   return hipGetLastError();
+}
+
+template <int BP, int BQ, int WP, int WQ, int SLOTS, bool PCOL, bool QCOL, Epilogue EPI, int ACT = 0>
+hipError_t tiles(Products a, int n, hipStream_t s) {
+  const int64_t total = number_tiles<EPI>(a, n, BP, BQ);
+  return launch_tiles<BP, BQ, WP, WQ, SLOTS, PCOL, QCOL, EPI, ACT>(a, EPI == kPartial ? total * a.splits : total, s);
+}
+
+// Tiles of 256 x 256, one per CU at a time.  What is left over after whole rounds is done in quarters,
+// two per CU, where that is half a round at most.
+template <bool PCOL, bool QCOL, Epilogue EPI, int ACT>
+hipError_t large_tiles(Products a, int n, hipStream_t s) {
+  constexpr int64_t kCus = 256;
+  const int64_t total = number_tiles<EPI>(a, n, 256, 256), over = total % kCus;
+  const bool split = over > 0 && over <= kCus / 2;
+  const hipError_t e = launch_tiles<256, 256, 2, 4, 2, PCOL, QCOL, EPI, ACT>(a, split ? total - over : total, s);
+  if (e != hipSuccess || !split) return e;
+  a.begin = static_cast<int>(total - over);
+  a.quarters = 1;
+  return launch_tiles<128, 128, 2, 2, 2, PCOL, QCOL, EPI, ACT>(a, over * 4, s);
 }
 
 // Gate and up: up to 32 rows of each by 8 waves (over 16 tokens by 4: more registers each);
@@ -1056,7 +1091,7 @@ hipError_t product(const Products& a, int n, hipStream_t s) {
     for (int k = 0; k < n; ++k) t += (a.of[k].np + own - 1) / own * ((a.of[k].nq + bq - 1) / bq);
     return t;
   };
-  if (count(256, 256) >= 256) return tiles<256, 256, 2, 4, 2, PCOL, QCOL, EPI, ACT>(a, n, s);
+  if (count(256, 256) >= 256) return large_tiles<PCOL, QCOL, EPI, ACT>(a, n, s);
   if constexpr (EPI == kGated || EPI == kSlopes) {
     if (count(128, 64) <= 256 || a.of[0].nq <= 64) return tiles<128, 64, 2, 2, 4, PCOL, QCOL, EPI, ACT>(a, n, s);
   }
