@@ -58,6 +58,19 @@ def test_workspace_sizes(libzero):
         assert st == 0 and n >= t * (3 * 832 + 2 * 1344) * 2 and n % 256 == 0
 
 
+@pytest.mark.parametrize("m,h", [(64, 96), (777, 1301), (1024, 8192), (4096, 14336), (8, 28672)])
+@pytest.mark.parametrize("most", [1, 33, 130, 1021])
+def test_the_drivers_workspace_serves_every_count_of_tokens(libzero, m, h, most):
+    from types import SimpleNamespace
+
+    from zero_sharded_optimizer_reduce_amd.drivers import Zero3FeedForward
+
+    room = Zero3FeedForward._workspace_bytes(SimpleNamespace(max_tokens=most), m, h)
+    flags = 2 if m * h % 8 else 0
+    needs = [_workspace(libzero, t, m, h, flags | back) for t in range(most + 1) for back in (0, 1)]
+    assert all(st == 0 for st, _ in needs) and max(n for _, n in needs) == room
+
+
 def test_the_c_abi_refuses(libzero):
     L = libzero
     act = lambda **k: L.zero_act8_save(*[{**dict(x=1 << 40, dtype=0, row=64, rows=4, cols=64, fmt=0, codes=1 << 41, scales=1 << 42,

@@ -1017,7 +1017,7 @@ template <bool PCOL, bool QCOL, Epilogue EPI, int ACT>
 hipError_t large_tiles(Products a, int n, hipStream_t s) {
   constexpr int64_t kCus = 256;
   const int64_t total = number_tiles<EPI>(a, n, 256, 256), over = total % kCus;
-  const bool split = over > 0 && over <= kCus / 2;
+  const bool split = total > kCus && over > 0 && over <= kCus / 2;
   const hipError_t e = launch_tiles<256, 256, 2, 4, 2, PCOL, QCOL, EPI, ACT>(a, split ? total - over : total, s);
   if (e != hipSuccess || !split) return e;
   a.begin = static_cast<int>(total - over);
@@ -1045,26 +1045,52 @@ hipError_t few(Products a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// How y's and dx's sums (nq rows of np values) are shared out: two workgroups for every CU, as
-// long as each has 512 of the summed index.  256 tokens through 4096 x 14336 have 64 tiles
-// of 128 x 128 for y.
+// Modelled times in us of n tiles whose sums have so many stages, fitted to launches with operands of
+// 1024 to 4096 x 2816 to 28672, from memory and from caches: up to 256 tiles have a CU each (four stages
+// of 128 x 64 on their way, with columns a little less work), up to 512 of 128 x 128 two on each.
+double time256(double stages, int64_t n) { return 8.0 + stages * (1.1 + 0.35 * static_cast<double>(n) / 256); }
+double time128(double stages, int64_t n) { return 3.0 + stages * (n <= 256 ? 0.64 : n <= 512 ? 1.1 : 1.25 * static_cast<double>(n) / 512); }
+double time64(double stages, bool columns) { return 3.2 + stages * (columns ? 0.36 : 0.42); }
+
+// How y's and dx's sums (nq rows of np values) are shared out.  Measured, 4096 x 14336 from memory, in
+// parts and in the best whole tiles: 64 rows 34 and 128 us, 256 54 and 123, 512 77 and 121, 1024 (four
+// parts of tiles of 256) 108 and 161, 2048 (two) 178 and 231; kk = 2816, 256 rows 18 and 19,
+// 1024 36 and 27 (whole).
 struct Parts {
   int splits, chunk;
+  bool large;   // tiles of 256 x 256
   int64_t pitch, bytes;
 };
-Parts parts_of(int64_t np, int64_t nq, int64_t kk) {
-  constexpr int64_t kRoom = 512, kLeast = 512, kMost = 16;
-  Parts x = {1, 0, (np + 7) / 8 * 8, 0};
-  const int64_t n = (np + 127) / 128 * ((nq + 127) / 128);
-  if (n == 0 || n > kRoom / 2) return x;
-  int64_t splits = kRoom / n;
-  if (splits > kk / kLeast) splits = kk / kLeast;
-  if (splits > kMost) splits = kMost;
-  if (splits < 2) return x;
-  const int64_t chunk = ((kk + splits - 1) / splits + 2 * kBk - 1) / (2 * kBk) * (2 * kBk);
-  x.splits = static_cast<int>((kk + chunk - 1) / chunk);
-  x.chunk = static_cast<int>(chunk);
-  x.bytes = x.splits * nq * x.pitch * 4;
+Parts parts_of(int64_t np, int64_t nq, int64_t kk, bool columns) {
+  Parts x = {1, 0, false, (np + 7) / 8 * 8, 0};
+  auto tiles_of = [&](int64_t bp, int64_t bq) { return (np + bp - 1) / bp * ((nq + bq - 1) / bq); };
+  const int64_t n256 = tiles_of(256, 256), n128 = tiles_of(128, 128), n64 = tiles_of(128, 64);
+  if (n128 == 0 || n256 >= 256) return x;
+  const double stages = static_cast<double>((kk + kBk - 1) / kBk);
+  double best = time128(stages, n128);
+  if (n64 <= 256 && time64(stages, columns) < best) best = time64(stages, columns);
+  if (time256(stages, n256) < best) best = time256(stages, n256);
+  for (int64_t splits = 2; splits <= 16; ++splits) {
+    const int64_t chunk = ((kk + splits - 1) / splits + 2 * kBk - 1) / (2 * kBk) * (2 * kBk);
+    const int64_t parts = (kk + chunk - 1) / chunk;
+    if (parts < 2) continue;
+    // written, and read by the second launch; the choice looks at whole 64 rows, so that the room that
+    // it needs grows within them
+    const int64_t bytes = parts * nq * x.pitch * 4, moved = 2 * (parts * ((nq + 63) / 64 * 64) * x.pitch * 4);
+    const double st = static_cast<double>(chunk / kBk), join = 4.5 + static_cast<double>(moved) / 5e6;
+    for (int large = 0; large < 2; ++large) {
+      const int64_t n = (large ? n256 : n128) * parts;
+      if (n > (large ? 256 : 512)) continue;
+      const double time = join + (large ? time256(st, n) : time128(st, n));
+      if (time < best) {
+        best = time;
+        x.splits = static_cast<int>(parts);
+        x.chunk = static_cast<int>(chunk);
+        x.large = large;
+        x.bytes = bytes;
+      }
+    }
+  }
   return x;
 }
 
@@ -1075,7 +1101,8 @@ hipError_t product_in_parts(Products a, const Parts& parts, void* room, hipStrea
   a.pitch = parts.pitch;
   a.partial = static_cast<float*>(room);
   const Product& g = a.of[0];
-  const hipError_t e = tiles<128, 128, 2, 2, 2, PCOL, false, kPartial>(a, 1, s);
+  const hipError_t e = parts.large ? tiles<256, 256, 2, 4, 2, PCOL, false, kPartial>(a, 1, s)
+                                   : tiles<128, 128, 2, 2, 2, PCOL, false, kPartial>(a, 1, s);
   if (e != hipSuccess) return e;
   const JoinArgs j = {a.partial, a.pitch, a.splits, g.nq, g.np, g.out, g.out_ld};
   const int64_t n = g.nq * (a.pitch / 8);
@@ -1091,10 +1118,15 @@ hipError_t product(const Products& a, int n, hipStream_t s) {
     for (int k = 0; k < n; ++k) t += (a.of[k].np + own - 1) / own * ((a.of[k].nq + bq - 1) / bq);
     return t;
   };
-  if (count(256, 256) >= 256) return large_tiles<PCOL, QCOL, EPI, ACT>(a, n, s);
-  if constexpr (EPI == kGated || EPI == kSlopes) {
-    if (count(128, 64) <= 256 || a.of[0].nq <= 64) return tiles<128, 64, 2, 2, 4, PCOL, QCOL, EPI, ACT>(a, n, s);
+  // 256 x 256 where they fill the card or their longer stages take less time than the rounds of 128 x 128
+  // (512 rows of 28672 values: 4096 a sum 97 and 142 us; 8192 values, 1024 a sum 24 and 13).
+  const int64_t n256 = count(256, 256), n128 = count(128, 128);
+  const double stages = (a.of[0].kk + kBk - 1) / kBk;
+  if constexpr (!QCOL) {   // (columns of 64 would need another order in LDS)
+    if (n256 < 256 && (count(128, 64) <= 256 || a.of[0].nq <= 64) && time64(stages, PCOL) < time256(stages, n256))
+      return tiles<128, 64, 2, 2, 4, PCOL, QCOL, EPI, ACT>(a, n, s);
   }
+  if (n256 >= 256 || time256(stages, n256) < time128(stages, n128)) return large_tiles<PCOL, QCOL, EPI, ACT>(a, n, s);
   return tiles<128, 128, 2, 2, 2, PCOL, QCOL, EPI, ACT>(a, n, s);
 }
 
@@ -1126,7 +1158,7 @@ int64_t ffn_workspace_bytes(int64_t tokens, int64_t model, int64_t hidden, bool 
     n += bytes(tokens * 2 * fp) + bytes(tokens * fp) + bytes(tokens * dp);
   else
     n += bytes(tokens * fp);
-  n += bytes(parts_of(model, tokens, backward ? 2 * fp : fp).bytes / 2);
+  n += bytes(parts_of(model, tokens, backward ? 2 * fp : fp, backward).bytes / 2);
   if (unaligned || model % kPad || hidden % kPad) n += 2 * bytes(hidden * dp) + bytes(model * fp);
   return n;
 }
@@ -1140,7 +1172,7 @@ hipError_t launch_ffn_forward(const FfnParams& p, hipStream_t s) {
   Carver ws = {static_cast<char*>(p.workspace)};
   uint16_t* h = ws.take(t * fp);
   const bool is_few = t <= kFewTokens;
-  const Parts parts = is_few ? Parts{1, 0, 0, 0} : parts_of(d, t, fp);
+  const Parts parts = is_few ? Parts{1, 0, false, 0, 0} : parts_of(d, t, fp, false);
   uint16_t* parts_room = ws.take(parts.bytes / 2);
   uint16_t* x_room = is_few ? nullptr : ws.take(t * dp);
   Matrix x = {p.x, p.x_row}, gate = {p.w_gate, d}, up = {p.w_up, d}, down = {p.w_down, f};
@@ -1200,7 +1232,7 @@ hipError_t launch_ffn_backward(const FfnParams& p, hipStream_t s) {
   uint16_t* h = ws.take(t * fp);
   uint16_t* x = ws.take(t * dp);
   uint16_t* dy_room = ws.take(t * dp);
-  const Parts parts = parts_of(d, t, 2 * fp);
+  const Parts parts = parts_of(d, t, 2 * fp, true);
   uint16_t* parts_room = ws.take(parts.bytes / 2);
   Matrix dy = {p.x, p.x_row}, gate = {p.w_gate, d}, up = {p.w_up, d}, down = {p.w_down, f};
   int dy_cols = static_cast<int>(d), w_cols = static_cast<int>(d), down_cols = static_cast<int>(f);
