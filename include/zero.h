@@ -520,7 +520,8 @@ int zero_ffn_workspace(int64_t tokens, int64_t model, int64_t hidden, int flags,
  *                 slices of the gathered view of a layer.
  *   save          host, or NULL: the checkpoint's buffers, written.
  *   workspace     device, 256-byte aligned, workspace_bytes >= zero_ffn_workspace's
- *                 answer; nothing in it carries over between calls.
+ *                 answer; nothing in it carries over between calls.  Calls that may
+ *                 run at the same time (streams, captured graphs) need one each.
  * Arithmetic: products of BF16 values summed in FP32 on the matrix cores; act in
  * FP32; g and u go into the checkpoint as summed, h is rounded to BF16 (the type the
  * second product takes), y is rounded to BF16.  Results are the same bits on every

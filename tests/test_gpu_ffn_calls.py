@@ -369,3 +369,23 @@ def test_driver_refusals():
     st.contribute(0, xs, [None, None])
     with pytest.raises(ValueError, match="activation"):
         Zero3FeedForward([(64, 96)], 2, 20, activation="tanh")
+
+
+def test_driver_needs_a_whole_forward_pass_for_each_backward_pass():
+    st = _driver([(64, 96)], 2, (20, 20))
+    xs = [torch.ones(20, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    ys = [torch.empty_like(x) for x in xs]
+    w = z.zero_rank_weights([20, 20], 2)
+    st.forward_layer(0, xs, ys)
+    st.backward_layer(0, xs, [None, None], w, HP)
+    before = _state(st)
+    with pytest.raises(ValueError, match="other tokens"):   # of the weights before the update
+        st.backward_layer(0, xs, [None, None], w, HP)
+    assert _same(before, _state(st))
+    st.forward_layer(0, xs, ys)
+    with pytest.raises(ValueError, match="x's shape"):
+        st.forward_layer(0, xs, [ys[0], ys[1][:19]])
+    with pytest.raises(ValueError, match="other tokens"):   # rank 0's is of another pass than rank 1's
+        st.backward_layer(0, xs, [None, None], w, HP)
+    st.forward_layer(0, xs, ys)
+    st.backward_layer(0, xs, [None, None], w, HP)

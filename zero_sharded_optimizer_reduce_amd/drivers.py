@@ -416,12 +416,14 @@ class Zero3FeedForward(Zero3Chain):
         ranks = self._per_rank(xs, ys)
         if any(x.shape[0] > self.max_tokens for x in xs):
             raise ValueError(f"more than max_tokens={self.max_tokens} tokens")
+        if keep:
+            self.tokens[u] = [None] * self.n   # until every rank's is kept
         w = self._matrices(u, self.forward_unit(u, stream=stream))
         for r, (x, y) in ranks:
-            if keep:
-                self.tokens[u][r] = x.shape[0]
             zero_ffn_forward(x, *w, y, self.workspace, activation=self.activation,
                              checkpoint=self.checkpoints[u][r].first(x.shape[0]) if keep else None, stream=stream)
+        if keep:
+            self.tokens[u] = [x.shape[0] for x in xs]
         return ys
 
     def contribute(self, u: int, dys: Sequence[torch.Tensor], dxs: Sequence[Optional[torch.Tensor]], stream=None):
@@ -441,9 +443,11 @@ class Zero3FeedForward(Zero3Chain):
 
     def backward_layer(self, u: int, dys, dxs, weights, hp, stream=None):
         """Layer u's backward pass on every rank, the reduction of its contributions and the
-        owners' updates."""
+        owners' updates.  The kept forward pass is of the weights before these: another
+        backward pass needs another forward pass."""
         self.contribute(u, dys, dxs, stream=stream)
         self.backward_unit(u, weights, hp, stream=stream)
+        self.tokens[u] = [None] * self.n
 
 
 class OffloadStep:
