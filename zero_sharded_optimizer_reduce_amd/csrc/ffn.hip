@@ -245,6 +245,7 @@ struct Products {
   int blocks;              // scales of a row
   int format, act, save;
   int rows;                // of a workgroup, with a few tokens
+  int spread;              // rows: whether each tile of P begins at another stage
   int splits, chunk;       // kPartial: parts of the summed index and their length, a multiple of 2 kBk
   float* partial;          // kPartial: [splits][nq][pitch]
   int64_t pitch;
@@ -425,7 +426,10 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
   const uint16_t* q_at = g.q + q0;
   const int p_rows = g.p_end, p_ld = static_cast<int>(g.p_ld), q_ld = static_cast<int>(g.q_ld);
   const int p_width = g.p_cols - p0, q_width = g.q_cols - q0;
-  int p_left = p_rows - p_first, q_left = g.q_end, p_turn = past_turn ? -kBk : g.turn - k_first, p_k = -kBk, q_k = -kBk, p_byte = 0, q_byte = 0, p_end = 0, q_end = 0;
+  int p_left = p_rows - p_first, q_left = g.q_end, p_turn = past_turn ? -kBk : g.turn - k_first, p_byte = 0, q_byte = 0, p_end = 0, q_end = 0;
+  // Rows: stages still to load (kk is whole stages), and where the next begins.
+  const int stages = QCOL ? 0 : kk / kBk;
+  int p_n = stages, q_n = stages, p_k = !PCOL && args.spread ? tp % stages * kBk : 0, q_k = p_k;
   __amdgpu_buffer_rsrc_t p_from, q_from;
   auto next_p = [&] {
     if constexpr (PCOL) {
@@ -437,9 +441,10 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
       p_left -= kBk;
       p_turn -= kBk;
     } else {
-      p_k += kBk;
-      p_end = p_k < kk ? sp.bytes : 0;
+      p_end = p_n > 0 ? sp.bytes : 0;
       p_byte = p_end ? p_k * 2 : 0;
+      --p_n;
+      p_k = p_k + kBk < kk ? p_k + kBk : 0;
     }
   };
   auto next_q = [&] {
@@ -448,9 +453,10 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
       q_at += kBk * static_cast<int64_t>(q_ld);
       q_left -= kBk;
     } else {
-      q_k += kBk;
-      q_end = q_k < kk ? sq.bytes : 0;
+      q_end = q_n > 0 ? sq.bytes : 0;
       q_byte = q_end ? q_k * 2 : 0;
+      --q_n;
+      q_k = q_k + kBk < kk ? q_k + kBk : 0;
     }
   };
   auto load_p = [&](uint16_t* lds, int i) {
@@ -491,9 +497,9 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
   // steps before the end: a barrier at each, and from there on the loads of the stage
   // SLOTS on into the free slot, a few per step (a wave issues in order: loads in a row
   // hold its products up).  With two slots each load has between half a stage and a whole one to
-  // arrive.  Tiles of 128 x 128 gain nothing from four: a CU takes in 55 to 95 bytes/ns, and a
-  // stage of 32 KiB takes the 0.46 us that says.  Few tiles of 128 x 64, alone on their CU, do:
-  // dh's product of 1001 x 1301 x 777 takes 12.7 us with four, 16.5 with two.
+  // arrive.  Tiles of 128 x 128, two on a CU, gain nothing from four: a CU takes in 55 to 95
+  // bytes/ns, and a stage of 32 KiB takes the 0.46 us that says.  Few tiles of 128 x 64, alone on their
+  // CU, do: dh's product of 1001 x 1301 x 777 takes 12.7 us with four, 16.5 with two.
   constexpr int kSteps = 2 * TP, kQSpan = TP - 2, kPSpan = TP;   // steps with loads
   static_assert(kSteps % 4 == 0, "a stage starts with the first place");
   f4 acc[TP][TQ] = {};
@@ -1103,6 +1109,18 @@ Parts parts_of(int64_t np, int64_t nq, int64_t kk, bool columns) {
   return x;
 }
 
+// 128 x 128, n workgroups.  With a CU each they keep four stages of rows on their way: gate and up of
+// 4096 x 14336 from memory for 128 tokens 55 us instead of 61, of 2048 x 8192 26 instead of 29; y
+// of 64 tokens in eight parts 31 instead of 34.  Columns gain nothing on average (dh of 14336 x 4096 35
+// instead of 37, of 4096 x 1024 11 instead of 10).
+template <bool PCOL, bool QCOL, Epilogue EPI, int ACT = 0>
+hipError_t tiles128(const Products& a, int products, int64_t n, hipStream_t s) {
+  if constexpr (!PCOL) {
+    if (n <= 256) return tiles<128, 128, 2, 2, 4, PCOL, QCOL, EPI, ACT>(a, products, s);
+  }
+  return tiles<128, 128, 2, 2, 2, PCOL, QCOL, EPI, ACT>(a, products, s);
+}
+
 template <bool PCOL>
 hipError_t product_in_parts(Products a, const Parts& parts, void* room, hipStream_t s) {
   a.splits = parts.splits;
@@ -1110,12 +1128,13 @@ hipError_t product_in_parts(Products a, const Parts& parts, void* room, hipStrea
   a.pitch = parts.pitch;
   a.partial = static_cast<float*>(room);
   const Product& g = a.of[0];
+  const int64_t n = (g.np + 127) / 128 * ((g.nq + 127) / 128) * static_cast<int64_t>(parts.splits);
   const hipError_t e = parts.large ? tiles<256, 256, 2, 4, 2, PCOL, false, kPartial>(a, 1, s)
-                                   : tiles<128, 128, 2, 2, 2, PCOL, false, kPartial>(a, 1, s);
+                                   : tiles128<PCOL, false, kPartial>(a, 1, n, s);
   if (e != hipSuccess) return e;
   const JoinArgs j = {a.partial, a.pitch, a.splits, g.nq, g.np, g.out, g.out_ld};
-  const int64_t n = g.nq * (a.pitch / 8);
-  hipLaunchKernelGGL(ffn_join_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, j);
+  const int64_t pieces = g.nq * (a.pitch / 8);
+  hipLaunchKernelGGL(ffn_join_kernel, dim3(static_cast<unsigned>((pieces + 255) / 256)), dim3(256), 0, s, j);
   return hipGetLastError();
 }
 
@@ -1136,7 +1155,7 @@ hipError_t product(const Products& a, int n, hipStream_t s) {
       return tiles<128, 64, 2, 2, 4, PCOL, QCOL, EPI, ACT>(a, n, s);
   }
   if (n256 >= 256 || time256(stages, n256) < time128(stages, n128)) return large_tiles<PCOL, QCOL, EPI, ACT>(a, n, s);
-  return tiles<128, 128, 2, 2, 2, PCOL, QCOL, EPI, ACT>(a, n, s);
+  return tiles128<PCOL, QCOL, EPI, ACT>(a, n, n128, s);
 }
 
 // The activation is a constant of the kernel: asked for each value, its code was 250 KB and did not
@@ -1204,6 +1223,10 @@ hipError_t launch_ffn_forward(const FfnParams& p, hipStream_t s) {
   a.format = p.ckpt.format;
   a.act = p.activation;
   a.save = p.save;
+  // Where x stays in an XCD's L2 (4 MiB) the tiles of the weights need not keep in step: they begin at
+  // different columns, which lie in different channels of the memory (4096 x 14336 from memory, 64 tokens:
+  // 51 us in step, 46 spread; 128: 55 and 51; 256: 78 and 77).
+  a.spread = t * d * 2 <= 4 << 20;
   Product& g = a.of[0];
   g.p = gate.at;
   g.p2 = up.at;
