@@ -39,7 +39,8 @@ SHAPES = [(1, 64, 64, 0, 0), (1, 1, 1, 0, 0), (2, 33, 65, 1, 0), (5, 72, 136, 0,
           (31, 70, 250, 3, 1), (33, 256, 320, 0, 8), (64, 192, 128, 0, 1), (65, 192, 128, 0, 0), (127, 320, 448, 4, 0),
           (128, 128, 128, 0, 0), (129, 129, 129, 0, 0), (200, 65, 511, 0, 3), (257, 576, 320, 16, 0), (300, 264, 1032, 0, 0),
           (513, 640, 704, 0, 0), (777, 131, 199, 5, 0), (1025, 256, 2048, 0, 0), (2048, 1024, 1152, 0, 0), (2304, 1024, 2176, 0, 0),
-          (100, 2048, 2816, 0, 0), (8192, 2048, 4160, 0, 0), (8209, 2050, 4163, 3, 1)]
+          (100, 2048, 2816, 0, 0), (8192, 2048, 4160, 0, 0), (8209, 2050, 4163, 3, 1), (200, 2053, 8300, 5, 0), (256, 1088, 9024, 0, 0),
+          (128, 1088, 11000, 0, 0), (64, 512, 8200, 0, 0), (2100, 1024, 200, 0, 0), (1030, 1024, 4100, 0, 1)]
 
 
 @pytest.mark.parametrize("saved", [False, True], ids=["", "saved"])

@@ -1065,6 +1065,8 @@ hipError_t few(Products a, hipStream_t s) {
 // of 128 x 64 on their way, with columns a little less work), up to 512 of 128 x 128 two on each.
 double time256(double stages, int64_t n) { return 8.0 + stages * (1.1 + 0.35 * static_cast<double>(n) / 256); }
 double time128(double stages, int64_t n) { return 3.0 + stages * (n <= 256 ? 0.64 : n <= 512 ? 1.1 : 1.25 * static_cast<double>(n) / 512); }
+// Gate and up of 4096 x 14336, 256 tokens: 67 us in one round, 77 in tiles of 128 x 128, 81 of 256 x 256.
+double time128x256(double stages, int64_t n) { return 5.0 + stages * (0.87 + 0.1 * static_cast<double>(n) / 256); }
 double time64(double stages, bool columns) { return 3.2 + stages * (columns ? 0.36 : 0.42); }
 
 // How y's and dx's sums (nq rows of np values) are shared out.  Measured, 4096 x 14336 from memory, in
@@ -1153,6 +1155,12 @@ hipError_t product(const Products& a, int n, hipStream_t s) {
   if constexpr (!QCOL) {   // (columns of 64 would need another order in LDS)
     if (n256 < 256 && (count(128, 64) <= 256 || a.of[0].nq <= 64) && time64(stages, PCOL) < time256(stages, n256))
       return tiles<128, 64, 2, 2, 4, PCOL, QCOL, EPI, ACT>(a, n, s);
+  }
+  if constexpr (EPI == kGated) {   // 256 tokens of fewer rows, to bring the weights in once
+    const int64_t n = count(128, 256);
+    const double time = time128x256(stages, n);
+    if (n <= 256 && time < time128(stages, n128) && time < time256(stages, n256))
+      return tiles<128, 256, 2, 4, 2, PCOL, QCOL, EPI, ACT>(a, 1, s);
   }
   if (n256 >= 256 || time256(stages, n256) < time128(stages, n128)) return large_tiles<PCOL, QCOL, EPI, ACT>(a, n, s);
   return tiles128<PCOL, QCOL, EPI, ACT>(a, n, n128, s);
