@@ -389,3 +389,49 @@ def test_driver_needs_a_whole_forward_pass_for_each_backward_pass():
         st.backward_layer(0, xs, [None, None], w, HP)
     st.forward_layer(0, xs, ys)
     st.backward_layer(0, xs, [None, None], w, HP)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("tokens,model", [(1, 1), (3, 70), (31, 1301), (40, 33), (300, 1301), (2100, 1000)])
+def test_the_forward_passes_checkpoint_of_x_is_zero_act8_saves(tokens, model, fmt):
+    gen = torch.Generator(device="cuda").manual_seed(tokens)
+    x = torch.randn(tokens, model + 3, generator=gen, device="cuda").to(torch.bfloat16)[:, :model]
+    for k, bad in enumerate((float("nan"), float("inf"), -float("inf"), 3e38, 1e-39, -0.0)):
+        x[(k * 7) % tokens, (k * 37) % model] = bad
+    w = [torch.zeros(s, dtype=torch.bfloat16, device="cuda") for s in ((40, model), (40, model), (model, 40))]
+    ck = z.FfnCheckpoint.empty(tokens, model, 40, fmt)
+    want = z.zero_act8_buffers(tokens, model)
+    for t in (*ck.x, *want):
+        t.fill_(77)
+    z.zero_ffn_forward(x, *w, torch.empty(tokens, model, dtype=torch.bfloat16, device="cuda"),
+                       z.zero_ffn_workspace(tokens, model, 40), checkpoint=ck)
+    z.zero_act8_save(x, *want, format=fmt)
+    assert torch.equal(ck.x[0], want[0]) and torch.equal(ck.x[1], want[1])
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("tokens,model", [(3, 70), (40, 33), (300, 1301), (2100, 1000)])
+def test_the_backward_pass_takes_x_as_zero_act8_load_gives_it(tokens, model, fmt):
+    """dW_gate = dg^T x with dg = 1 in one token alone: x's values themselves."""
+    gen = torch.Generator(device="cuda").manual_seed(model)
+    x = torch.randn(tokens, model, generator=gen, device="cuda").mul_(1e3).to(torch.bfloat16)
+    at, hidden = tokens - 1, 8
+    x[at, model - 1] = float("inf")   # the last block
+    ck = z.FfnCheckpoint.empty(tokens, model, hidden, fmt)
+    z.zero_act8_save(x, *ck.x, format=fmt)
+    ones = torch.ones(tokens, hidden, dtype=torch.bfloat16, device="cuda")
+    z.zero_act8_save(ones, *ck.gate, format=fmt)
+    z.zero_act8_save(ones, *ck.up, format=fmt)
+    dy = torch.zeros(tokens, model, dtype=torch.bfloat16, device="cuda")
+    dy[at, 0] = 1.0
+    w = [torch.zeros(s, dtype=torch.bfloat16, device="cuda") for s in ((hidden, model), (hidden, model), (model, hidden))]
+    w[2][0] = 1.0
+    d = [torch.full_like(v, 5.0) for v in w]
+    z.zero_ffn_backward(dy, ck, *w, None, *d, z.zero_ffn_workspace(tokens, model, hidden, backward=True), activation="relu")
+    want = torch.empty_like(x)
+    z.zero_act8_load(*ck.x, want, format=fmt)
+    last = (model - 1) // 32 * 32
+    assert bool(want[at, last:].isnan().all()) and bool(want[at, :last].isfinite().all())
+    for k in (0, 1):
+        assert torch.equal(d[k][:, :last], want[at, :last].expand(hidden, last))
+        assert bool(d[k][:, last:].isnan().all())

@@ -233,8 +233,20 @@ struct Product {
   int out_cols;            // columns that are written: np, or the pitch, with zeros
 };
 
+struct JoinArgs {
+  const float* partial;
+  int64_t pitch;
+  int splits, nq, np;
+  uint16_t* out;
+  int64_t out_ld;
+};
+
 struct Products {
   Product of[3];
+  int tiles;               // workgroups of tiles; those behind them do the side work
+  int64_t side;            // its pieces, one a thread: of x (kGated: saved, kSlopes: loaded) or of a join (columns of Q)
+  Act8Params x;
+  JoinArgs join;
   int first[3];            // tile number of each; those past the last have 0x7FFFFFFF
   int begin, quarters;     // the first tile of the launch; whether its workgroups take quarters of tiles
   // kGated and kSlopes
@@ -244,7 +256,7 @@ struct Products {
   int64_t h_ld;
   int blocks;              // scales of a row
   int format, act, save;
-  int rows;                // of a workgroup, with a few tokens
+  int rows;                // of a workgroup, with a few tokens (`tiles` workgroups have them)
   int spread;              // rows: whether each tile of P begins at another stage
   int splits, chunk;       // kPartial: parts of the summed index and their length, a multiple of 2 kBk
   float* partial;          // kPartial: [splits][nq][pitch]
@@ -341,6 +353,82 @@ __device__ __forceinline__ uint32_t across_groups(uint32_t top) {
   return top;
 }
 
+// ------------------------------------------------------------------ side work
+// Small streaming work that the products around it do not wait for goes behind the tiles of a
+// launch, where a launch of its own would take 3 to 5 us: x into its checkpoint (beside gate
+// and up), x's values from it (beside dh), dx's parts added up (beside the weights' gradients):
+// 256 x 512 x 1408 forward with its checkpoint 32.5 -> 29.9 us, backward 44 -> 37.
+// Piece k is 8 neighbours of a row.
+constexpr int64_t kSideMost = 1 << 18;   // pieces; more have a launch that fills the card (8192 x 4096: 20 us)
+__host__ __device__ inline int64_t pieces_of(const Act8Params& a) {   // whole blocks of four
+  return a.rows * ((a.cols + ZERO_ACT8_BLOCK - 1) / ZERO_ACT8_BLOCK * 4);
+}
+// 8 values from `at` on, of which n are there; any alignment.
+__device__ __forceinline__ b8 load_piece(const uint16_t* at, int n) {
+  u32x4 w = {};
+  if (n >= 8) {
+    __builtin_memcpy(&w, at, 16);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < n) w[q >> 1] |= static_cast<uint32_t>(at[q]) << ((q & 1) * 16);
+  }
+  return __builtin_bit_cast(b8, w);
+}
+
+__device__ __forceinline__ void save_piece(const Act8Params& a, int k) {
+  const int blocks = static_cast<int>((a.cols + ZERO_ACT8_BLOCK - 1) / ZERO_ACT8_BLOCK), row = k / (blocks * 4);
+  const int piece = k - row * blocks * 4, n = static_cast<int>(a.cols) - piece * 8;
+  const bool there = k < pieces_of(a);
+  b8 w = {};
+  if (there && n > 0) w = load_piece(static_cast<const uint16_t*>(a.values) + row * a.row + piece * 8, n);
+  float v[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) v[q] = static_cast<float>(w[q]);
+  uint32_t top = top_of(v);
+#pragma unroll
+  for (int off = 1; off <= 2; off <<= 1) {
+    const uint32_t m = __shfl_xor(top, off, 64);
+    top = m > top ? m : top;
+  }
+  if (!there) return;
+  const uint32_t byte = act8_scale_byte(top, a.format);
+  uint32_t codes[2];
+  act8_codes(v, act8_inverse(byte), a.format, codes);
+  store_codes8(a.codes + row * a.cols + piece * 8, u32x2{codes[0], codes[1]}, n);
+  if ((piece & 3) == 0) a.scales[static_cast<int64_t>(row) * blocks + piece / 4] = static_cast<uint8_t>(byte);
+}
+__device__ __forceinline__ void read_piece(const Act8Params& a, int k) {
+  const int blocks = static_cast<int>((a.cols + ZERO_ACT8_BLOCK - 1) / ZERO_ACT8_BLOCK), row = k / (blocks * 4);
+  const int piece = k - row * blocks * 4, n = static_cast<int>(a.cols) - piece * 8;
+  if (k >= pieces_of(a) || n <= 0) return;
+  const u32x2 w = load_codes8(a.codes + row * a.cols + piece * 8, n);
+  const float scale = act8_scale(a.scales[static_cast<int64_t>(row) * blocks + piece / 4]);
+  const uint32_t words[2] = {w.x, w.y};
+  float v[8];
+  if (a.format == ZERO_ACT8_INT8)
+    act8_numbers_int8(words, v);
+  else
+    act8_numbers_e4m3(words, v);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) v[q] *= scale;   // exact
+  store8(static_cast<uint16_t*>(a.values) + row * a.row + piece * 8, v, n);
+}
+__device__ __forceinline__ void join_piece(const JoinArgs& a, int64_t k) {
+  const int64_t pieces = a.pitch / 8, n = a.nq * pieces;
+  if (k >= n) return;
+  const int64_t q = k / pieces;
+  const int p = static_cast<int>(k - q * pieces) * 8;
+  f4 lo = {}, hi = {};
+  for (int s = 0; s < a.splits; ++s) {
+    const f4* from = reinterpret_cast<const f4*>(a.partial + (s * static_cast<int64_t>(a.nq) + q) * a.pitch + p);
+    lo += from[0];
+    hi += from[1];
+  }
+  const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  store8(a.out + q * a.out_ld + p, v, a.np - p);
+}
+
 // A tile of BP x BQ results by WP x WQ waves.  ACT: of kGated and kSlopes.  Bound by the matrix
 // units, whose clock falls as they fill.  Measured, 8192 x 4096 x 14336 with tiles of 256 x 256: gate
 // and up, saved, 1345 us (1431 TFLOP/s, matrix units 77% busy), y 653 (1472, 85%), dh 851 (1130, 59%: the
@@ -364,7 +452,19 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
   __shared__ __align__(16) uint16_t qslot2[MORE ? BQ * kBk : 1];
   __shared__ __align__(16) uint16_t qslot3[MORE ? BQ * kBk : 1];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  int id = xcd_order(blockIdx.x, gridDim.x);
+  if constexpr (EPI == kGated || EPI == kSlopes || QCOL) {
+    if (static_cast<int>(blockIdx.x) >= args.tiles) {
+      const int k = (blockIdx.x - args.tiles) * (NW * 64) + threadIdx.x;
+      if constexpr (EPI == kGated)
+        save_piece(args.x, k);
+      else if constexpr (EPI == kSlopes)
+        read_piece(args.x, k);
+      else
+        join_piece(args.join, k);
+      return;
+    }
+  }
+  int id = xcd_order(blockIdx.x, args.tiles);
   const int split = EPI == kPartial ? id % args.splits : 0;
   if constexpr (EPI == kPartial) id /= args.splits;
   // One of the four quarters of a larger tile, or a tile.
@@ -724,27 +824,8 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
 // ------------------------------------------------------------------ parts of a long sum
 // Where a product has fewer tiles than the card has room for, several workgroups share a
 // tile's sum and this adds their parts up, in order.  For 256 rows of 512, a launch's 4.4 us.
-struct JoinArgs {
-  const float* partial;
-  int64_t pitch;
-  int splits, nq, np;
-  uint16_t* out;
-  int64_t out_ld;
-};
 __global__ __launch_bounds__(256) void ffn_join_kernel(JoinArgs a) {
-  const int64_t pieces = a.pitch / 8, n = a.nq * pieces;
-  const int64_t k = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (k >= n) return;
-  const int64_t q = k / pieces;
-  const int p = static_cast<int>(k - q * pieces) * 8;
-  f4 lo = {}, hi = {};
-  for (int s = 0; s < a.splits; ++s) {
-    const f4* from = reinterpret_cast<const f4*>(a.partial + (s * static_cast<int64_t>(a.nq) + q) * a.pitch + p);
-    lo += from[0];
-    hi += from[1];
-  }
-  const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-  store8(a.out + q * a.out_ld + p, v, a.np - p);
+  join_piece(a, static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x);
 }
 
 // ------------------------------------------------------------------ a few tokens
@@ -762,23 +843,16 @@ __global__ __launch_bounds__(256) void ffn_join_kernel(JoinArgs a) {
 constexpr int kFewTokens = 32;
 constexpr int kFewStep = 64;   // summed index of a wave's turn: a cache line of each row
 
-// 8 values from `at` on, of which n are there; any alignment.
-__device__ __forceinline__ b8 load_piece(const uint16_t* at, int n) {
-  u32x4 w = {};
-  if (n >= 8) {
-    __builtin_memcpy(&w, at, 16);
-  } else {
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (q < n) w[q >> 1] |= static_cast<uint32_t>(at[q]) << ((q & 1) * 16);
-  }
-  return __builtin_bit_cast(b8, w);
-}
-
 template <int TB, int NW, int RB, bool GATED>
 __global__ __launch_bounds__(NW * 64) void ffn_few_kernel(Products args) {
   constexpr int M = GATED ? 2 : 1, kParts = M * RB * TB;
   __shared__ f4 part[NW][kParts][64];
+  if constexpr (GATED) {
+    if (static_cast<int>(blockIdx.x) >= args.tiles) {
+      save_piece(args.x, (blockIdx.x - args.tiles) * (NW * 64) + threadIdx.x);
+      return;
+    }
+  }
   const Product& g = args.of[0];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int row0 = blockIdx.x * args.rows, kk = g.kk, nq = g.nq;
@@ -1012,11 +1086,14 @@ int64_t number_tiles(Products& a, int n, int bp, int bq) {
   return total;
 }
 
-// `count` workgroups, from a.begin on.
+// `count` workgroups of tiles, from a.begin on, and the side work's.
 template <int BP, int BQ, int WP, int WQ, int SLOTS, bool PCOL, bool QCOL, Epilogue EPI, int ACT = 0>
-hipError_t launch_tiles(const Products& a, int64_t count, hipStream_t s) {
-  hipLaunchKernelGGL((ffn_product_kernel<BP, BQ, WP, WQ, SLOTS, PCOL, QCOL, EPI, ACT>), dim3(static_cast<unsigned>(count)),
-                     dim3(WP * WQ * 64), 0, s, a);
+hipError_t launch_tiles(Products& a, int64_t count, hipStream_t s) {
+  constexpr int kThreads = WP * WQ * 64;
+  a.tiles = static_cast<int>(count);
+  const int64_t side = (a.side + kThreads - 1) / kThreads;
+  hipLaunchKernelGGL((ffn_product_kernel<BP, BQ, WP, WQ, SLOTS, PCOL, QCOL, EPI, ACT>), dim3(static_cast<unsigned>(count + side)),
+                     dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -1037,6 +1114,7 @@ hipError_t large_tiles(Products a, int n, hipStream_t s) {
   if (e != hipSuccess || !split) return e;
   a.begin = static_cast<int>(total - over);
   a.quarters = 1;
+  a.side = 0;
   return launch_tiles<128, 128, 2, 2, 2, PCOL, QCOL, EPI, ACT>(a, over * 4, s);
 }
 
@@ -1051,12 +1129,13 @@ hipError_t few(Products a, hipStream_t s) {
   const int np = a.of[0].np, each = (np + kCus * kMost - 1) / (kCus * kMost);   // workgroups of a CU
   const int rows = (np + kCus * each - 1) / (kCus * each);
   a.rows = a.save ? kMost : rows < 8 ? 8 : rows;
-  const dim3 grid(static_cast<unsigned>((np + a.rows - 1) / a.rows));
-  constexpr int kWaves = GATED ? 4 : 8;
+  a.tiles = (np + a.rows - 1) / a.rows;
+  const int waves = GATED && a.of[0].nq > 16 ? 4 : 8, threads = waves * 64;
+  const dim3 grid(static_cast<unsigned>(a.tiles + (a.side + threads - 1) / threads));
   if (a.of[0].nq <= 16)
-    hipLaunchKernelGGL((ffn_few_kernel<1, 8, kBlocks, GATED>), grid, dim3(8 * 64), 0, s, a);
+    hipLaunchKernelGGL((ffn_few_kernel<1, 8, kBlocks, GATED>), grid, dim3(threads), 0, s, a);
   else
-    hipLaunchKernelGGL((ffn_few_kernel<2, kWaves, kBlocks, GATED>), grid, dim3(kWaves * 64), 0, s, a);
+    hipLaunchKernelGGL((ffn_few_kernel<2, GATED ? 4 : 8, kBlocks, GATED>), grid, dim3(threads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -1123,8 +1202,9 @@ hipError_t tiles128(const Products& a, int products, int64_t n, hipStream_t s) {
   return tiles<128, 128, 2, 2, 2, PCOL, QCOL, EPI, ACT>(a, products, s);
 }
 
+// later: the launch that can add the parts up beside its own work.
 template <bool PCOL>
-hipError_t product_in_parts(Products a, const Parts& parts, void* room, hipStream_t s) {
+hipError_t product_in_parts(Products a, const Parts& parts, void* room, hipStream_t s, Products* later = nullptr) {
   a.splits = parts.splits;
   a.chunk = parts.chunk;
   a.pitch = parts.pitch;
@@ -1136,6 +1216,11 @@ hipError_t product_in_parts(Products a, const Parts& parts, void* room, hipStrea
   if (e != hipSuccess) return e;
   const JoinArgs j = {a.partial, a.pitch, a.splits, g.nq, g.np, g.out, g.out_ld};
   const int64_t pieces = g.nq * (a.pitch / 8);
+  if (later && pieces <= kSideMost) {
+    later->join = j;
+    later->side = pieces;
+    return hipSuccess;
+  }
   hipLaunchKernelGGL(ffn_join_kernel, dim3(static_cast<unsigned>((pieces + 255) / 256)), dim3(256), 0, s, j);
   return hipGetLastError();
 }
@@ -1220,11 +1305,14 @@ hipError_t launch_ffn_forward(const FfnParams& p, hipStream_t s) {
     down = packing.add(down.at, f, ws.take(d * fp), fp, d, f);
   }
   ZERO_TRY(packing.go(s));
-  if (p.save) {
-    Act8Params a = {const_cast<uint16_t*>(p.x), p.x_row, t, d, p.ckpt.x_codes, p.ckpt.x_scales, p.ckpt.format, 0};
-    ZERO_TRY(launch_act8_save(a, s));
-  }
   Products a = {};
+  if (p.save) {
+    a.x = {const_cast<uint16_t*>(p.x), p.x_row, t, d, p.ckpt.x_codes, p.ckpt.x_scales, p.ckpt.format, 0};
+    if (pieces_of(a.x) <= kSideMost)
+      a.side = pieces_of(a.x);
+    else
+      ZERO_TRY(launch_act8_save(a.x, s));
+  }
   a.gate = {p.ckpt.gate_codes, p.ckpt.gate_scales};
   a.up = {p.ckpt.up_codes, p.ckpt.up_scales};
   a.blocks = static_cast<int>((f + ZERO_ACT8_BLOCK - 1) / ZERO_ACT8_BLOCK);
@@ -1289,12 +1377,13 @@ hipError_t launch_ffn_backward(const FfnParams& p, hipStream_t s) {
     down_cols = static_cast<int>(fp);
   }
   ZERO_TRY(packing.go(s));
-  if (t > 0) {
-    Act8Params held = {x, dp, t, d, p.ckpt.x_codes, p.ckpt.x_scales, p.ckpt.format, 0};
-    ZERO_TRY(launch_act8_load(held, s));
-  }
   // dh, and from it dg, du and h
   Products a = {};
+  a.x = {x, dp, t, d, p.ckpt.x_codes, p.ckpt.x_scales, p.ckpt.format, 0};
+  if (pieces_of(a.x) <= kSideMost)
+    a.side = pieces_of(a.x);
+  else
+    ZERO_TRY(launch_act8_load(a.x, s));
   a.gate = {p.ckpt.gate_codes, p.ckpt.gate_scales};
   a.up = {p.ckpt.up_codes, p.ckpt.up_scales};
   a.blocks = static_cast<int>((f + ZERO_ACT8_BLOCK - 1) / ZERO_ACT8_BLOCK);
@@ -1318,6 +1407,7 @@ hipError_t launch_ffn_backward(const FfnParams& p, hipStream_t s) {
   g.out_ld = 2 * fp;
   g.out_cols = static_cast<int>(fp);
   if (t > 0) ZERO_TRY((activated<true, kSlopes>(a, s)));
+  Products c = {};
   if (p.y && t > 0) {   // dx
     Products b = {};
     Product& y = b.of[0];
@@ -1335,9 +1425,9 @@ hipError_t launch_ffn_backward(const FfnParams& p, hipStream_t s) {
     y.out = p.y;
     y.out_ld = p.y_row;
     y.out_cols = static_cast<int>(d);
-    ZERO_TRY((parts.splits > 1 ? product_in_parts<true>(b, parts, parts_room, s) : product<true, false, kStore>(b, 1, s)));
+    ZERO_TRY((parts.splits > 1 ? product_in_parts<true>(b, parts, parts_room, s, &c) : product<true, false, kStore>(b, 1, s)));
   }
-  Products c = {};   // without tokens: sums of nothing, zeros
+  // the weights' gradients; without tokens sums of nothing, zeros
   for (int k = 0; k < 3; ++k) {
     Product& w = c.of[k];
     const bool last = k == 2;
