@@ -823,7 +823,7 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
 
 // ------------------------------------------------------------------ parts of a long sum
 // Where a product has fewer tiles than the card has room for, several workgroups share a
-// tile's sum and this adds their parts up, in order.  For 256 rows of 512, a launch's 4.4 us.
+// tile's sum and this adds their parts up, in order.  256 rows of 512 alone: 4.4 us, a launch.
 __global__ __launch_bounds__(256) void ffn_join_kernel(JoinArgs a) {
   join_piece(a, static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x);
 }
@@ -1149,7 +1149,7 @@ double time128x256(double stages, int64_t n) { return 5.0 + stages * (0.87 + 0.1
 double time64(double stages, bool columns) { return 3.2 + stages * (columns ? 0.36 : 0.42); }
 
 // How y's and dx's sums (nq rows of np values) are shared out.  Measured, 4096 x 14336 from memory, in
-// parts and in the best whole tiles: 64 rows 34 and 128 us, 256 54 and 123, 512 77 and 121, 1024 (four
+// parts and in the best whole tiles: 64 rows 31 and 121 us, 256 54 and 123, 512 77 and 121, 1024 (four
 // parts of tiles of 256) 108 and 161, 2048 (two) 178 and 231; kk = 2816, 256 rows 18 and 19,
 // 1024 36 and 27 (whole).
 struct Parts {
