@@ -525,7 +525,7 @@ int zero_ffn_workspace(int64_t tokens, int64_t model, int64_t hidden, int flags,
  * Arithmetic: products of BF16 values summed in FP32 on the matrix cores; act in
  * FP32; g and u go into the checkpoint as summed, h is rounded to BF16 (the type the
  * second product takes), y is rounded to BF16.  Results are the same bits on every
- * call with the same inputs.
+ * call with the same inputs, y whether a checkpoint is written or not.
  * tokens = 0 launches nothing.
  * Errors: ZERO_ERR_ARG (NULL, negative sizes, activation, format, overlapping
  * buffers: nothing written may overlap anything else), ZERO_ERR_ALIGN, ZERO_ERR_SIZE

@@ -1,0 +1,51 @@
+"""Feed-forward calls at the edges of what they take: with and without a checkpoint."""
+import math
+
+import pytest
+import torch
+
+import ffn_plain as fp
+
+pytestmark = pytest.mark.gpu
+
+z = pytest.importorskip("zero_sharded_optimizer_reduce_amd")
+
+
+def _normal(gen, *shape, sigma=1.0):
+    return torch.randn(*shape, generator=gen, device="cuda").mul_(sigma).to(torch.bfloat16)
+
+
+def _weights(gen, model, hidden):
+    return [_normal(gen, hidden, model, sigma=1 / math.sqrt(model)), _normal(gen, hidden, model, sigma=1 / math.sqrt(model)),
+            _normal(gen, model, hidden, sigma=1 / math.sqrt(hidden))]
+
+
+def _forward(x, w, act="silu", checkpoint=None, y=None):
+    y = torch.empty(x.shape, dtype=torch.bfloat16, device="cuda") if y is None else y
+    ws = z.zero_ffn_workspace(x.shape[0], x.shape[1], w[0].shape[0])
+    ws.fill_(0xFF)   # NaN everywhere
+    z.zero_ffn_forward(x, *w, y, ws, activation=act, checkpoint=checkpoint)
+    return y
+
+
+def _backward(dy, ck, w, act="silu", dx=None):
+    dx = torch.empty(dy.shape, dtype=torch.bfloat16, device="cuda") if dx is None else dx
+    d = [torch.empty_like(t) for t in w]
+    ws = z.zero_ffn_workspace(dy.shape[0], dy.shape[1], w[0].shape[0], backward=True)
+    ws.fill_(0xFF)
+    z.zero_ffn_backward(dy, ck, *w, dx, *d, ws, activation=act)
+    return [dx, *d]
+
+
+def _bits(a, b):
+    return torch.equal(a.contiguous().view(torch.int16), b.contiguous().view(torch.int16))
+
+
+# ------------------------------------------------------------------ with and without a checkpoint
+@pytest.mark.parametrize("tokens", [1, 7, 16, 17, 32, 33, 200, 700])
+@pytest.mark.parametrize("model,hidden", [(4096, 14336), (1024, 7936), (2048, 11008), (1301, 2999), (512, 1408)])
+def test_a_checkpoint_changes_no_bit_of_y(model, hidden, tokens):
+    gen = torch.Generator(device="cuda").manual_seed(tokens)
+    x, w = _normal(gen, tokens, model), _weights(gen, model, hidden)
+    kept = _forward(x, w, checkpoint=z.FfnCheckpoint.empty(tokens, model, hidden))
+    assert _bits(_forward(x, w), kept)
