@@ -1,4 +1,5 @@
-"""Feed-forward calls at the edges of what they take: with and without a checkpoint."""
+"""Feed-forward calls at the edges of what they take: with and without a checkpoint,
+infinities."""
 import math
 
 import pytest
@@ -49,3 +50,25 @@ def test_a_checkpoint_changes_no_bit_of_y(model, hidden, tokens):
     x, w = _normal(gen, tokens, model), _weights(gen, model, hidden)
     kept = _forward(x, w, checkpoint=z.FfnCheckpoint.empty(tokens, model, hidden))
     assert _bits(_forward(x, w), kept)
+
+
+# ------------------------------------------------------------------ infinities
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu"])
+@pytest.mark.parametrize("tokens", [1, 20, 40, 300, 2100])
+@pytest.mark.parametrize("model,hidden", [(64, 65), (70, 33), (64, 96), (33, 1), (1024, 2111)])
+def test_an_infinity_gives_the_infinite_sum(model, hidden, tokens, act):
+    """Positive weights and +inf in x: g, u, h and y are +inf, whatever fills the rows of the
+    matrices up to the kernels' tiles."""
+    gen = torch.Generator(device="cuda").manual_seed(hidden)
+    x = _normal(gen, tokens, model)
+    w = [torch.rand(s, generator=gen, device="cuda").add_(0.5).div_(model).to(torch.bfloat16)
+         for s in ((hidden, model), (hidden, model), (model, hidden))]
+    want = _forward(x, w, act)
+    at = tokens // 2
+    x[at, model // 3] = math.inf
+    ck = z.FfnCheckpoint.empty(tokens, model, hidden)
+    y = _forward(x, w, act, ck)
+    assert bool((y[at] == math.inf).all())
+    others = torch.arange(tokens, device="cuda") != at
+    assert _bits(y[others], want[others]) and bool(torch.isfinite(y[others].float()).all())
+    assert bool((ck.gate[1][at] == 255).all()) and bool((ck.up[1][at] == 255).all())

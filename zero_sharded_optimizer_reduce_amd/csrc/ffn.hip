@@ -733,6 +733,10 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args
         const int p = first_p + i * 16 + lp;
 #pragma unroll
         for (int n = 0; n < 8; ++n) v[n] = activate<ACT>(a[n]) * b[n];
+        if (p + 8 > np) {   // past the matrices' rows an infinity in x times their zeros is NaN, which would reach y
+#pragma unroll
+          for (int n = 0; n < 8; ++n) v[n] = p + n < np ? v[n] : 0.0f;
+        }
         if (in_q && p < out_cols) store8(out + i * 16, v, 8);   // the workspace's: whole octets
         if (!save) continue;
         // 32 neighbours are one block: the lane's 8 and those of lanes ^ 16, ^ 32, ^ 48
