@@ -504,10 +504,11 @@ typedef struct zero_ffn_checkpoint {
   int32_t format;
 } zero_ffn_checkpoint;
 
-/* Bytes of workspace that zero_ffn_forward, or with ZERO_FFN_BACKWARD
- * zero_ffn_backward, needs.  Weights that are not 16-byte aligned need
- * ZERO_FFN_UNALIGNED (room for aligned copies; sizes that are no multiples of 64
- * have that room anyway).
+/* Bytes of workspace with which zero_ffn_forward, or with ZERO_FFN_BACKWARD
+ * zero_ffn_backward, takes any count of tokens up to `tokens`.  (A call may need more
+ * than one of more tokens: sums of few rows are shared out, with room for the parts.)
+ * Weights that are not 16-byte aligned need ZERO_FFN_UNALIGNED (room for aligned
+ * copies; sizes that are no multiples of 64 have that room anyway).
  * Errors: ZERO_ERR_ARG (NULL, unknown flags, tokens < 0, a side < 1), ZERO_ERR_SIZE
  * (sizes above ZERO_FFN_MAX_TOKENS, ZERO_FFN_MAX_SIDE, or activations that
  * zero_act8_save would refuse). */
@@ -520,8 +521,9 @@ int zero_ffn_workspace(int64_t tokens, int64_t model, int64_t hidden, int flags,
  *                 slices of the gathered view of a layer.
  *   save          host, or NULL: the checkpoint's buffers, written.
  *   workspace     device, 256-byte aligned, workspace_bytes >= zero_ffn_workspace's
- *                 answer; nothing in it carries over between calls.  Calls that may
- *                 run at the same time (streams, captured graphs) need one each.
+ *                 answer for as many tokens or more; nothing in it carries over
+ *                 between calls.  Calls that may run at the same time (streams,
+ *                 captured graphs) need one each.
  * Arithmetic: products of BF16 values summed in FP32 on the matrix cores; act in
  * FP32; g and u go into the checkpoint as summed, h is rounded to BF16 (the type the
  * second product takes), y is rounded to BF16.  Results are the same bits on every

@@ -1,5 +1,5 @@
 """Feed-forward calls at the edges of what they take: with and without a checkpoint,
-infinities."""
+infinities, workspaces of larger batches."""
 import math
 
 import pytest
@@ -72,3 +72,19 @@ def test_an_infinity_gives_the_infinite_sum(model, hidden, tokens, act):
     others = torch.arange(tokens, device="cuda") != at
     assert _bits(y[others], want[others]) and bool(torch.isfinite(y[others].float()).all())
     assert bool((ck.gate[1][at] == 255).all()) and bool((ck.up[1][at] == 255).all())
+
+
+# ------------------------------------------------------------------ a workspace for more tokens
+@pytest.mark.parametrize("model,hidden,most,tokens", [(4096, 14336, 513, 512), (4096, 14336, 2049, 2048), (2048, 8192, 1500, 1024),
+                                                      (1301, 777, 2000, 64)])
+def test_a_workspace_serves_fewer_tokens(model, hidden, most, tokens):
+    gen = torch.Generator(device="cuda").manual_seed(tokens)
+    x, w, dy = _normal(gen, tokens, model), _weights(gen, model, hidden), _normal(gen, tokens, model, sigma=1e-3)
+    rooms = [z.zero_ffn_workspace(most, model, hidden, backward=back) for back in (False, True)]
+    ck = z.FfnCheckpoint.empty(tokens, model, hidden)
+    y, dx, d = torch.empty_like(x), torch.empty_like(x), [torch.empty_like(t) for t in w]
+    z.zero_ffn_forward(x, *w, y, rooms[0], checkpoint=ck)
+    z.zero_ffn_backward(dy, ck, *w, dx, *d, rooms[1])
+    assert _bits(y, _forward(x, w))
+    for a, b in zip((dx, *d), _backward(dy, ck, w)):
+        assert _bits(a, b)

@@ -579,8 +579,8 @@ class FfnCheckpoint:
 
 def zero_ffn_workspace(tokens: int, model: int, hidden: int, backward: bool = False, unaligned: bool = False,
                        device="cuda") -> torch.Tensor:
-    """A device workspace for zero_ffn_forward or, with backward, zero_ffn_backward.
-    unaligned: the weights' addresses are no multiples of 16 bytes."""
+    """A device workspace for zero_ffn_forward or, with backward, zero_ffn_backward of up to
+    `tokens` tokens.  unaligned: the weights' addresses are no multiples of 16 bytes."""
     n = C.c_int64()
     flags = (_lib.ZERO_FFN_BACKWARD if backward else 0) | (_lib.ZERO_FFN_UNALIGNED if unaligned else 0)
     check(load().zero_ffn_workspace(tokens, model, hidden, flags, C.byref(n)), "zero_ffn_workspace")

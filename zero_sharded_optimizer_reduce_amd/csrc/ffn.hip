@@ -1296,6 +1296,18 @@ int64_t ffn_workspace_bytes(int64_t tokens, int64_t model, int64_t hidden, bool 
   return n;
 }
 
+// The room that parts take grows with the rows within 64 of them, and may fall from one 64 to the next;
+// from 256 tiles of 256 x 256 on there is none.  So the most that any count up to `tokens` takes is that
+// of `tokens` itself or of a multiple of 64 with parts.
+int64_t ffn_workspace_room(int64_t tokens, int64_t model, int64_t hidden, bool backward, bool unaligned) {
+  int64_t most = ffn_workspace_bytes(tokens, model, hidden, backward, unaligned);
+  for (int64_t t = 64; t <= tokens && (model + 255) / 256 * ((t + 255) / 256) < 256; t += 64) {
+    const int64_t n = ffn_workspace_bytes(t, model, hidden, backward, unaligned);
+    if (n > most) most = n;
+  }
+  return most;
+}
+
 bool ffn_weights_aligned(const FfnParams& p) {
   return aligned(p.w_gate, p.model) && aligned(p.w_up, p.model) && aligned(p.w_down, p.hidden);
 }

@@ -177,11 +177,13 @@ hipError_t launch_muon_update(const MuonUpdateParams& p, bool vec, hipStream_t s
 int64_t ns_workspace_bytes(int64_t mats, int64_t rows, int64_t cols);
 hipError_t launch_newton_schulz(const NsParams& p, hipStream_t stream);
 
-// Activations to 8 bits and back, and the feed-forward block: the workspace it
-// needs (unaligned: for weights that are not 16-byte aligned) and its launches.
+// Activations to 8 bits and back, and the feed-forward block: the workspace that a call
+// needs (unaligned: for weights that are not 16-byte aligned), the workspace with which any
+// call of so many tokens or fewer can do, and the launches.
 hipError_t launch_act8_save(const Act8Params& p, hipStream_t stream);
 hipError_t launch_act8_load(const Act8Params& p, hipStream_t stream);
 int64_t ffn_workspace_bytes(int64_t tokens, int64_t model, int64_t hidden, bool backward, bool unaligned);
+int64_t ffn_workspace_room(int64_t tokens, int64_t model, int64_t hidden, bool backward, bool unaligned);
 bool ffn_weights_aligned(const FfnParams& p);
 hipError_t launch_ffn_forward(const FfnParams& p, hipStream_t stream);
 hipError_t launch_ffn_backward(const FfnParams& p, hipStream_t stream);

@@ -582,7 +582,7 @@ int zero_ffn_workspace(int64_t tokens, int64_t model, int64_t hidden, int flags,
   if (flags & ~(ZERO_FFN_BACKWARD | ZERO_FFN_UNALIGNED)) return fail(ZERO_ERR_ARG, "ffn: unknown workspace flags");
   int st = check_ffn_shape(tokens, model, hidden, e);
   if (st) return fail(st, e.msg);
-  *bytes_out = ffn_workspace_bytes(tokens, model, hidden, flags & ZERO_FFN_BACKWARD, flags & ZERO_FFN_UNALIGNED);
+  *bytes_out = ffn_workspace_room(tokens, model, hidden, flags & ZERO_FFN_BACKWARD, flags & ZERO_FFN_UNALIGNED);
   return ZERO_OK;
 }
 

@@ -393,13 +393,9 @@ class Zero3FeedForward(Zero3Chain):
         self.workspace = _empty(max(self._workspace_bytes(m, h) for m, h in self.layers), torch.uint8, device)
 
     def _workspace_bytes(self, m: int, h: int) -> int:
-        """Of any call with at most max_tokens tokens: the room for sums in parts grows within 64
-        tokens, may fall from one 64 to the next, and none is taken from 256 x 256 tokens on."""
         unaligned = m * h % 8 != 0   # the view and the contributions start at allocations, the matrices follow
-        most = self.max_tokens
-        counts = {most, *range(64, min(most, 256 * 256) + 1, 64)}
-        return max(zero_ffn_workspace(t, m, h, backward=back, unaligned=unaligned, device="meta").numel()
-                   for t in counts for back in (False, True))
+        return max(zero_ffn_workspace(self.max_tokens, m, h, backward=back, unaligned=unaligned, device="meta").numel()
+                   for back in (False, True))
 
     def _matrices(self, u: int, flat: torch.Tensor):
         m, h = self.layers[u]
