@@ -1,5 +1,5 @@
 """Feed-forward calls at the edges of what they take: with and without a checkpoint,
-infinities, workspaces of larger batches."""
+infinities, workspaces of larger batches, the driver's kept passes."""
 import math
 
 import pytest
@@ -88,3 +88,33 @@ def test_a_workspace_serves_fewer_tokens(model, hidden, most, tokens):
     assert _bits(y, _forward(x, w))
     for a, b in zip((dx, *d), _backward(dy, ck, w)):
         assert _bits(a, b)
+
+
+# ------------------------------------------------------------------ the driver's kept passes
+HP = dict(lr=1e-2, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.1, step=1)
+
+
+@pytest.mark.parametrize("update", ["backward_unit", "backward_unit_fused", "update_unit"])
+def test_an_update_of_a_unit_forgets_its_kept_pass(update):
+    """Whichever of the chain's updates: a kept pass is of the weights before it."""
+    from zero_sharded_optimizer_reduce_amd.drivers import Zero3FeedForward
+
+    st = Zero3FeedForward([(64, 96), (64, 96)], 2, 20)
+    for t in (*st.master, *st.bf16):
+        t.zero_()
+    xs = [torch.ones(20, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    ys = [torch.empty_like(x) for x in xs]
+    w = z.zero_rank_weights([20, 20], 2)
+    for u in (0, 1):
+        st.forward_layer(u, xs, ys)
+    st.contribute(1, xs, [None, None])
+    if update == "update_unit":
+        st.reduce_unit(1, w)
+        st.update_unit(1, HP)
+    else:
+        getattr(st, update)(1, w, HP)
+    with pytest.raises(ValueError, match="other tokens"):
+        st.contribute(1, xs, [None, None])
+    st.contribute(0, xs, [None, None])   # the other unit's is still of its weights
+    st.forward_layer(1, xs, ys)
+    st.contribute(1, xs, [None, None])

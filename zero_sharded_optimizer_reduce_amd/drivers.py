@@ -439,10 +439,18 @@ class Zero3FeedForward(Zero3Chain):
 
     def backward_layer(self, u: int, dys, dxs, weights, hp, stream=None):
         """Layer u's backward pass on every rank, the reduction of its contributions and the
-        owners' updates.  The kept forward pass is of the weights before these: another
-        backward pass needs another forward pass."""
+        owners' updates."""
         self.contribute(u, dys, dxs, stream=stream)
         self.backward_unit(u, weights, hp, stream=stream)
+
+    # A kept forward pass is of the weights before an update: after it, another backward pass
+    # needs another forward pass.
+    def update_unit(self, u: int, hp, stream=None):
+        super().update_unit(u, hp, stream=stream)
+        self.tokens[u] = [None] * self.n
+
+    def backward_unit_fused(self, u: int, weights, hp, stream=None, regather: bool = False):
+        super().backward_unit_fused(u, weights, hp, stream=stream, regather=regather)
         self.tokens[u] = [None] * self.n
 
 
