@@ -517,6 +517,7 @@ int zero_ffn_workspace(int64_t tokens, int64_t model, int64_t hidden, int flags,
 /* Gated feed-forward block, forward:
  *   g = x Wg^T,  u = x Wu^T,  h = act(g) * u,  y = h Wd^T.
  *   x, y          device BF16, element (t, j) at x[t*x_row_stride + j], 2-byte aligned.
+ *                 With one row stride they may be columns of one buffer, side by side.
  *   w_gate, w_up  device BF16 [hidden, model], w_down [model, hidden], contiguous:
  *                 slices of the gathered view of a layer.
  *   save          host, or NULL: the checkpoint's buffers, written.

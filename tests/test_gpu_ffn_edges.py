@@ -1,5 +1,6 @@
 """Feed-forward calls at the edges of what they take: with and without a checkpoint,
-infinities, workspaces of larger batches, the driver's kept passes."""
+infinities, workspaces of larger batches, the driver's kept passes, matrices side by
+side."""
 import math
 
 import pytest
@@ -118,3 +119,41 @@ def test_an_update_of_a_unit_forgets_its_kept_pass(update):
     st.contribute(0, xs, [None, None])   # the other unit's is still of its weights
     st.forward_layer(1, xs, ys)
     st.contribute(1, xs, [None, None])
+
+
+# ------------------------------------------------------------------ matrices side by side
+@pytest.mark.parametrize("tokens,model,hidden,gap", [(1, 64, 96, 0), (20, 64, 96, 0), (40, 64, 128, 0), (200, 70, 96, 3), (300, 256, 320, 8),
+                                                     (1000, 512, 1408, 0), (2100, 1024, 1100, 0)])
+def test_x_and_y_side_by_side_in_one_buffer(tokens, model, hidden, gap):
+    """Columns of one buffer: rows alternate in memory and share no element."""
+    gen = torch.Generator(device="cuda").manual_seed(tokens)
+    w = _weights(gen, model, hidden)
+    for first in (0, 1):   # x before y, and behind it
+        buf = torch.full((tokens, 2 * model + 2 * gap), 3.0, dtype=torch.bfloat16, device="cuda")
+        halves = [buf[:, :model], buf[:, model + gap:2 * model + gap]]
+        a, b = halves[first], halves[1 - first]
+        a.copy_(_normal(gen, tokens, model))
+        x = a.contiguous()
+        ck = z.FfnCheckpoint.empty(tokens, model, hidden)
+        _forward(a, w, checkpoint=ck, y=b)
+        assert _bits(b, _forward(x, w)) and _bits(a, x)
+        _backward_want = _backward(x, ck, w)
+        got = _backward(a, ck, w, dx=b)
+        for p, q in zip(got, _backward_want):
+            assert _bits(p, q)
+        assert _bits(a, x) and bool((buf[:, 2 * model + gap:] == 3).all()) and bool((buf[:, model:model + gap] == 3).all())
+
+
+def test_matrices_that_share_elements_are_refused():
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    w = _weights(gen, 64, 96)
+    buf = torch.zeros(40, 256, dtype=torch.bfloat16, device="cuda")
+    for first in (1, 32, 63):
+        with pytest.raises(z.ZeroError, match="overlap"):
+            _forward(buf[:, :64], w, y=buf[:, first:first + 64])
+        with pytest.raises(z.ZeroError, match="overlap"):
+            _forward(buf[:, first:first + 64], w, y=buf[:, :64])
+    with pytest.raises(z.ZeroError, match="overlap"):   # a row further on
+        _forward(buf[1:, :64], w, y=buf[:39, 33:97])
+    with pytest.raises(z.ZeroError, match="overlap"):   # round the row's end
+        _forward(buf[:39, 200:].as_strided((39, 64), (256, 1)), w, y=buf[:39, :64])

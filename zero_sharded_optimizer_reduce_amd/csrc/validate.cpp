@@ -775,22 +775,37 @@ int check_ffn_shape(int64_t tokens, int64_t model, int64_t hidden, Err& e) {
 }
 
 namespace {
-// Buffers of a call: what it writes may overlap nothing else.
+// Buffers of a call: what it writes may overlap nothing else.  Matrices with one row stride
+// may lie side by side, each in its own columns of a wider buffer.
 struct Buffers {
   static constexpr int kMost = 18;
   Range range[kMost];
   const char* name[kMost];
   bool written[kMost];
+  int64_t step[kMost], width[kMost];   // bytes from row to row and of a row; 0: one piece
   int n = 0;
   void add(const char* what, const void* p, int64_t bytes, bool writes) {
     range[n] = range_of(p, bytes);
     name[n] = what;
+    step[n] = width[n] = 0;
     written[n++] = writes;
+  }
+  void add_rows(const char* what, const void* p, int64_t rows, int64_t cols, int64_t row_stride, bool writes) {
+    add(what, p, matrix_bytes(rows, cols, row_stride, 2), writes);
+    if (rows < 2) return;
+    step[n - 1] = row_stride * 2;
+    width[n - 1] = cols * 2;
+  }
+  bool side_by_side(int i, int j) const {
+    if (step[i] == 0 || step[i] != step[j]) return false;
+    const int64_t apart = static_cast<int64_t>(range[j].lo) - static_cast<int64_t>(range[i].lo);
+    const int64_t column = (apart % step[i] + step[i]) % step[i];   // of i's rows, where j's begin
+    return column >= width[i] && column + width[j] <= step[i];
   }
   int check(Err& e) const {
     for (int i = 0; i < n; ++i)
       for (int j = 0; j < i; ++j)
-        if ((written[i] || written[j]) && overlaps(range[i], range[j]))
+        if ((written[i] || written[j]) && overlaps(range[i], range[j]) && !side_by_side(i, j))
           return set_err(e, ZERO_ERR_ARG, "ffn: %s and %s overlap", name[j], name[i]);
     return ZERO_OK;
   }
@@ -833,11 +848,11 @@ int check_ffn(bool backward, const uint16_t* in, int64_t in_row, int64_t tokens,
   }
   st = check_ffn_matrix(backward ? "dy" : "x", in, tokens, model, in_row, e);
   if (st) return st;
-  b.add(backward ? "dy" : "x", in, matrix_bytes(tokens, model, in_row, 2), false);
+  b.add_rows(backward ? "dy" : "x", in, tokens, model, in_row, false);
   if (out || !backward) {
     st = check_ffn_matrix(backward ? "dx" : "y", out, tokens, model, out_row, e);
     if (st) return st;
-    b.add(backward ? "dx" : "y", out, matrix_bytes(tokens, model, out_row, 2), true);
+    b.add_rows(backward ? "dx" : "y", out, tokens, model, out_row, true);
   }
   if (ckpt && tokens > 0) {
     const int64_t mb = (model + ZERO_ACT8_BLOCK - 1) / ZERO_ACT8_BLOCK, hb = (hidden + ZERO_ACT8_BLOCK - 1) / ZERO_ACT8_BLOCK;
