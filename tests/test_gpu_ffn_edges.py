@@ -1,6 +1,6 @@
 """Feed-forward calls at the edges of what they take: with and without a checkpoint,
 infinities, workspaces of larger batches, the driver's kept passes, matrices side by
-side."""
+side, far rows, weights and gradients that are not finite."""
 import math
 
 import pytest
@@ -157,3 +157,85 @@ def test_matrices_that_share_elements_are_refused():
         _forward(buf[1:, :64], w, y=buf[:39, 33:97])
     with pytest.raises(z.ZeroError, match="overlap"):   # round the row's end
         _forward(buf[:39, 200:].as_strided((39, 64), (256, 1)), w, y=buf[:39, :64])
+
+
+# ------------------------------------------------------------------ far rows
+def test_gradients_with_rows_far_apart():
+    """Row strides with which the last rows of dy and dx lie over 2^32 bytes behind the first."""
+    tokens, model, hidden, stride = 600, 64, 128, 1 << 22
+    gen = torch.Generator().manual_seed(2)
+    w = [fp.signs(gen, hidden, model), fp.signs(gen, hidden, model), fp.signs(gen, model, hidden)]
+    held = [fp.small_checkpoint(gen, tokens, n, 8) for n in (model, hidden, hidden)]
+    ck = z.FfnCheckpoint(*(h[:2] for h in held))
+    bufs = [torch.zeros((tokens - 1) * stride + 2 * model, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    dy, dx = (b.as_strided((tokens, model), (stride, 1)) for b in bufs)
+    dy.copy_(fp.sparse_signs(gen, tokens, model, 8))
+    got = _backward(dy, ck, w, "relu", dx)
+    want = fp.backward64(dy.double(), *(h[2] for h in held), *(t.double() for t in w), "relu")
+    for a, b, name in zip(got, want, ("dx", "d_gate", "d_up", "d_down")):
+        assert torch.equal(a, b.to(torch.bfloat16)), name
+    assert int(bufs[0].count_nonzero()) == int(dy.count_nonzero()) and int(bufs[1].count_nonzero()) == int(dx.count_nonzero())
+
+
+# ------------------------------------------------------------------ weights and gradients that are not finite
+SIZES = [(5, 64, 96), (31, 130, 70), (40, 70, 33), (200, 256, 320), (1000, 512, 1408), (2100, 1024, 2111)]
+
+
+def _clean(tokens, model, hidden):
+    gen = torch.Generator(device="cuda").manual_seed(tokens)
+    x, w, dy = _normal(gen, tokens, model), _weights(gen, model, hidden), _normal(gen, tokens, model, sigma=1e-2)
+    ck = z.FfnCheckpoint.empty(tokens, model, hidden, "e4m3")
+    y = _forward(x, w, checkpoint=ck)
+    return x, w, dy, ck, y, _backward(dy, ck, w)
+
+
+def _but(n, *without):
+    keep = torch.ones(n, dtype=torch.bool, device="cuda")
+    keep[list(without)] = False
+    return keep
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("tokens,model,hidden", SIZES)
+def test_a_weight_that_is_not_finite_reaches_only_its_own_results(tokens, model, hidden, bad):
+    x, w, dy, ck, y, grads = _clean(tokens, model, hidden)
+    for r, c in ((0, 0), (hidden - 1, model - 1)):   # the last one beside what fills the tiles up
+        for k in (0, 1):
+            v = [t.clone() for t in w]
+            v[k][r, c] = bad
+            ck2 = z.FfnCheckpoint.empty(tokens, model, hidden, "e4m3")
+            y2 = _forward(x, v, checkpoint=ck2)
+            if math.isnan(bad):
+                assert bool(y2.isnan().all())
+            held, other, ref, same = ((ck2.gate, ck2.up, ck.gate, ck.up), (ck2.up, ck2.gate, ck.up, ck.gate))[k]
+            assert torch.equal(other[0], same[0]) and torch.equal(other[1], same[1])
+            assert bool((held[1][:, r // 32] == 255).all())
+            keep = _but(held[1].shape[1], r // 32)
+            assert torch.equal(held[1][:, keep], ref[1][:, keep])
+            keep = _but(hidden, *range(r // 32 * 32, min(hidden, r // 32 * 32 + 32)))
+            assert torch.equal(held[0][:, keep], ref[0][:, keep])
+            got = _backward(dy, ck, v)
+            assert not bool(got[0][:, c].isfinite().any()) and _bits(got[0][:, _but(model, c)], grads[0][:, _but(model, c)])
+            assert all(_bits(a, b) for a, b in zip(got[1:], grads[1:]))
+        v = [t.clone() for t in w]
+        v[2][c, r] = bad
+        y2 = _forward(x, v)
+        assert not bool(y2[:, c].isfinite().any()) and _bits(y2[:, _but(model, c)], y[:, _but(model, c)])
+        got = _backward(dy, ck, v)
+        assert not bool(got[0].isfinite().any())   # through dh[:, r], in every sum
+        for k in (1, 2):
+            assert not bool(got[k][r].isfinite().any()) and _bits(got[k][_but(hidden, r)], grads[k][_but(hidden, r)])
+        assert _bits(got[3], grads[3])
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("tokens,model,hidden", SIZES)
+def test_a_gradient_that_is_not_finite_reaches_only_its_own_results(tokens, model, hidden, bad):
+    x, w, dy, ck, y, grads = _clean(tokens, model, hidden)
+    for t, c in ((0, 0), (tokens - 1, model - 1)):
+        dy2 = dy.clone()
+        dy2[t, c] = bad
+        dx, d_gate, d_up, d_down = _backward(dy2, ck, w)
+        assert not bool(dx[t].isfinite().any()) and _bits(dx[_but(tokens, t)], grads[0][_but(tokens, t)])
+        assert not bool(d_gate.isfinite().any()) and not bool(d_up.isfinite().any())   # sums over the token
+        assert not bool(d_down[c].isfinite().any()) and _bits(d_down[_but(model, c)], grads[3][_but(model, c)])
