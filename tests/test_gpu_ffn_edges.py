@@ -1,6 +1,7 @@
 """Feed-forward calls at the edges of what they take: with and without a checkpoint,
 infinities, workspaces of larger batches, the driver's kept passes, matrices side by
-side, far rows, weights and gradients that are not finite."""
+side, far rows, weights and gradients that are not finite, activations far
+out."""
 import math
 
 import pytest
@@ -239,3 +240,45 @@ def test_a_gradient_that_is_not_finite_reaches_only_its_own_results(tokens, mode
         assert not bool(dx[t].isfinite().any()) and _bits(dx[_but(tokens, t)], grads[0][_but(tokens, t)])
         assert not bool(d_gate.isfinite().any()) and not bool(d_up.isfinite().any())   # sums over the token
         assert not bool(d_down[c].isfinite().any()) and _bits(d_down[_but(model, c)], grads[3][_but(model, c)])
+
+
+# ------------------------------------------------------------------ activations far out
+def _act(g, act):
+    """act(g) and its derivative in 64 bits, without the cancellation of 1 + tanh far out."""
+    if act == "relu":
+        return torch.clamp(g, min=0), (g > 0).double()
+    k, c = math.sqrt(2 / math.pi), 0.044715
+    inner, turn = (g, torch.ones_like(g)) if act == "silu" else (2 * k * (g + c * g ** 3), 2 * k * (1 + 3 * c * g * g))
+    s, t = torch.sigmoid(inner), torch.sigmoid(-inner)
+    return g * s, s + torch.where(s * t > 0, g * s * t * turn, torch.zeros_like(g))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu"])
+@pytest.mark.parametrize("tokens", [29, 64])
+def test_activations_and_slopes_far_out(tokens, act, fmt):
+    """x picks one gate value per token, up is 1, down hands h through: y is act(g), and from the
+    checkpoint's g the gradients of gate's and up's first rows are act'(g) and act(g)."""
+    half = [1e-30, 1e-3, 5.0, 8.0, 12.0, 16.0, 17.0, 30.0, 80.0, 88.0, 104.0, 1e4, 1e18, 3e37]
+    big = torch.tensor([0.0, *half, *(-v for v in half)], device="cuda")
+    n = big.numel()
+    x = torch.zeros(tokens, 64, device="cuda")
+    x[:n] = torch.eye(n, 64, device="cuda")
+    wg, wu, wd = (torch.zeros(64, 64, device="cuda") for _ in range(3))
+    wg[0, :n] = big
+    wu[0, :n] = 1.0
+    wd[0, 0] = 1.0
+    x, *w = [t.to(torch.bfloat16) for t in (x, wg, wu, wd)]
+    ck = z.FfnCheckpoint.empty(tokens, 64, 64, fmt)
+    y = _forward(x, w, act, ck)
+    _, d_gate, d_up, _ = _backward(torch.ones_like(x), ck, w, act)
+    held = fp.held_values(*ck.gate, fmt)[:n, 0]
+    assert bool(((held - w[0][0, :n].double()).abs() <= 2.0 ** -4 * held.abs() + 1e-38).all())
+    # One rounding to BF16, and what act is computed with: exponents of size |v| off by 3 |v| steps of FP32, and
+    # below 2^-126 zeros; above 0 sigma and its complement are off by a step of 1, times the slope's g (1 + 3 c g^2)
+    # where they are not the limits (|g| <= 17 for SiLU, 6 for GELU)
+    for got, v, k in ((y[:n, 0], w[0][0, :n].double(), 0), (d_up[0, :n], held, 0), (d_gate[0, :n], held, 1)):
+        want = _act(v, act)[k]
+        off = (got.double() - want).abs()
+        bound = 2.0 ** -8 * 1.02 * want.abs() + torch.where(v > 0, 2.0 ** -16, 1e-36) * (k == 1) + 1e-36
+        assert bool(torch.isfinite(got.float()).all()) and bool((off <= bound).all()), (k, v[off > bound], got[off > bound], want[off > bound])
