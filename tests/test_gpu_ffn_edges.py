@@ -1,7 +1,7 @@
 """Feed-forward calls at the edges of what they take: with and without a checkpoint,
 infinities, workspaces of larger batches, the driver's kept passes, matrices side by
 side, far rows, weights and gradients that are not finite, activations far
-out."""
+out, gradients against differences of the forward pass."""
 import math
 
 import pytest
@@ -282,3 +282,35 @@ def test_activations_and_slopes_far_out(tokens, act, fmt):
         off = (got.double() - want).abs()
         bound = 2.0 ** -8 * 1.02 * want.abs() + torch.where(v > 0, 2.0 ** -16, 1e-36) * (k == 1) + 1e-36
         assert bool(torch.isfinite(got.float()).all()) and bool((off <= bound).all()), (k, v[off > bound], got[off > bound], want[off > bound])
+
+
+# ------------------------------------------------------------------ gradients against differences
+@pytest.mark.parametrize("tokens,model,hidden", [(1, 64, 64), (3, 33, 70), (20, 64, 130), (40, 70, 131), (150, 192, 256)])
+def test_gradients_are_differences_of_the_forward_pass(tokens, model, hidden):
+    """Gates that stay on their side of ReLU's corner and whole numbers that BF16 and the
+    checkpoints hold: y is a polynomial of degree two in each entry, and central differences
+    of the kernels' own y are its derivative, to the last bit."""
+    gen = torch.Generator().manual_seed(tokens)
+    x = torch.zeros(tokens, model)
+    for row in x:   # three entries of +-1: g is an odd multiple of 4, u odd
+        row[torch.randperm(model, generator=gen)[:3]] = torch.randint(0, 2, (3,), generator=gen).float() * 2 - 1
+    x = x.to(torch.bfloat16).cuda()
+    w = [fp.signs(gen, hidden, model) * 4, fp.signs(gen, hidden, model), fp.sparse_signs(gen, model, hidden, 2)]
+    dy = fp.signs(gen, tokens, model)
+    ck = z.FfnCheckpoint.empty(tokens, model, hidden)
+    y = _forward(x, w, "relu", ck)
+    g, u, h, want = fp.forward64(x.double(), *(t.double() for t in w), "relu")
+    assert torch.equal(y.double(), want) and float(h.abs().max()) <= 36
+    assert torch.equal(fp.held_values(*ck.gate, "int8"), g) and torch.equal(fp.held_values(*ck.up, "int8"), u)
+    grads = _backward(dy, ck, w, "relu")
+    for k, (t, grad) in enumerate(zip((x, *w), grads)):
+        flat = grad.double().abs().flatten()
+        some = torch.randint(0, t.numel(), (6,), generator=gen).tolist()
+        for at in {0, t.numel() - 1, int(flat.argmax()), int(flat.gt(0).nonzero()[-1]), *some}:
+            ends = []
+            for step in (1, -1):
+                moved = [v.clone() for v in (x, *w)]
+                moved[k].view(-1)[at] += step
+                ends.append(_forward(moved[0], moved[1:], "relu").double())
+            slope = ((ends[0] - ends[1]) * dy.double()).sum() / 2
+            assert grad.reshape(-1)[at] == slope.to(torch.bfloat16), (k, at)
