@@ -469,7 +469,8 @@ enum { ZERO_ACT8_INT8 = 0, ZERO_ACT8_E4M3 = 1 };
  *   e = the least whole number >= -126 with a <= M * 2^e,
  *   code = round_to_nearest_even(x * 2^-e) in the format,  scale = e + 127.
  * The scaling is exact and no value saturates.  A whole number is off by at most
- * 2^-1 * 2^e <= a / 127, an e4m3 value by at most 2^-4 of itself (or 2^-10 * 2^e).
+ * 2^-1 * 2^e (a / 127 at most, but for blocks at the least e, which may lose all of
+ * a), an e4m3 value by at most 2^-4 of itself (or 2^-10 * 2^e).
  * A block that holds a NaN, an infinity or a magnitude above 127 * 2^121 (e4m3: 448 *
  * 2^119), next to which a code could stand for 2^128, has scale 255 and codes 0.
  *   x             device, BF16 or FP32 (x_dtype), element (i, j) at
