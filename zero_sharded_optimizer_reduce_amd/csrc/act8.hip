@@ -4,9 +4,10 @@
 // Both move data and are bound by HBM: 3.03 bytes a BF16 value.  A lane takes 8
 // neighbours ("unit"): 16 bytes of BF16, 8 bytes of codes; the four lanes of a block
 // find its largest magnitude with two exchanges.
-// 16384 x 14336 BF16: saved in 114 us (6.2 TB/s), read back in 98 (7.3 TB/s).  Two units a lane, on their
-// way together: with one 124 and 122 us, with two 118 and 123, with four 128 and 122, with
-// eight 135 and 126; storing past the caches brings two to 114 and 98.
+// 16384 x 14336 BF16, passes in a row: saved and read back in 230 us, read back alone in 116 (6.1 TB/s).  Two
+// units a lane, on their way together; least times of single launches: with one 124 and 122 us, with
+// two 118 and 123, with four 128 and 122, with eight 135 and 126; storing past the caches brings
+// two to 114 and 94 to 98, of which passes in a row keep the 116 (their median).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

@@ -432,10 +432,11 @@ __device__ __forceinline__ void join_piece(const JoinArgs& a, int64_t k) {
 }
 
 // A tile of BP x BQ results by WP x WQ waves.  ACT: of kGated and kSlopes.  Bound by the matrix
-// units, whose clock falls as they fill.  Measured, 8192 x 4096 x 14336 with tiles of 256 x 256: gate
-// and up, saved, 1345 us (1431 TFLOP/s, matrix units 77% busy), y 653 (1472, 85%), dh 851 (1130, 59%: the
-// epilogue moves 0.95 GB at 4.2 TB/s while they wait, since all CUs come to it together), dx 1248
-// (1542, 81%), the weights' gradients 1919 and 143 for the quarters (1399, 77%).
+// units, whose clock falls as they fill.  Measured, 8192 x 4096 x 14336 with tiles of 256 x 256, medians
+// of 40 passes in a row: gate and up, saved, 1381 us (1393 TFLOP/s, matrix units 77% busy), y 645 (1492,
+// 85%), dh 917 (1050, 59%: the epilogue moves 0.95 GB while they wait, since all CUs come to it
+// together), dx 1289 (1493, 81%), the weights' gradients 1961 and 145 for the quarters (1370, 77%).  On
+// another box 1488, 695, 928, 1292 and 2004.
 template <int BP, int BQ, int WP, int WQ, int SLOTS, bool PCOL, bool QCOL, Epilogue EPI, int ACT>
 __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args) {
   constexpr int NW = WP * WQ;
@@ -842,8 +843,8 @@ __global__ __launch_bounds__(256) void ffn_join_kernel(JoinArgs a) {
 // several times, which costs no memory: so the workgroups get equal shares.  The waves of a workgroup
 // take turns along the summed index and add up at the end, in order, in LDS.
 // Rows and columns of any alignment are read where they lie.
-// Measured: 1 token through 4096 x 14336 40 us for gate and up (5.9 TB/s), 22 for down (5.4); 24 tokens
-// through 4096 x 11008 37 (4.9) and 28 (3.2: the tokens' rows, which every CU takes in from L2, are
+// Measured, medians: 1 token through 4096 x 14336 42 us for gate and up (5.6 TB/s), 21 for down (5.6); 24 tokens
+// through 4096 x 11008 38 (4.8) and 28 (3.2: the tokens' rows, which every CU takes in from L2, are
 // 1.5 times its share of the weights; with the sum in two, and twice the rows, 21 before the
 // parts are added up, which costs as much).
 constexpr int kFewTokens = 32;
@@ -1023,7 +1024,8 @@ __global__ __launch_bounds__(NW * 64) void ffn_few_kernel(Products args) {
 // ------------------------------------------------------------------ operands that the products cannot take
 // A matrix whose rows are not 16-byte aligned, or end inside a stage: copied to the
 // workspace with a pitch of whole stages, zeros behind each row.  Bound by its launch and the
-// unaligned reads: x and the weights of 777 x 1301 x 1999 10 us for 36 MB.
+// unaligned reads: x and the weights of 777 x 1301 x 1999 11 us for 36 MB; of a wide layer by the bytes, three
+// weights read and written on every call (256 tokens of 4096 x 11000 forward 205 us, of 4096 x 11008 105).
 struct PackArgs {
   struct {
     const uint16_t* from;
