@@ -436,7 +436,7 @@ __device__ __forceinline__ void join_piece(const JoinArgs& a, int64_t k) {
 // of 40 passes in a row: gate and up, saved, 1381 us (1393 TFLOP/s, matrix units 77% busy), y 645 (1492,
 // 85%), dh 917 (1050, 59%: the epilogue moves 0.95 GB while they wait, since all CUs come to it
 // together), dx 1289 (1493, 81%), the weights' gradients 1961 and 145 for the quarters (1370, 77%).  On
-// another box 1488, 695, 928, 1292 and 2004.
+// another card 1488, 695, 928, 1292 and 2004.
 template <int BP, int BQ, int WP, int WQ, int SLOTS, bool PCOL, bool QCOL, Epilogue EPI, int ACT>
 __global__ __launch_bounds__(WP * WQ * 64) void ffn_product_kernel(Products args) {
   constexpr int NW = WP * WQ;
